@@ -373,12 +373,196 @@ gdn_status gdn_forward_layers_bf16(const gdn_layer_buffers_bf16 *layers, size_t 
                                    const uint32_t *params, size_t n_params, int with_capture,
                                    size_t state_capture_elems, gdn_stream_t stream);
 
+/*
+ * ======================================================================
+ * The full-attention layers of a hybrid model's serving step.
+ *
+ * Hybrid LLMs put a full-attention layer between their Gated DeltaNet
+ * layers.  The calls below are that layer's part of a step over a paged
+ * key-value cache: gdn_kv_plan assigns pages and slots from the request
+ * lengths, gdn_rope_store rotates q and k and stores k and v, gdn_attn_paged
+ * attends.  All three read the lengths on the device, so a whole step can be
+ * enqueued or graph-captured without a host round trip.  Ownership, streams
+ * and errors are those of the calls above; the params structs are HOST memory
+ * that the call reads before it returns.  The source pages have no counterpart
+ * of these calls.
+ *
+ * The cache.  k_cache and v_cache (same layout, f32 or bf16) hold, for page p,
+ * key head h and position o within the page, head_dim contiguous elements at
+ *     p * cache_page_stride + h * cache_head_stride + o * cache_slot_stride
+ * (strides in elements; [head_dim, page_size, n_kv_heads, n_pages] or
+ * [head_dim, n_kv_heads, page_size, n_pages], innermost first, or a view of a
+ * larger array).  Slot number: p * page_size + o.  Any page_size >= 1.
+ *
+ * Rows of q, k, v and of the outputs: per token, [head_dim, n_heads] contiguous
+ * elements; tokens lie a token stride apart, so views of a fused projection's
+ * output are taken as they are.
+ */
+#define GDN_DTYPE_F32 0u
+#define GDN_DTYPE_BF16 1u
+
+typedef struct gdn_kv_plan_params {
+  uint32_t n_seqs;     /* requests */
+  uint32_t page_size;
+  uint32_t n_pages;    /* pages of the cache */
+  uint32_t max_pages;  /* entries of a block-table row */
+  uint32_t n_free_max; /* entries of free_pages */
+  uint32_t n_slots;    /* entries of slot_map and positions */
+} gdn_kv_plan_params;
+
+/*
+ * gdn_kv_plan -- the bookkeeping of one step, on the device.  All arrays are
+ * DEVICE int32; request s has ctx_lens[s] cached tokens, adds new_lens[s]
+ * (0: an idle slot), and holds the pages block_table[s][0 .. owned[s]).
+ * free_pages[0 .. n_free[0]) is a stack of unused pages, taken from its end.
+ *
+ *   need[s]   = max(owned[s], ceil((ctx_lens[s] + new_lens[s]) / page_size))
+ *   block_table[s][owned[s] .. need[s]) = the next pages of the stack, request
+ *               after request (updated in place; other entries are kept)
+ *   owned_out[s] = need[s];  kv_lens[s] = ctx_lens[s] + new_lens[s]
+ *   n_free_out[0] = n_free[0] - pages taken
+ *   token_start[s] (n_seqs + 1 entries) = new tokens of the requests before s
+ *   positions[i], slot_map[i] of the step's token i (the requests' new tokens,
+ *               packed): its position in its request and its cache slot;
+ *               entries past the step's tokens are 0 and -1
+ *
+ * After a rollback to a shorter ctx_lens the pages beyond stay owned and are
+ * filled again.  A request whose pages the stack cannot give is not served: its
+ * tokens' slots are -1, its kv_lens stays ctx_lens, its table row and owned
+ * stay, and GDN_DEVICE_OUT_OF_PAGES is set; once one was not served, no later
+ * request that needs a page is.  A request with impossible numbers (negative,
+ * more cached tokens than its pages hold, more pages than max_pages) is not
+ * served either (its kv_lens is 0 where the cached part itself is impossible),
+ * and GDN_DEVICE_BAD_REQUEST is set, as it is when the step has more than
+ * n_slots tokens (the first n_slots are written) or n_free is out of range.
+ *
+ * Checks: INVALID_ARGUMENT for NULL or not 4-byte-aligned pointers, zero
+ * n_seqs, page_size, n_pages or max_pages, page counts times page_size at 2^31
+ * or above, and an output that overlaps another array.
+ * One launch; results do not depend on its shape.
+ */
+gdn_status gdn_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *owned,
+                       const int32_t *free_pages, const int32_t *n_free, int32_t *block_table,
+                       int32_t *kv_lens, int32_t *owned_out, int32_t *n_free_out,
+                       int32_t *token_start, int32_t *slot_map, int32_t *positions,
+                       const gdn_kv_plan_params *params, gdn_stream_t stream);
+
+#define GDN_ROPE_INTERLEAVED 0x1u /* pairs (2j, 2j+1) instead of (j, j + rot_dim/2) */
+#define GDN_ROPE_INVERSE 0x2u     /* the inverse rotation, which is the gradient's */
+#define GDN_ROPE_MAX_DIM 256u     /* largest head_dim */
+
+typedef struct gdn_rope_params {
+  uint32_t dtype; /* of q, k, v, outputs and caches */
+  uint32_t head_dim, rot_dim; /* the first rot_dim elements of a head are rotated, the rest copied */
+  uint32_t n_q_heads, n_kv_heads, n_tokens;
+  uint32_t n_axes, n_positions; /* rows of `positions`; rows of cos_sin */
+  uint32_t flags;
+  uint32_t page_size, n_pages; /* gdn_rope_store only, as the cache strides */
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride; /* token strides */
+  int64_t positions_stride; /* elements between axes; 0: every axis reads the same row */
+  int64_t cache_page_stride, cache_head_stride, cache_slot_stride;
+  uint8_t axis_of_pair[GDN_ROPE_MAX_DIM / 2]; /* the axis of each of the rot_dim/2 pairs */
+} gdn_rope_params;
+
+/*
+ * gdn_rope -- rotary positions with one or more axes (time; time, height,
+ * width; ...).  Pair j of every q and k head, at the token's position
+ * p = positions[axis_of_pair[j]][token]:
+ *     (a, b) -> (a c - b s, b c + a s),   c = cos_sin[p][j], s = cos_sin[p][rot_dim/2 + j]
+ * cos_sin: DEVICE f32 [rot_dim, n_positions], innermost first.  Computed in
+ * f32 and rounded once when stored.  q_out and k_out may be q and k (in place).
+ * The gradients of q and k are the same call on the outputs' gradients with
+ * GDN_ROPE_INVERSE.
+ *
+ * gdn_rope_store -- gdn_rope whose k goes to the cache, with v beside it: token
+ * i's rows are stored at slot_map[i] (-1: nowhere; DEVICE int32).  Two tokens
+ * of a call must not share a slot.
+ *
+ * A position outside [0, n_positions) makes the token's rotated elements NaN
+ * and sets GDN_DEVICE_BAD_POSITION; a slot past the cache stores nothing and
+ * sets GDN_DEVICE_BAD_PAGE.
+ *
+ * Checks: INVALID_ARGUMENT for NULL pointers, zero sizes (n_tokens may be 0:
+ * nothing is done), head_dim odd, 0 or above GDN_ROPE_MAX_DIM, rot_dim odd or
+ * outside (0, head_dim], an axis_of_pair entry >= n_axes, unknown flags or
+ * dtype, pointers not aligned to an element, token strides below a row's
+ * length, an output that overlaps another buffer (other than exactly its own
+ * input); UNSUPPORTED for GDN_ROPE_INVERSE with gdn_rope_store.  Any alignment
+ * and strides are taken; 16-byte aligned rows go 16 bytes at a time.
+ */
+gdn_status gdn_rope(const void *q, const void *k, const int32_t *positions, const float *cos_sin,
+                    void *q_out, void *k_out, const gdn_rope_params *params, gdn_stream_t stream);
+
+gdn_status gdn_rope_store(const void *q, const void *k, const void *v, const int32_t *positions,
+                          const float *cos_sin, const int32_t *slot_map, void *q_out, void *k_cache,
+                          void *v_cache, const gdn_rope_params *params, gdn_stream_t stream);
+
+typedef struct gdn_attn_params {
+  uint32_t dtype; /* of q, the caches and the output */
+  uint32_t head_dim; /* 64, 128 or 256 */
+  uint32_t n_q_heads, n_kv_heads;
+  uint32_t n_seqs, n_tokens; /* requests; rows of q */
+  uint32_t page_size, n_pages, max_pages;
+  uint32_t window; /* > 0: a token sees its last `window` keys only */
+  float scale;     /* of the scores, e.g. 1/sqrt(head_dim) */
+  int64_t q_stride, out_stride; /* token strides */
+  int64_t cache_page_stride, cache_head_stride, cache_slot_stride;
+} gdn_attn_params;
+
+/*
+ * gdn_attn_paged -- attention of each request's newest tokens over its cached
+ * keys and values.  Request s has kv_lens[s] keys, the step's among them, in
+ * the pages of block_table row s (max_pages entries), and the q rows
+ * token_start[s] .. token_start[s + 1] (NULL: row s).  Its row t of T sees
+ * keys j <= kv_lens[s] - T + t, and of those the last `window` if window > 0:
+ *     output = sum_j p_j v_j,   p = softmax over the seen j of scale * q.k_j
+ * per query head h, with key head h / (n_q_heads / n_kv_heads).  A row that
+ * sees no key is zero.  Cache contents that a row does not see do not reach it,
+ * NaN and infinities included; infinities that it does see give NaN or
+ * infinities.  One token per request (decode) or a window of a few
+ * (verification of drafted tokens) is what it is built for; longer windows are
+ * right but read the keys once per 16 rows.
+ *
+ * Everything is accumulated in f32, with operands split so that products are
+ * good to f32 (bf16 inputs are exact), and rounded once.  Results do not vary
+ * from run to run.
+ *
+ * workspace: DEVICE, at least gdn_attn_workspace_size bytes, 16-byte aligned,
+ * contents irrelevant before and unspecified after; concurrent calls need one
+ * each.  The size depends on dtype, head_dim, heads, n_seqs and n_tokens only,
+ * and not on the lengths.
+ *
+ * A table entry outside [0, n_pages) for a key that is read makes the rows of
+ * that request's key head NaN and sets GDN_DEVICE_BAD_PAGE; a length outside
+ * [0, max_pages * page_size] or a token_start that does not ascend within
+ * [0, n_tokens] is clipped and sets GDN_DEVICE_BAD_REQUEST.
+ *
+ * Checks: INVALID_ARGUMENT for NULL pointers, zero sizes (n_tokens may be 0),
+ * n_q_heads % n_kv_heads != 0, unknown dtype, a scale that is not finite, caches
+ * not 16-byte aligned or their strides not multiples of 16 bytes, bf16 q not
+ * 4-byte aligned or with an odd stride, other pointers not aligned to an
+ * element, token strides below a row's length, page counts times page_size at
+ * 2^31 - 2^16 or above, n_tokens < n_seqs without token_start, output
+ * overlapping any other buffer, the workspace rules; UNSUPPORTED for a head_dim
+ * other than 64, 128, 256.
+ */
+gdn_status gdn_attn_workspace_size(const gdn_attn_params *params, size_t *bytes);
+
+gdn_status gdn_attn_paged(const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *kv_lens,
+                          const int32_t *token_start, void *output, const gdn_attn_params *params,
+                          void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the thread's next call. */
 const char *gdn_last_error(void);
 
 /* Bits of the device status word. */
 #define GDN_DEVICE_WAIT_TIMEOUT 0x1u /* a chunked kernel's bounded wait ran out */
+#define GDN_DEVICE_OUT_OF_PAGES 0x2u /* gdn_kv_plan: the free stack could not serve a request */
+#define GDN_DEVICE_BAD_REQUEST 0x4u  /* gdn_kv_plan, gdn_attn_paged: impossible lengths or offsets */
+#define GDN_DEVICE_BAD_PAGE 0x8u     /* a page number or slot outside the cache */
+#define GDN_DEVICE_BAD_POSITION 0x10u /* gdn_rope*: a position outside the cos/sin table */
 
 /*
  * gdn_device_status -- the library's device-side failure channel (see

@@ -37,6 +37,32 @@ class LayerBuffers(ctypes.Structure):
                                                 "state_out", "state_capture")]
 
 
+_U32, _I64 = ctypes.c_uint32, ctypes.c_int64
+
+
+class KvPlanParams(ctypes.Structure):
+    """Mirror of gdn_kv_plan_params (include/gdn.h)."""
+    _fields_ = [(n, _U32) for n in ("n_seqs", "page_size", "n_pages", "max_pages", "n_free_max", "n_slots")]
+
+
+class RopeParams(ctypes.Structure):
+    """Mirror of gdn_rope_params (include/gdn.h)."""
+    _fields_ = [(n, _U32) for n in ("dtype", "head_dim", "rot_dim", "n_q_heads", "n_kv_heads", "n_tokens",
+                                    "n_axes", "n_positions", "flags", "page_size", "n_pages")] + \
+        [(n, _I64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride",
+                             "positions_stride", "cache_page_stride", "cache_head_stride",
+                             "cache_slot_stride")] + [("axis_of_pair", ctypes.c_uint8 * 128)]
+
+
+class AttnParams(ctypes.Structure):
+    """Mirror of gdn_attn_params (include/gdn.h)."""
+    _fields_ = [(n, _U32) for n in ("dtype", "head_dim", "n_q_heads", "n_kv_heads", "n_seqs", "n_tokens",
+                                    "page_size", "n_pages", "max_pages", "window")] + \
+        [("scale", ctypes.c_float)] + \
+        [(n, _I64) for n in ("q_stride", "out_stride", "cache_page_stride", "cache_head_stride",
+                             "cache_slot_stride")]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -84,6 +110,16 @@ def lib() -> ctypes.CDLL:
             L.gdn_forward_chunked_noalloc.restype = ctypes.c_int
             L.gdn_device_status.argtypes = [u32p, ctypes.c_int, vp]
             L.gdn_device_status.restype = ctypes.c_int
+            L.gdn_kv_plan.argtypes = [vp] * 12 + [ctypes.POINTER(KvPlanParams), vp]
+            L.gdn_kv_plan.restype = ctypes.c_int
+            L.gdn_rope.argtypes = [vp] * 6 + [ctypes.POINTER(RopeParams), vp]
+            L.gdn_rope.restype = ctypes.c_int
+            L.gdn_rope_store.argtypes = [vp] * 9 + [ctypes.POINTER(RopeParams), vp]
+            L.gdn_rope_store.restype = ctypes.c_int
+            L.gdn_attn_workspace_size.argtypes = [ctypes.POINTER(AttnParams), ctypes.POINTER(sz)]
+            L.gdn_attn_workspace_size.restype = ctypes.c_int
+            L.gdn_attn_paged.argtypes = [vp] * 7 + [ctypes.POINTER(AttnParams), vp, sz, vp]
+            L.gdn_attn_paged.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -115,6 +151,10 @@ def gdn_path_name(params, capture: bool = False) -> str:
 
 
 GDN_DEVICE_WAIT_TIMEOUT = 0x1
+GDN_DEVICE_OUT_OF_PAGES = 0x2
+GDN_DEVICE_BAD_REQUEST = 0x4
+GDN_DEVICE_BAD_PAGE = 0x8
+GDN_DEVICE_BAD_POSITION = 0x10
 
 
 def gdn_device_status(reset: bool = False, stream=0) -> int:

@@ -9,9 +9,11 @@
 #include <cstring>
 
 #include "../../include/gdn.h"
+#include "abi_common.h"
 #include "gdn_internal.h"
+#include "paged_internal.h"
 
-namespace {
+namespace gdn {
 
 thread_local char g_last_error[512] = "";
 
@@ -22,6 +24,16 @@ gdn_status fail(gdn_status st, const char *fmt, ...) {
   va_end(ap);
   return st;
 }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::aligned;
+using gdn::fail;
+using gdn::g_last_error;
+using gdn::overlap;
+using gdn::Span;
 
 // Largest n_tokens that runs on the decode launch shape under GDN_PATH_AUTO.
 constexpr uint32_t kDecodeMaxTokens = 16;
@@ -49,19 +61,6 @@ bool mul_ok(unsigned long long a, unsigned long long b, unsigned long long *out)
   *out = static_cast<unsigned long long>(r);
   return true;
 }
-
-struct Span {
-  const void *p;
-  unsigned long long bytes;
-  const char *name;
-};
-
-bool overlap(const Span &a, const Span &b) {
-  const auto a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 struct Decoded {
   gdn::Problem prob;
@@ -558,9 +557,11 @@ gdn_status gdn_device_status(uint32_t *status, int reset, gdn_stream_t stream) {
   unsigned int one = 0, two = 0;
   cudaError_t err = gdn::chunked_wait_status(&one, reset != 0, cs);
   if (err == cudaSuccess) err = gdn::chunked_split_wait_status(&two, reset != 0, cs);
+  unsigned int paged = 0;
+  if (err == cudaSuccess) err = gdn::paged_status(&paged, reset != 0, cs);
   if (err != cudaSuccess)
     return fail(GDN_ERR_CUDA, "gdn: reading the device status failed: %s", cudaGetErrorString(err));
-  *status = one | two;
+  *status = one | two | paged;
   return GDN_OK;
 }
 
