@@ -56,6 +56,7 @@ constexpr int kSms = 152;
 constexpr int kJoinWarps = 4;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;  // the lowest finite f32
 
 // ------------------------------------------------------------ matrix instructions
 
@@ -120,12 +121,13 @@ struct Call {
   float scale_log2;
   int64_t q_stride, out_stride, page_stride, head_stride, slot_stride;
   FastDiv page_div, group_div;
+  bool whole_tiles;  // pages hold whole 16-key tiles
 };
 
 // A request's share of the work.
 struct Request {
   int t0, tokens;   // its rows of q
-  int len, lo;      // its keys: [lo, len) are seen by at least one token
+  int len, lo;      // its keys: those that at least one token sees lie in [lo, len)
   int blocks;       // row blocks per key head
   int tiles;        // units per (key head, row block); 1 when there is no key
   bool bad;
@@ -159,7 +161,7 @@ __device__ __forceinline__ Request request(const Call &c, uint32_t s) {
   }
   r.len = len;
   const long long lo = c.window ? static_cast<long long>(len) - r.tokens + 1 - c.window : 0;
-  r.lo = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0);
+  r.lo = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0) / kTile * kTile;  // tiles begin at multiples of 16
   const long long rows = static_cast<long long>(r.tokens) * c.group;
   r.blocks = static_cast<int>((rows + ROWS - 1) / ROWS);
   const int tiles = (len - r.lo + kUnit - 1) / kUnit;
@@ -177,32 +179,52 @@ __device__ __forceinline__ long long share_start(long long total, int ctas, int 
 template <typename T, int D>
 struct Shape {
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
-  static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks per row
+  static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
   static constexpr int kHalf = kTile * kRowBytes;  // bytes of a half tile
-  // half tiles in a warp's ring: about 24 KB, so that two CTAs share an SM; at least 3
-  static constexpr int kRing = kHalf <= 2048 ? 8 : kHalf == 4096 ? 6 : 3;
-  static constexpr int kSteps = kChunks / 2;  // matrix steps over D (32 bytes each)
+  // half tiles in a warp's ring
+  static constexpr int kRing = kHalf == 2048 ? 8 : kHalf == 4096 ? 5 : kHalf == 8192 ? 6 : 3;
+  static constexpr int kCtas = kHalf == 2048 ? 3 : kHalf == 4096 ? 2 : 1;  // CTAs an SM holds
+  static constexpr int kSteps = kChunks / 2;       // matrix steps over D (32 bytes each)
+  // the join of a CTA's warps goes through shared memory in pieces of 8 rows x kJoinCols
+  static constexpr int kJoinCols = D < 128 ? D : 128;
+  static constexpr int kJoinRow = kJoinCols + 4;  // padded: a fragment's rows fall on different banks
+  static constexpr int kJoinBytes = kWarps * 8 * kJoinRow * 4;
 };
 
-// Byte offset of 16-byte chunk `c` of row `r` in a half tile.  Chunks of eight
-// consecutive rows at one c fall on eight different bank groups (ldmatrix);
-// for f32 the order also keeps chunk pairs of four consecutive rows apart
-// (the transposed 4-byte reads of V).
+// A half tile in shared memory: row r's chunk c lies at r * kRowBytes +
+// ((c ^ order(r)) << 4).  order permutes the three low bits, so that one chunk
+// of eight consecutive rows falls on eight different bank groups (ldmatrix);
+// for f32 it also keeps two neighbouring chunks of four consecutive rows apart
+// (the transposed 4-byte reads of V).  order(x ^ y) = order(x) ^ order(y): a
+// lane's offset for a step is its offset for step 0 with a constant XORed in.
+template <typename T>
+__device__ __host__ constexpr int order(int r) {
+  return sizeof(T) == 4 ? ((r & 3) << 1 | (r >> 2 & 1)) : (r & 7);
+}
 template <typename T, int D>
-__device__ __forceinline__ int swizzled(int r, int c) {
-  const int f = sizeof(T) == 4 ? ((r & 3) << 1 | (r >> 2 & 1)) : (r & 7);
-  return r * Shape<T, D>::kRowBytes + ((c ^ f) << 4);
+__device__ __forceinline__ constexpr int swizzled(int r, int c) {
+  return r * Shape<T, D>::kRowBytes + ((c ^ order<T>(r)) << 4);
 }
 
 template <typename T, int D, int NT>
 struct Warp;
 
-// bf16: K fragments by ldmatrix, q fragments in registers.
+// bf16: K and V fragments by ldmatrix, q fragments in registers.
 template <int D, int NT>
 struct Warp<__nv_bfloat16, D, NT> {
   using S = Shape<__nv_bfloat16, D>;
   static constexpr int kQSmem = 0;
   unsigned q[S::kSteps][NT][2];
+  unsigned k_at[4], v_at[4];  // this lane's offsets in a half tile for steps 0-3; step + 4: 128 bytes on
+
+  __device__ __forceinline__ explicit Warp(int lane) {
+    const int rk = (lane & 7) + (lane >> 3 & 1) * 8, rv = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k_at[i] = swizzled<__nv_bfloat16, D>(rk, i * 2 + (lane >> 4));
+      v_at[i] = swizzled<__nv_bfloat16, D>(rv, i * 2 + (lane >> 3 & 1));
+    }
+  }
 
   // row(n): q's row of column n of this warp's tile, or nullptr
   template <typename F>
@@ -219,15 +241,24 @@ struct Warp<__nv_bfloat16, D, NT> {
     }
   }
 
-  __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile, const void *, int lane) const {
-    const int r = (lane & 7) + (lane >> 3 & 1) * 8;
+  // s = K Q^T of the tile's 16 keys; two chains of products, for their latency
+  __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile, const void *) const {
+    float t[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][j] = t[nt][j] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < S::kSteps; ++ks) {
       unsigned a[4];
-      ldmatrix_x4(a, k_tile + swizzled<__nv_bfloat16, D>(r, ks * 2 + (lane >> 4)));
+      ldmatrix_x4(a, k_tile + k_at[ks & 3] + (ks >> 2) * 128);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_bf16(s[nt], a, q[ks][nt][0], q[ks][nt][1]);
+      for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? t[nt] : s[nt], a, q[ks][nt][0], q[ks][nt][1]);
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j];
   }
 
   // The B fragments of P^T from the score tile's layout: hi and lo halves.
@@ -247,13 +278,13 @@ struct Warp<__nv_bfloat16, D, NT> {
     }
   };
 
-  // V^T fragment of 16 elements of D over the tile's 16 keys; keys outside [k0, k1) as zeros
+  // V^T fragment of 16 elements of D over the tile's 16 keys
   struct V {
     unsigned a[4];
-    __device__ __forceinline__ V(unsigned v_tile, int md, int lane) {
-      const int r = (lane & 7) + (lane >> 4) * 8;
-      ldmatrix_x4_trans(a, v_tile + swizzled<__nv_bfloat16, D>(r, md * 2 + (lane >> 3 & 1)));
+    __device__ __forceinline__ V(const Warp &w, unsigned v_tile, int md) {
+      ldmatrix_x4_trans(a, v_tile + w.v_at[md & 3] + (md >> 2) * 128);
     }
+    // keys outside [k0, k1) as zeros
     __device__ __forceinline__ void keep(int k0, int k1, int lane) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -263,6 +294,7 @@ struct Warp<__nv_bfloat16, D, NT> {
         a[h * 2 + 1] &= m;
       }
     }
+    // c += V^T P^T
     __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
       mma_bf16(c, a, p.hi[nt][0], p.hi[nt][1]);
       mma_bf16(c, a, p.lo[nt][0], p.lo[nt][1]);
@@ -270,42 +302,72 @@ struct Warp<__nv_bfloat16, D, NT> {
   };
 };
 
-// f32: three TF32 products of split operands; q in shared memory.
+// f32: three TF32 products of split operands; q's halves in shared memory.
+// The tensor cores cut the low bits of a running sum at every product, so the
+// long sums are taken outside them: a product's sum starts at zero, over 32
+// elements of D (scores) or the tile's 16 keys (output), and is added in f32.
 template <int D, int NT>
 struct Warp<float, D, NT> {
   using S = Shape<float, D>;
-  static constexpr int kQRow = D + 4;
+  static constexpr int kQRow = 2 * D + 8;  // (hi, lo) pairs, padded
   static constexpr int kQSmem = NT * 8 * kQRow * 4;
+  unsigned k_at[4], v_at[8], q_at;
+
+  __device__ __forceinline__ explicit Warp(int lane) {
+    const int rk = (lane & 7) + (lane >> 3 & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k_at[i] = swizzled<float, D>(rk, i * 2 + (lane >> 4));
+    // key (i & 1) * 4 + lane % 4, element (i >> 1) * 8 + lane / 4
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v_at[i] = swizzled<float, D>((i & 1) * 4 + (lane & 3), (i >> 1) * 2 + (lane >> 4)) + (lane >> 2 & 3) * 4;
+    q_at = (lane / 4) * kQRow + (lane & 3) * 2;
+  }
 
   template <typename F>
   __device__ __forceinline__ void load_q(F row, void *q_smem, int) {
-    float *qs = static_cast<float *>(q_smem);
+    uint2 *qs = static_cast<uint2 *>(q_smem);
     for (int i = threadIdx.x; i < NT * 8 * D; i += kThreads) {
       const float *p = row(i / D);
-      qs[i / D * kQRow + i % D] = p ? p[i % D] : 0.0f;
+      const Tf32Pair x(p ? p[i % D] : 0.0f);
+      qs[i / D * (kQRow / 2) + i % D] = make_uint2(x.hi, x.lo);
     }
   }
 
-  __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile, const void *q_smem, int lane) const {
-    const float *qs = static_cast<const float *>(q_smem) + (lane / 4) * kQRow + (lane & 3);
-    const int r = (lane & 7) + (lane >> 3 & 1) * 8;
-#pragma unroll 4
-    for (int ks = 0; ks < S::kSteps; ++ks) {
-      unsigned a[4], hi[4], lo[4];
-      ldmatrix_x4(a, k_tile + swizzled<float, D>(r, ks * 2 + (lane >> 4)));
+  __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile, const void *q_smem) const {
+    const unsigned *qs = static_cast<const unsigned *>(q_smem) + q_at;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll(S::kSteps / 4 > 2 ? 2 : S::kSteps / 4)
+    for (int k4 = 0; k4 < S::kSteps / 4; ++k4) {
+      float t[NT][4], e[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[nt][j] = e[nt][j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Tf32Pair x(__uint_as_float(a[i]));
-        hi[i] = x.hi;
-        lo[i] = x.lo;
+        unsigned a[4], lo[4];
+        ldmatrix_x4(a, k_tile + k_at[i] + k4 * 128);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const Tf32Pair x(__uint_as_float(a[j]));
+          a[j] = x.hi;
+          lo[j] = x.lo;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 b0 = *reinterpret_cast<const uint2 *>(qs + nt * 8 * kQRow + (k4 * 4 + i) * 16);
+          const uint2 b1 = *reinterpret_cast<const uint2 *>(qs + nt * 8 * kQRow + (k4 * 4 + i) * 16 + 8);
+          mma_tf32(t[nt], a, b0.x, b1.x);
+          mma_tf32(e[nt], lo, b0.x, b1.x);
+          mma_tf32(e[nt], a, b0.y, b1.y);
+        }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const Tf32Pair b0(qs[nt * 8 * kQRow + ks * 8]), b1(qs[nt * 8 * kQRow + ks * 8 + 4]);
-        mma_tf32(s[nt], lo, b0.hi, b1.hi);
-        mma_tf32(s[nt], hi, b0.lo, b1.lo);
-        mma_tf32(s[nt], hi, b0.hi, b1.hi);
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j] + e[nt][j];
     }
   }
 
@@ -330,15 +392,16 @@ struct Warp<float, D, NT> {
 
   struct V {
     unsigned hi[2][4], lo[2][4];  // two steps of 8 keys
-    __device__ __forceinline__ V(unsigned v_tile, int md, int lane) {
+    __device__ __forceinline__ V(const Warp &w, unsigned v_tile, int md) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = h * 8 + (i >> 1) * 4 + (lane & 3), d = md * 16 + (i & 1) * 8 + lane / 4;
+          // register i: key (i >> 1) * 4 + lane % 4 of the step, element (i & 1) * 8 + lane / 4 of the 16
           float x;
           asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x)
-                       : "r"(v_tile + swizzled<float, D>(key, d >> 2) + (d & 3) * 4) : "memory");
+                       : "r"(v_tile + w.v_at[(md & 1) * 4 + (i & 1) * 2 + (i >> 1)] + (md >> 1) * 128 + h * 8 * S::kRowBytes)
+                       : "memory");
           const Tf32Pair t(x);
           hi[h][i] = t.hi;
           lo[h][i] = t.lo;
@@ -354,41 +417,83 @@ struct Warp<float, D, NT> {
         }
     }
     __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
+      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mma_tf32(c, lo[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
-        mma_tf32(c, hi[h], p.lo[nt][2 * h], p.lo[nt][2 * h + 1]);
-        mma_tf32(c, hi[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
+        mma_tf32(y, lo[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
+        mma_tf32(y, hi[h], p.lo[nt][2 * h], p.lo[nt][2 * h + 1]);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) mma_tf32(y, hi[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] += y[j];
     }
   };
 };
 
 template <typename T, int D, int NT>
 constexpr int smem_bytes() {
-  return kWarps * Shape<T, D>::kRing * Shape<T, D>::kHalf + Warp<T, D, NT>::kQSmem;
+  using S = Shape<T, D>;
+  return kWarps * S::kRing * S::kHalf + S::kJoinBytes + Warp<T, D, NT>::kQSmem;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------ the main kernel
 
+// One (request, key head, row block) item of a CTA's share, or the part of it
+// that lies in the share.
+template <int ROWS>
+struct Item {
+  uint32_t seq;
+  Request r;
+  long long in_seq;      // units of the request before the item's part
+  int item;              // head * r.blocks + block
+  int tile0, tile1;      // its units
+  int k0, k1;            // its keys
+
+  // Whether [u, u1) begins with an item; the request at or after `seq` that holds unit in_seq.
+  __device__ __forceinline__ bool find(const Call &c, long long u, long long u1) {
+    if (u >= u1) return false;
+    while (in_seq >= r.units(c)) {
+      in_seq = 0;
+      if (++seq >= c.n_seqs) return false;
+      r = request<ROWS>(c, seq);
+    }
+    item = static_cast<int>(in_seq / r.tiles);
+    tile0 = static_cast<int>(in_seq - static_cast<long long>(item) * r.tiles);
+    tile1 = static_cast<int>(min(static_cast<long long>(r.tiles), tile0 + (u1 - u)));
+    k0 = r.lo + tile0 * kUnit;
+    k1 = min(r.len, r.lo + tile1 * kUnit);
+    return true;
+  }
+  // Tiles of 16 keys of this part that `warp` takes: k0 + 16 (warp + 4 i).
+  __device__ __forceinline__ int tiles_of(int warp) const {
+    const int first = k0 + kTile * warp;
+    return first < k1 ? (k1 - first + kUnit - 1) / kUnit : 0;
+  }
+};
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
+__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
   using S = Shape<T, D>;
   using W = Warp<T, D, NT>;
   constexpr int kRows = NT * 8;
-  constexpr int kJoinRow = D + 4;  // padded row of the join area
-  static_assert(kWarps * kRows * kJoinRow * 4 <= kWarps * S::kRing * S::kHalf, "the join area lies in the rings");
+  static_assert(smem_bytes<T, D, NT>() <= 226 * 1024 / S::kCtas, "the CTAs of an SM share its memory");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kWarps], s_total, s_offset;
+  __shared__ long long s_scan[kWarps], s_offset;
   __shared__ uint32_t s_seq;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_bad[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned char *ring = smem + warp * S::kRing * S::kHalf;
-  const unsigned ring_at = smem_u32(ring);
-  float *join = reinterpret_cast<float *>(smem);
-  void *q_smem = smem + kWarps * S::kRing * S::kHalf;
+  const unsigned ring = smem_u32(smem) + warp * S::kRing * S::kHalf;
+  float *join = reinterpret_cast<float *>(smem + kWarps * S::kRing * S::kHalf);
+  void *q_smem = smem + kWarps * S::kRing * S::kHalf + S::kJoinBytes;
 
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
@@ -437,22 +542,102 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_paged_kernel(const __grid_c
     }
   }
   __syncthreads();
-  uint32_t seq = s_seq;
-  long long in_seq = s_offset;  // units of the request before this point
 
-  W w;
-  for (long long u = u0; u < u1;) {
-    Request r = request<kRows>(c, seq);
-    while (in_seq >= r.units(c)) {  // next request with work
-      in_seq = 0;
-      if (++seq >= c.n_seqs) return;
-      r = request<kRows>(c, seq);
+  // The ring's feed runs ahead of the products, across items: `f` is the item
+  // that the next half tile belongs to, `f_i` its tile.
+  Item<kRows> f;
+  f.seq = s_seq;
+  f.in_seq = s_offset;
+  f.r = request<kRows>(c, f.seq);
+  Item<kRows> it = f;
+  long long f_u = u0;
+  int f_i = 0, f_n = 0, f_head = 0;
+  unsigned f_slot = 0;
+  const int32_t *f_table = nullptr;
+  bool f_value = false, f_any = false;
+  unsigned bad_slots = 0;  // bit i: the K tile in slot i of the ring is not there (its page is none of the cache's)
+  int page = 0;           // the page of the next tile (of this lane's row of it), looked up a tile ahead
+  long long row_at = 0;   // byte offset of the tile's first row (of this lane's row; -1: zeros) in the caches
+  constexpr int kPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;  // rows one access of the warp covers
+  const int my_row = S::kChunks >= 32 ? 0 : lane / S::kChunks, my_chunk = lane % S::kChunks;
+  const long long slot_bytes = c.slot_stride * static_cast<int>(sizeof(T));
+  const long long my_src = my_row * slot_bytes + my_chunk * 16;
+  const unsigned my_dst = swizzled<T, D>(my_row, my_chunk);
+  auto look_up = [&] {
+    const int key = f.k0 + kTile * warp + f_i * kUnit + (c.whole_tiles ? 0 : lane & 15);
+    page = key < f.k1 ? f_table[c.page_div.div(key)] : 0;
+  };
+  auto next_item = [&] {  // to the next item in which this warp has a tile
+    for (f_any = false; f.find(c, f_u, u1); ) {
+      f_u += f.tile1 - f.tile0;
+      f.in_seq += f.tile1 - f.tile0;
+      f_n = f.tiles_of(warp);
+      if (f_n > 0) {
+        f_any = true;
+        f_i = 0;
+        f_head = f.item / f.r.blocks;
+        f_table = c.table + static_cast<uint64_t>(f.seq) * c.max_pages;
+        look_up();
+        break;
+      }
     }
-    const int item = static_cast<int>(in_seq / r.tiles);  // (head, row block) of the request
-    const int tile0 = static_cast<int>(in_seq - static_cast<long long>(item) * r.tiles);
-    const int tile1 = static_cast<int>(min(static_cast<long long>(r.tiles), tile0 + (u1 - u)));
-    const int head = item / r.blocks, block = item - head * r.blocks;
-    const int k0 = r.lo + tile0 * kUnit, k1 = min(r.len, r.lo + tile1 * kUnit);
+  };
+  next_item();
+  auto fetch = [&] {  // the next half tile: K of a tile, then its V
+    if (f_any) {
+      const char *base = static_cast<const char *>(f_value ? c.v : c.k);
+      const unsigned to = ring + f_slot * S::kHalf;
+      if (c.whole_tiles) {  // a tile lies in one page: rows past the end are another request's or stale, and cut out later
+        if (!f_value) {
+          const int key = f.k0 + kTile * warp + f_i * kUnit;
+          const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
+          const bool none = static_cast<uint32_t>(page) >= c.n_pages;
+          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
+          if (none) page = 0;
+          row_at = (page * c.page_stride + f_head * c.head_stride) * static_cast<int>(sizeof(T)) + o * slot_bytes;
+        }
+        const char *src = base + row_at + my_src;
+#pragma unroll
+        for (int x = 0; x < kTile * S::kChunks / 32; ++x) {
+          const int row = x * 32 / S::kChunks;
+          const unsigned dst = to + (my_dst ^ (order<T>(row) << 4)) + row * S::kRowBytes + (S::kChunks > 32 ? (x & 1) * 512 : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src + (S::kChunks > 32 ? (x & 1) * 512 : 0)) : "memory");
+          if (S::kChunks <= 32 || (x & 1)) src += kPer * slot_bytes;
+        }
+      } else {
+        if (!f_value) {
+          const int key = f.k0 + kTile * warp + f_i * kUnit + (lane & 15);
+          const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
+          const bool none = key < f.k1 && static_cast<uint32_t>(page) >= c.n_pages;
+          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
+          row_at = key < f.k1 && !none
+                       ? (page * c.page_stride + f_head * c.head_stride) * static_cast<int>(sizeof(T)) + o * slot_bytes
+                       : -1;
+        }
+#pragma unroll 4
+        for (int x = 0; x < kTile * S::kChunks / 32; ++x) {
+          const int row = (x * 32 + lane) / S::kChunks, ch = (x * 32 + lane) % S::kChunks;
+          const long long off = __shfl_sync(kFull, row_at, row);
+          cp_async_16_or_zero(to + swizzled<T, D>(row, ch), base + (off < 0 ? 0 : off) + ch * 16, off >= 0);
+        }
+      }
+      f_slot = f_slot + 1 == S::kRing ? 0 : f_slot + 1;
+      if (f_value) {
+        if (++f_i < f_n) look_up();
+        else next_item();
+      }
+      f_value = !f_value;
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int h = 0; h < S::kRing - 1; ++h) fetch();
+
+  W w(lane);
+  unsigned slot = 0;
+  for (long long u = u0; it.find(c, u, u1);) {
+    const Request &r = it.r;
+    const int head = it.item / r.blocks, block = it.item - head * r.blocks;
 
     // Column n of the score tile is row block * kRows + n of the item: token row / group, query head row % group.
     const int rows = r.tokens * static_cast<int>(c.group);
@@ -476,136 +661,113 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_paged_kernel(const __grid_c
       }
     const int t_first = c.group_div.div(block * kRows), t_last = c.group_div.div(min(block * kRows + kRows, rows) - 1);
     // keys in [all0, all1) are seen by every row of the block
-    const int all1 = r.len - r.tokens + t_first + 1;
+    const int all1 = min(r.len - r.tokens + t_first + 1, it.k1);
     const int all0 = c.window ? r.len - r.tokens + t_last + 1 - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
     if (W::kQSmem) __syncthreads();
 
+    // Sums are kept relative to 2^m; m follows the running maximum only when that has grown by more than
+    // 2^8, so that the rescaling is rare (a probability is then below 2^8, far from f32's range).  Starting
+    // from the lowest finite value, a column that sees nothing keeps zero sums.
     float acc[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.0f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kLowest;
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    // This warp's tiles: keys k0 + 16 (warp + 4 i).
-    const int first = k0 + kTile * warp;
-    const int n_tiles = first < k1 ? (k1 - first + kUnit - 1) / kUnit : 0;
-    const int32_t *table = c.table + static_cast<uint64_t>(seq) * c.max_pages;
-    // Lane i < 16 (and i + 16) looks up tile row i: page number now, a tile ahead of its use.
-    auto page_of = [&](int i) -> int {
-      const int key = first + i * kUnit + (lane & 15);
-      return i < n_tiles && key < k1 ? table[c.page_div.div(key)] : 0;
-    };
-    int page = page_of(0);
+    const int n_tiles = it.tiles_of(warp);
+    int key0 = it.k0 + kTile * warp;
     bool bad_page = false;
-    long long row_at = -1;  // element offset of this lane's row of the tile being fetched; -1: zeros
-    auto fetch = [&](int h) {  // half tile h: K of tile h / 2, or V
-      const int i = h >> 1;
-      if (i < n_tiles) {
-        if (!(h & 1)) {
-          const int key = first + i * kUnit + (lane & 15);
-          const int j = c.page_div.div(key);
-          row_at = -1;
-          if (key < k1) {
-            if (static_cast<uint32_t>(page) < c.n_pages)
-              row_at = page * c.page_stride + head * c.head_stride + static_cast<int64_t>(key - j * static_cast<int>(c.page_size)) * c.slot_stride;
-            else
-              bad_page = true;
-          }
-          page = page_of(i + 1);
-        }
-        const T *base = static_cast<const T *>(h & 1 ? c.v : c.k);
-        const unsigned to = ring_at + (h % S::kRing) * S::kHalf;
-#pragma unroll
-        for (int x = 0; x < kTile * S::kChunks / 32; ++x) {
-          const int at = x * 32 + lane, row = at / S::kChunks, ch = at % S::kChunks;
-          const long long off = __shfl_sync(kFull, row_at, row);
-          cp_async_16_or_zero(to + swizzled<T, D>(row, ch), base + (off < 0 ? 0 : off) + ch * (16 / static_cast<int>(sizeof(T))), off >= 0);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int h = 0; h < S::kRing - 1; ++h) fetch(h);
-
-    unsigned slot = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int key0 = first + i * kUnit;
+#pragma unroll 1
+    for (int i = 0; i < n_tiles; ++i, key0 += kUnit) {
       // scores
-      fetch(2 * i + S::kRing - 1);
+      fetch();
       cp_async_wait<S::kRing - 1>();
       __syncwarp();
       float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-      w.scores(s, ring_at + slot * S::kHalf, q_smem, lane);
+      w.scores(s, ring + slot * S::kHalf, q_smem);
+      bad_page |= bad_slots >> slot & 1;
       slot = slot + 1 == S::kRing ? 0 : slot + 1;
-      const bool edge = key0 + kTile > min(all1, k1) || key0 < all0;
+      const bool edge = key0 + kTile > all1 || key0 < all0;
+      bool grown = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = s[nt][j] * c.scale_log2, y = s[nt][j + 2] * c.scale_log2;
-          if (edge) {
-            const int ka = key0 + lane / 4, kb = ka + 8;
-            const int hi = min(last[nt][j], k1 - 1);
-            const long long lo = c.window ? static_cast<long long>(last[nt][j]) - c.window : -1;
-            if (ka > hi || ka <= lo) x = -INFINITY;
-            if (kb > hi || kb <= lo) y = -INFINITY;
+        for (int j = 0; j < 4; ++j) s[nt][j] *= c.scale_log2;
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = key0 + lane / 4 + (j >> 1) * 8, hi = min(last[nt][j & 1], it.k1 - 1);
+            const long long lo = c.window ? static_cast<long long>(last[nt][j & 1]) - c.window : -1;
+            if (key > hi || key <= lo) s[nt][j] = -INFINITY;
           }
-          float top = fmaxf(x, y);
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-          top = fmaxf(top, m[nt][j]);
-          const float base = top == -INFINITY ? 0.0f : top;  // nothing seen yet: exp2(-inf) = 0
-          f[j] = exp2f(m[nt][j] - base);
-          m[nt][j] = top;
-          s[nt][j] = exp2f(x - base);
-          s[nt][j + 2] = exp2f(y - base);
-          l[nt][j] = l[nt][j] * f[j] + (s[nt][j] + s[nt][j + 2]);
-        }
-        if (__any_sync(kFull, f[0] != 1.0f || f[1] != 1.0f)) {
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) grown |= s[nt][j] > m[nt][j & 1] + 8.0f;
+      if (__any_sync(kFull, grown)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float g[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(s[nt][j], s[nt][j + 2]);
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+            top = fmaxf(top, m[nt][j]);
+            g[j] = exp2_fast(m[nt][j] - top);
+            m[nt][j] = top;
+            l[nt][j] *= g[j];
+          }
 #pragma unroll
           for (int md = 0; md < D / 16; ++md) {
-            acc[md][nt][0] *= f[0];
-            acc[md][nt][1] *= f[1];
-            acc[md][nt][2] *= f[0];
-            acc[md][nt][3] *= f[1];
+            acc[md][nt][0] *= g[0];
+            acc[md][nt][1] *= g[1];
+            acc[md][nt][2] *= g[0];
+            acc[md][nt][3] *= g[1];
           }
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[nt][j] = exp2_fast(s[nt][j] - m[nt][j]);
+          s[nt][j + 2] = exp2_fast(s[nt][j + 2] - m[nt][j]);
+          l[nt][j] += s[nt][j] + s[nt][j + 2];
+        }
       const typename W::P p(s, lane);
       // output
       __syncwarp();
-      fetch(2 * i + S::kRing);
+      fetch();
       cp_async_wait<S::kRing - 1>();
       __syncwarp();
-      const unsigned v_tile = ring_at + slot * S::kHalf;
+      const unsigned v_tile = ring + slot * S::kHalf;
       slot = slot + 1 == S::kRing ? 0 : slot + 1;
-      if (!edge || t_first == t_last) {
+      if (!edge) {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
-          typename W::V v(v_tile, md, lane);
-          if (edge) v.keep(all0 - key0, min(all1, k1) - key0, lane);
+          const typename W::V v(w, v_tile, md);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p, nt);
         }
       } else {
-        // Tokens see different keys of this tile.  A key that a token does not see must not reach its
-        // row even as 0 * v (v may be infinite or NaN), so each token's columns take the product with
-        // V's unseen keys cut out.
+        // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite
+        // or NaN), so each token's columns take the product with V's unseen keys cut out.
 #pragma unroll 1
         for (int t = t_first; t <= t_last; ++t) {
           const int hi = r.len - r.tokens + t + 1 - key0;
-          const int lo = c.window ? hi - static_cast<int>(min(c.window, 0x3fffffffu)) : -1;
+          const int lo = c.window ? hi - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
 #pragma unroll
           for (int md = 0; md < D / 16; ++md) {
-            typename W::V v(v_tile, md, lane);
-            v.keep(lo, min(hi, k1 - key0), lane);
+            typename W::V v(w, v_tile, md);
+            v.keep(lo, min(hi, it.k1 - key0), lane);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -619,71 +781,82 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_paged_kernel(const __grid_c
       }
       __syncwarp();
     }
-    cp_async_wait<0>();
 
     // Join the four warps.
     bad_page = __any_sync(kFull, bad_page);
     if (lane == 0) s_bad[warp] = bad_page;
-    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = nt * 8 + (lane & 3) * 2 + j;
         float x = l[nt][j];
         x += __shfl_xor_sync(kFull, x, 4);
         x += __shfl_xor_sync(kFull, x, 8);
         x += __shfl_xor_sync(kFull, x, 16);
         if (lane < 4) {
-          s_m[warp][row] = m[nt][j];
-          s_l[warp][row] = x;
-        }
-#pragma unroll
-        for (int md = 0; md < D / 16; ++md) {
-          join[(warp * kRows + row) * kJoinRow + md * 16 + lane / 4] = acc[md][nt][j];
-          join[(warp * kRows + row) * kJoinRow + md * 16 + lane / 4 + 8] = acc[md][nt][j + 2];
+          s_m[warp][nt * 8 + lane * 2 + j] = m[nt][j];
+          s_l[warp][nt * 8 + lane * 2 + j] = x;
         }
       }
-    __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == r.tiles;
+    const bool whole = it.tile0 == 0 && it.tile1 == r.tiles;
     const int part_slot = 2 * cta + (u == u0 ? 0 : 1);
-    const bool poison = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];  // rows over a page that does not exist are NaN
-    if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
-    for (int x = tid; x < kRows * D; x += kThreads) {
-      const int row = x / D, d = x % D, item_row = block * kRows + row;
-      if (item_row >= rows) break;
-      float top = s_m[0][row];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][row]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f, den = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float f = exp2f(s_m[i][row] - base);
-        sum += f * join[(i * kRows + row) * kJoinRow + d];
-        den += f * s_l[i][row];
-      }
-      if (poison) sum = den = NAN;
-      if (whole) {
-        const int t = c.group_div.div(item_row);
-        // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
-        const bool empty = r.len - r.tokens + t < 0;
-        T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
-               (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d;
-        Act<T>::put(o, empty && !poison ? 0.0f : sum / den);
-      } else {
-        c.part[(static_cast<size_t>(part_slot) * kRows + row) * D + d] = sum;
-        if (d == 0) c.part_ml[static_cast<size_t>(part_slot) * kRows + row] = make_float2(top, den);
+      for (int d0 = 0; d0 < D; d0 += S::kJoinCols) {
+#pragma unroll
+        for (int md = 0; md < S::kJoinCols / 16; ++md)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * S::kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
+        __syncthreads();
+        const bool poison = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];  // rows over a page that does not exist are NaN
+        if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
+#pragma unroll 1
+        for (int x = tid; x < 8 * S::kJoinCols / 4; x += kThreads) {
+          const int row = x / (S::kJoinCols / 4), d = x % (S::kJoinCols / 4) * 4, n = nt * 8 + row;
+          const int item_row = block * kRows + n;
+          if (item_row >= rows) break;
+          float top = s_m[0][n];
+#pragma unroll
+          for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][n]);
+          float sum[4] = {}, den = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) {
+            const float g = exp2_fast(s_m[i][n] - top);
+            const float4 y = *reinterpret_cast<const float4 *>(join + (i * 8 + row) * S::kJoinRow + d);
+            sum[0] += g * y.x;
+            sum[1] += g * y.y;
+            sum[2] += g * y.z;
+            sum[3] += g * y.w;
+            den += g * s_l[i][n];
+          }
+          if (poison) den = NAN;
+          if (whole) {
+            const int t = c.group_div.div(item_row);
+            // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
+            const bool empty = r.len - r.tokens + t < 0 && !poison;
+            T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
+                   (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d0 + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Act<T>::put(o + e, empty ? 0.0f : sum[e] / den);
+          } else {
+            const size_t at = static_cast<size_t>(part_slot) * kRows + n;
+            *reinterpret_cast<float4 *>(c.part + at * D + d0 + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            if (d0 + d == 0) c.part_ml[at] = make_float2(top, den);
+          }
+        }
+        __syncthreads();
       }
     }
-    if (!whole && tile0 == 0 && tid == 0) {
+    if (!whole && it.tile0 == 0 && tid == 0) {
       const long long end = u + r.tiles - 1;  // the item's last unit
-      c.meta[cta] = make_int4(static_cast<int>(seq), item, static_cast<int>(((end + 1) * ctas - 1) / total), part_slot);
+      c.meta[cta] = make_int4(static_cast<int>(it.seq), it.item, static_cast<int>(((end + 1) * ctas - 1) / total), part_slot);
     }
-    u += tile1 - tile0;
-    in_seq += tile1 - tile0;
-    __syncthreads();
+    u += it.tile1 - it.tile0;
+    it.in_seq += it.tile1 - it.tile0;
   }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ the join
@@ -705,16 +878,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const __
   const int x0 = blockIdx.x, n = meta.z - x0 + 1;
   auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? meta.w : 2 * (x0 + i)) * kRows + row; };
 
-  float top = -INFINITY;
+  float top = kLowest;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, c.part_ml[slot(i)].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-  const float base = top == -INFINITY ? 0.0f : top;
   float acc[kPer] = {}, den = 0.0f;
 #pragma unroll 4
   for (int i = warp; i < n; i += kJoinWarps) {
     const float2 ml = c.part_ml[slot(i)];
-    const float f = exp2f(ml.x - base);
+    const float f = exp2_fast(ml.x - top);
     den += f * ml.y;
     const float *src = c.part + slot(i) * D + lane;
 #pragma unroll
@@ -741,12 +913,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const __
 
 // ------------------------------------------------------------ host
 
-template <typename T, int D, int NT>
-constexpr int ctas_per_sm() {
-  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT>() + 2048);
-  return by_smem < 1 ? 1 : by_smem > 4 ? 4 : by_smem;
-}
-
 int row_tiles(const gdn_attn_params &p) {
   const uint64_t window = (p.n_tokens + static_cast<uint64_t>(p.n_seqs) - 1) / p.n_seqs;
   return window * (p.n_q_heads / p.n_kv_heads) <= 8 ? 1 : 2;
@@ -756,7 +922,9 @@ int row_tiles(const gdn_attn_params &p) {
 template <typename F>
 auto dispatch(const gdn_attn_params &p, F f) {
   auto by_rows = [&](auto t, auto d) {
-    return row_tiles(p) == 1 ? f(t, d, std::integral_constant<int, 1>{}) : f(t, d, std::integral_constant<int, 2>{});
+    // the rings and q of 16 rows do not fit an SM's shared memory at 1 KB per key
+    constexpr int most = sizeof(t) * d() >= 1024 ? 1 : 2;
+    return row_tiles(p) == 1 ? f(t, d, std::integral_constant<int, 1>{}) : f(t, d, std::integral_constant<int, most>{});
   };
   auto by_dim = [&](auto t) {
     return p.head_dim == 64    ? by_rows(t, std::integral_constant<int, 64>{})
@@ -772,7 +940,7 @@ size_t part_floats(int ctas, int rows, int d) { return static_cast<size_t>(2) * 
 
 size_t attn_workspace_bytes(const gdn_attn_params &p) {
   return dispatch(p, [&](auto t, auto d, auto nt) {
-    constexpr int ctas = kSms * ctas_per_sm<decltype(t), d(), nt()>();
+    constexpr int ctas = kSms * Shape<decltype(t), d()>::kCtas;
     return part_floats(ctas, nt() * 8, d()) * 4 + static_cast<size_t>(2) * ctas * nt() * 8 * sizeof(float2) +
            ctas * sizeof(int4);
   });
@@ -804,9 +972,10 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   c.slot_stride = p.cache_slot_stride;
   c.page_div = FastDiv(p.page_size);
   c.group_div = FastDiv(c.group);
+  c.whole_tiles = p.page_size % kTile == 0;
   return dispatch(p, [&](auto t, auto d, auto nt) {
     using T = decltype(t);
-    constexpr int D = d(), NT = nt(), ctas = kSms * ctas_per_sm<T, D, NT>(), smem = smem_bytes<T, D, NT>();
+    constexpr int D = d(), NT = nt(), ctas = kSms * Shape<T, D>::kCtas, smem = smem_bytes<T, D, NT>();
     // widest alignment first: sums, (maximum, sum) pairs, item records
     c.meta = static_cast<int4 *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.meta + ctas);
