@@ -8,9 +8,11 @@
 // Products and sums are f32; a result is rounded once, when stored.
 //
 // One pass: every element is read once and written once, so HBM bounds long
-// prompts and latency bounds decode steps.  A CTA takes one token (or a part of
-// its heads): the token's R cos/sin values are gathered once into shared memory
-// for all heads, while the row data is already on its way into registers.
+// prompts and latency bounds decode steps.  A lane keeps one place in the head
+// (E pairs, as two vectors: their halves, or neighbours) and goes through the
+// rows of a token, a warp covering 32 / (places per head) rows at a time: the
+// token's cosines stay in the lane's registers for all of them, several rows
+// are on their way at once, and no warp waits for another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,138 +25,199 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;  // items (two vectors each) a thread has in flight
-constexpr int kMaxRot = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 2;  // rows a lane has on their way
+constexpr int kCtasPerSm = 6;
+constexpr uint32_t kEnoughWarps = 152 * kCtasPerSm * kWarps;  // what the GPU holds
 
-// E contiguous elements: one 16-byte access, or a single element.
+// E contiguous elements, moved in one access of 16 bytes (or one element), and
+// their values in f32; one rounding to nearest on the way back.
 template <typename T, int E>
-struct alignas(sizeof(T) * E) Vec {
-  T x[E];
+struct Vec;
+
+template <int E>
+struct alignas(4 * E) Vec<float, E> {
+  float x[E];
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = x[e];
+  }
+  __device__ __forceinline__ void put(const float (&f)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = f[e];
+  }
 };
 
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void narrow(float *d, float x) { *d = x; }
-__device__ __forceinline__ void narrow(__nv_bfloat16 *d, float x) { *d = __float2bfloat16_rn(x); }
-
-struct RopeDivs {
-  FastDiv items, page;
-};
-
-template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const __grid_constant__ RopeArgs a,
-                                                            const RopeDivs dv) {
-  using V = Vec<T, E>;
-  __shared__ float s_cs[kMaxRot];
-  const gdn_rope_params &p = a.p;
-  const uint32_t token = blockIdx.x, half = p.rot_dim / 2;
-  const bool store = a.v != nullptr, inter = (p.flags & GDN_ROPE_INTERLEAVED) != 0;
-  const uint32_t per_row = p.head_dim / (2 * E), rot_items = p.rot_dim / (2 * E);
-
-  long long slot_at = -1;  // element offset of the token's slot in the caches
-  if (store) {
-    const int slot = a.slot_map[token];
-    if (slot >= 0) {
-      const uint32_t page = dv.page.div(static_cast<uint32_t>(slot));
-      if (page < p.n_pages)
-        slot_at = page * p.cache_page_stride + (slot - static_cast<long long>(page) * p.page_size) * p.cache_slot_stride;
-      else if (threadIdx.x == 0)
-        report(GDN_DEVICE_BAD_PAGE);
+template <int E>
+struct alignas(2 * E) Vec<__nv_bfloat16, E> {
+  __nv_bfloat162 x[E / 2];
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 y = __bfloat1622float2(x[e]);
+      f[2 * e] = y.x;
+      f[2 * e + 1] = y.y;
     }
   }
-  // rows of the token: q heads, k heads, v heads; without a slot k and v go nowhere
-  const uint32_t rows = p.n_q_heads + (store ? (slot_at >= 0 ? 2 * p.n_kv_heads : 0) : p.n_kv_heads);
-  const uint32_t n_items = rows * per_row;
+  __device__ __forceinline__ void put(const float (&f)[E]) {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) x[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+  }
+};
 
-  bool staged = false;
-  for (uint32_t i0 = blockIdx.y * (kThreads * kUnroll) + threadIdx.x; i0 < n_items || !staged;
-       i0 += gridDim.y * (kThreads * kUnroll)) {
-    V lo[kUnroll], hi[kUnroll];
-    const T *src[kUnroll];
-    T *dst[kUnroll];
-    uint32_t col[kUnroll], gap[kUnroll];
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  __nv_bfloat16 x;
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(x); }
+  __device__ __forceinline__ void put(const float (&f)[1]) { x = __float2bfloat16_rn(f[0]); }
+};
+
+// Rotates the E pairs of two vectors: (lo[e], hi[e]), or neighbours within lo, then hi.
+template <typename T, int E>
+__device__ __forceinline__ void rotate(Vec<T, E> &lo, Vec<T, E> &hi, const float (&c)[E], const float (&s)[E], bool inter) {
+  float a[E], b[E];
+  lo.get(a);
+  hi.get(b);
+  if (inter && E > 1) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t item = i0 + u * kThreads;
-      if (item >= n_items) continue;
-      const uint32_t row = dv.items.div(item), j = item - row * per_row;
-      // the item's two vectors: a pair's two halves, or neighbours
-      const bool split = !inter && j < rot_items;
-      col[u] = split ? j * E : j * 2 * E;
-      gap[u] = split ? half : E;
-      if (row < p.n_q_heads) {
-        src[u] = static_cast<const T *>(a.q) + token * p.q_stride + row * p.head_dim;
-        dst[u] = static_cast<T *>(a.q_out) + token * p.q_out_stride + row * p.head_dim;
-      } else if (row < p.n_q_heads + p.n_kv_heads) {
-        const uint32_t h = row - p.n_q_heads;
-        src[u] = static_cast<const T *>(a.k) + token * p.k_stride + h * p.head_dim;
-        dst[u] = store ? static_cast<T *>(a.k_cache) + slot_at + h * p.cache_head_stride
-                       : static_cast<T *>(a.k_out) + token * p.k_out_stride + h * p.head_dim;
-      } else {
-        const uint32_t h = row - p.n_q_heads - p.n_kv_heads;
-        src[u] = static_cast<const T *>(a.v) + token * p.v_stride + h * p.head_dim;
-        dst[u] = static_cast<T *>(a.v_cache) + slot_at + h * p.cache_head_stride;
-        col[u] = j * 2 * E;
-        gap[u] = E;
-      }
-      lo[u] = *reinterpret_cast<const V *>(src[u] + col[u]);
-      hi[u] = *reinterpret_cast<const V *>(src[u] + col[u] + gap[u]);
+    for (int e = 0; e < E / 2; ++e) {
+      const float x = a[2 * e], y = b[2 * e];
+      a[2 * e] = x * c[e] - a[2 * e + 1] * s[e];
+      a[2 * e + 1] = a[2 * e + 1] * c[e] + x * s[e];
+      b[2 * e] = y * c[E / 2 + e] - b[2 * e + 1] * s[E / 2 + e];
+      b[2 * e + 1] = b[2 * e + 1] * c[E / 2 + e] + y * s[E / 2 + e];
     }
-    if (!staged) {
-      for (uint32_t j = threadIdx.x; j < half; j += kThreads) {
-        const int pos = a.positions[p.axis_of_pair[j] * p.positions_stride + token];
-        float c, s;
-        if (static_cast<uint32_t>(pos) < p.n_positions) {
-          const float *t = a.cos_sin + static_cast<uint64_t>(pos) * p.rot_dim;
-          c = t[j];
-          s = t[half + j];
-        } else {  // no such row: the token's rotated values are NaN
-          c = s = nanf("");
-          report(GDN_DEVICE_BAD_POSITION);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float x = a[e];
+      a[e] = x * c[e] - b[e] * s[e];
+      b[e] = b[e] * c[e] + x * s[e];
+    }
+  }
+  lo.put(a);
+  hi.put(b);
+}
+
+constexpr uint32_t kMixed = 255;
+
+struct RopeDivs {
+  FastDiv parts, page;
+  uint32_t n_parts;      // a token's rows are cut into this many parts, one per warp
+  uint32_t part_rows;
+  uint8_t place_axis[GDN_ROPE_MAX_DIM / 2];  // the axis of a place's E pairs; kMixed: several, or cos_sin only by the element
+};
+
+template <typename T, int E>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __grid_constant__ RopeArgs a,
+                                                                        const RopeDivs dv) {
+  using V = Vec<T, E>;
+  const gdn_rope_params &p = a.p;
+  const uint32_t half = p.rot_dim / 2, lane = threadIdx.x & 31;
+  const bool store = a.v != nullptr, inter = (p.flags & GDN_ROPE_INTERLEAVED) != 0;
+  const uint32_t places = p.head_dim / (2 * E), rot_places = p.rot_dim / (2 * E);
+  // rows of a token: q heads, k heads, v heads
+  const uint32_t k_row = p.n_q_heads, v_row = k_row + p.n_kv_heads;
+  const uint32_t n_rows = store ? v_row + p.n_kv_heads : v_row;
+  // the warp's rows at a time (one where a head has more places than the warp has lanes)
+  const uint32_t at_once = places < 32 ? 32 / places : 1, my_row = places < 32 ? lane / places : 0;
+  const bool active = my_row < at_once;
+  const uint32_t n_units = p.n_tokens * dv.n_parts;  // below 2^31: parts > 1 only with few tokens
+
+  for (uint32_t j = places < 32 ? lane - my_row * places : lane; j < places; j += 32) {
+    const bool turns = j < rot_places;
+    // where q and k rows have this place's two vectors, and v rows
+    const uint32_t col = turns && !inter ? j * E : j * 2 * E, gap = turns && !inter ? half : E, v_col = j * 2 * E;
+    const uint32_t axis = turns ? dv.place_axis[j] : 0;
+
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit < n_units) {
+      const uint32_t token = dv.parts.div(unit), part = unit - token * dv.n_parts;
+      const uint32_t row1 = min(n_rows, (part + 1) * dv.part_rows);
+      const int slot = store ? a.slot_map[token] : -1;
+      const T *q = static_cast<const T *>(a.q) + token * p.q_stride, *k = static_cast<const T *>(a.k) + token * p.k_stride,
+              *v = static_cast<const T *>(a.v) + token * p.v_stride;
+      V lo[kUnroll], hi[kUnroll];
+      auto load = [&](uint32_t r0) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const uint32_t r = r0 + u * at_once;
+          if (r >= row1 || !active) continue;
+          const T *src = r < k_row   ? q + r * p.head_dim + col
+                         : r < v_row ? k + (r - k_row) * p.head_dim + col
+                                     : v + (r - v_row) * p.head_dim + v_col;
+          lo[u] = *reinterpret_cast<const V *>(src);
+          hi[u] = *reinterpret_cast<const V *>(src + (r < v_row ? gap : E));
         }
-        s_cs[j] = c;
-        s_cs[half + j] = (p.flags & GDN_ROPE_INVERSE) ? -s : s;
-      }
-      __syncthreads();
-      staged = true;
-    }
+      };
+      uint32_t r0 = part * dv.part_rows + my_row;
+      load(r0);  // on its way while the cosines are looked up
+      float c[E], s[E];
+      if (turns) {
+        if (E % 4 == 0 && axis != kMixed) {
+          const int pos = a.positions[axis * p.positions_stride + token];
+          if (static_cast<uint32_t>(pos) < p.n_positions) {
+            const float *t = a.cos_sin + static_cast<uint64_t>(pos) * p.rot_dim + j * E;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t item = i0 + u * kThreads;
-      if (item >= n_items) continue;
-      const uint32_t row = dv.items.div(item), j = item - row * per_row;
-      if (row < p.n_q_heads + p.n_kv_heads && j < rot_items) {
-        const uint32_t c0 = j * E;  // first of the item's E pairs
-        if (inter) {
-          if constexpr (E == 1) {  // the pair is (lo, hi)
-            const float fa = widen(lo[u].x[0]), fb = widen(hi[u].x[0]), c = s_cs[c0], s = s_cs[half + c0];
-            narrow(&lo[u].x[0], fa * c - fb * s);
-            narrow(&hi[u].x[0], fb * c + fa * s);
-          } else {
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-              const float c = s_cs[c0 + e], s = s_cs[half + c0 + e];
-              const float c2 = s_cs[c0 + E / 2 + e], s2 = s_cs[half + c0 + E / 2 + e];
-              const float fa = widen(lo[u].x[2 * e]), fb = widen(lo[u].x[2 * e + 1]);
-              const float ga = widen(hi[u].x[2 * e]), gb = widen(hi[u].x[2 * e + 1]);
-              narrow(&lo[u].x[2 * e], fa * c - fb * s);
-              narrow(&lo[u].x[2 * e + 1], fb * c + fa * s);
-              narrow(&hi[u].x[2 * e], ga * c2 - gb * s2);
-              narrow(&hi[u].x[2 * e + 1], gb * c2 + ga * s2);
+            for (int e = 0; e + 3 < E; e += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(t + e), y = *reinterpret_cast<const float4 *>(t + half + e);
+              c[e] = x.x, c[e + 1] = x.y, c[e + 2] = x.z, c[e + 3] = x.w;
+              s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
             }
+          } else {  // no such row: the token's rotated values are NaN
+#pragma unroll
+            for (int e = 0; e < E; ++e) c[e] = s[e] = nanf("");
+            report(GDN_DEVICE_BAD_POSITION);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float c = s_cs[c0 + e], s = s_cs[half + c0 + e];
-            const float fa = widen(lo[u].x[e]), fb = widen(hi[u].x[e]);
-            narrow(&lo[u].x[e], fa * c - fb * s);
-            narrow(&hi[u].x[e], fb * c + fa * s);
+            const int pos = a.positions[p.axis_of_pair[j * E + e] * p.positions_stride + token];
+            if (static_cast<uint32_t>(pos) < p.n_positions) {
+              const float *t = a.cos_sin + static_cast<uint64_t>(pos) * p.rot_dim + j * E + e;
+              c[e] = t[0];
+              s[e] = t[half];
+            } else {
+              c[e] = s[e] = nanf("");
+              report(GDN_DEVICE_BAD_POSITION);
+            }
           }
         }
+        if (p.flags & GDN_ROPE_INVERSE) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[e] = -s[e];
+        }
       }
-      *reinterpret_cast<V *>(dst[u] + col[u]) = lo[u];
-      *reinterpret_cast<V *>(dst[u] + col[u] + gap[u]) = hi[u];
+      long long slot_at = -1;  // element offset of the token's slot in the caches; -1: k and v go nowhere
+      if (slot >= 0) {
+        const uint32_t page = dv.page.div(static_cast<uint32_t>(slot));
+        if (page < p.n_pages)
+          slot_at = page * p.cache_page_stride + static_cast<int64_t>(slot - page * p.page_size) * p.cache_slot_stride;
+        else
+          report(GDN_DEVICE_BAD_PAGE);
+      }
+      while (r0 < row1 && active) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const uint32_t r = r0 + u * at_once;
+          if (r >= row1) continue;
+          if (turns && r < v_row) rotate<T, E>(lo[u], hi[u], c, s, inter);
+          T *dst;
+          if (r < k_row) {
+            dst = static_cast<T *>(a.q_out) + token * p.q_out_stride + r * p.head_dim + col;
+          } else if (!store) {
+            dst = static_cast<T *>(a.k_out) + token * p.k_out_stride + (r - k_row) * p.head_dim + col;
+          } else {
+            if (slot_at < 0) continue;
+            dst = r < v_row ? static_cast<T *>(a.k_cache) + slot_at + (r - k_row) * p.cache_head_stride + col
+                            : static_cast<T *>(a.v_cache) + slot_at + (r - v_row) * p.cache_head_stride + v_col;
+          }
+          *reinterpret_cast<V *>(dst) = lo[u];
+          *reinterpret_cast<V *>(dst + (r < v_row ? gap : E)) = hi[u];
+        }
+        r0 += kUnroll * at_once;
+        load(r0);
+      }
     }
   }
 }
@@ -162,35 +225,54 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const __grid_constan
 template <typename T, int E>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   const gdn_rope_params &p = a.p;
-  const uint32_t per_row = p.head_dim / (2 * E);
-  const uint32_t items = (p.n_q_heads + p.n_kv_heads * (a.v ? 2 : 1)) * per_row;
-  const RopeDivs dv{FastDiv(per_row), FastDiv(p.page_size ? p.page_size : 1)};
-  const uint32_t y = (items + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  gdn_rope_kernel<T, E><<<dim3(p.n_tokens, y < 65535 ? y : 65535), kThreads, 0, stream>>>(a, dv);
+  const uint32_t places = p.head_dim / (2 * E), at_once = places < 32 ? 32 / places : 1;
+  const uint32_t rows = p.n_q_heads + p.n_kv_heads * (a.v ? 2 : 1);
+  RopeDivs dv;
+  dv.page = FastDiv(p.page_size ? p.page_size : 1);
+  // A token's rows to one warp, so that its cosines are read once; with fewer
+  // tokens to several warps, down to one step of rows each: latency.
+  const uint32_t steps = (rows + at_once - 1) / at_once;
+  uint32_t parts = p.n_tokens < kEnoughWarps ? kEnoughWarps / p.n_tokens : 1;
+  if (parts > steps) parts = steps;
+  dv.part_rows = (steps + parts - 1) / parts * at_once;
+  dv.n_parts = (rows + dv.part_rows - 1) / dv.part_rows;
+  dv.parts = FastDiv(dv.n_parts);
+  const bool wide = E % 4 == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && p.rot_dim % 8 == 0;
+  for (uint32_t j = 0; j < p.rot_dim / (2 * E); ++j) {
+    const uint8_t *x = p.axis_of_pair + j * E;
+    bool one = wide && x[0] < kMixed;
+    for (uint32_t e = 1; e < E; ++e) one = one && x[e] == x[0];
+    dv.place_axis[j] = one ? x[0] : kMixed;
+  }
+  const uint64_t ctas = (static_cast<uint64_t>(p.n_tokens) * dv.n_parts + kWarps - 1) / kWarps;
+  gdn_rope_kernel<T, E><<<static_cast<uint32_t>(ctas), kThreads, 0, stream>>>(a, dv);
   return cudaGetLastError();
 }
 
-// Whether every 16-byte vector of E elements that the vector form accesses is
-// aligned and none crosses the rotated part's or a head's end.
-template <typename T>
-bool vectors_fit(const RopeArgs &a) {
-  constexpr int E = 16 / sizeof(T);
+// Whether every access of E elements is aligned and none crosses the rotated
+// part's or a head's end.
+bool vectors_fit(const RopeArgs &a, uint32_t e, uint32_t elem) {
   const gdn_rope_params &p = a.p;
-  if (p.head_dim % (2 * E) || p.rot_dim % (2 * E)) return false;
+  if (p.head_dim % (2 * e) || p.rot_dim % (2 * e)) return false;
   const void *ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out, a.k_cache, a.v_cache};
   for (const void *x : ptrs)
-    if (reinterpret_cast<uintptr_t>(x) % 16) return false;
+    if (reinterpret_cast<uintptr_t>(x) % (e * elem)) return false;
   const int64_t strides[] = {p.q_stride, p.k_stride, a.v ? p.v_stride : 0, p.q_out_stride,
                              a.k_out ? p.k_out_stride : 0, a.v ? p.cache_page_stride : 0,
                              a.v ? p.cache_head_stride : 0, a.v ? p.cache_slot_stride : 0};
   for (int64_t s : strides)
-    if (s % E) return false;
+    if (s % e) return false;
   return true;
 }
 
+// 16-byte vectors where they fit, 8-byte ones for heads such as 72 bf16
+// elements, single elements for any other layout.
 template <typename T>
 cudaError_t launch_type(const RopeArgs &a, cudaStream_t stream) {
-  return vectors_fit<T>(a) ? launch<T, 16 / sizeof(T)>(a, stream) : launch<T, 1>(a, stream);
+  constexpr int E = 16 / sizeof(T);
+  return vectors_fit(a, E, sizeof(T))       ? launch<T, E>(a, stream)
+         : vectors_fit(a, E / 2, sizeof(T)) ? launch<T, E / 2>(a, stream)
+                                            : launch<T, 1>(a, stream);
 }
 
 }  // namespace
