@@ -24,7 +24,7 @@ import math
 import torch
 
 from ._native import (GDN_ERR_INVALID_ARGUMENT, GDN_OK, AttnParams, GdnError, KvPlanParams,
-                      RopeParams, _stream, gdn_last_error, lib)
+                      RopeParams, gdn_last_error, lib)
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2
@@ -38,27 +38,42 @@ def _bad(message):
     return GdnError(GDN_ERR_INVALID_ARGUMENT, message)
 
 
-def _look(t):
-    return t.dtype, t.shape, t.stride(), t.is_cuda
-
-
 def _looks(names, tensors):
     """What the params of a call depend on, for every tensor of it."""
     try:
-        return tuple(map(_look, tensors))
-    except AttributeError:
+        return tuple([(t.dtype, t.shape, t.stride(), t.get_device()) for t in tensors])
+    except (AttributeError, TypeError):
         for name, t in zip(names, tensors):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor (got {type(t)})") from None
         raise
 
 
+def _stream(stream, t):
+    """The call's stream handle: `stream`, or the current one of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_functions: dict = {}
+
+
+def _function(name):
+    """The library's function, looked up once."""
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    return f
+
+
 def _keep(key, make):
     got = _kept.get(key)
     if got is None:
+        made = make()
         if len(_kept) >= _MAX_KEPT:
             _kept.clear()
-        got = _kept[key] = make()
+        got = _kept[key] = made
     return got
 
 
@@ -66,6 +81,8 @@ def _cuda(names, tensors):
     for name, t in zip(names, tensors):
         if not t.is_cuda:
             raise _bad(f"{name} must be a CUDA tensor")
+        if t.device != tensors[0].device:
+            raise _bad(f"{name} must be on {names[0]}'s device")
 
 
 def _int32(name, t, shape):
@@ -109,9 +126,8 @@ def _dtype(name, t):
     return _DTYPES[t.dtype]
 
 
-def _done(st):
-    if st != GDN_OK:
-        raise GdnError(st, gdn_last_error())
+def _failed(st):
+    return GdnError(st, gdn_last_error())
 
 
 # ------------------------------------------------------------------ plan
@@ -140,10 +156,13 @@ def gdn_kv_plan(ctx_lens, new_lens, owned, free_pages, n_free, block_table, page
                   (n + 1,), (slot_map.numel(),), (slot_map.numel(),))
         for name, t, shape in zip(_PLAN, tensors, shapes):
             _int32(name, t, shape)
-        return KvPlanParams(n, page_size, n_pages, block_table.shape[1], free_pages.numel(), slot_map.numel())
+        return ctypes.byref(KvPlanParams(n, page_size, n_pages, block_table.shape[1], free_pages.numel(),
+                                         slot_map.numel()))
 
     p = _keep(("plan", page_size, n_pages, _looks(_PLAN, tensors)), make)
-    _done(lib().gdn_kv_plan(*[t.data_ptr() for t in tensors], ctypes.byref(p), _stream(stream, ctx_lens.device)))
+    st = _function("gdn_kv_plan")(*[t.data_ptr() for t in tensors], p, _stream(stream, ctx_lens))
+    if st != GDN_OK:
+        raise _failed(st)
 
 
 # ------------------------------------------------------------------ rope
@@ -199,14 +218,17 @@ def gdn_rope(q, k, positions, cos_sin, q_out, k_out, axes=None, interleaved=Fals
     of q and k from those of q_out and k_out."""
     tensors = (q, k, positions, cos_sin, q_out, k_out)
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
-    axes = bytes(axes) if axes is not None else None
+    if axes is not None and type(axes) is not bytes:
+        axes = bytes(axes)
 
     def make():
         _cuda(_ROPE, tensors)
-        return _rope_params(q, k, None, positions, cos_sin, q_out, k_out, None, None, None, axes, flags)
+        return ctypes.byref(_rope_params(q, k, None, positions, cos_sin, q_out, k_out, None, None, None, axes, flags))
 
     p = _keep(("rope", flags, axes, _looks(_ROPE, tensors)), make)
-    _done(lib().gdn_rope(*[t.data_ptr() for t in tensors], ctypes.byref(p), _stream(stream, q.device)))
+    st = _function("gdn_rope")(*[t.data_ptr() for t in tensors], p, _stream(stream, q))
+    if st != GDN_OK:
+        raise _failed(st)
 
 
 def gdn_rope_store(q, k, v, positions, cos_sin, slot_map, k_cache, v_cache, q_out, axes=None,
@@ -215,14 +237,18 @@ def gdn_rope_store(q, k, v, positions, cos_sin, slot_map, k_cache, v_cache, q_ou
     ``slot_map`` (int32 [n_tokens]; -1: nowhere)."""
     tensors = (q, k, v, positions, cos_sin, slot_map, q_out, k_cache, v_cache)
     flags = ROPE_INTERLEAVED if interleaved else 0
-    axes = bytes(axes) if axes is not None else None
+    if axes is not None and type(axes) is not bytes:
+        axes = bytes(axes)
 
     def make():
         _cuda(_STORE, tensors)
-        return _rope_params(q, k, v, positions, cos_sin, q_out, None, slot_map, k_cache, v_cache, axes, flags)
+        return ctypes.byref(_rope_params(q, k, v, positions, cos_sin, q_out, None, slot_map, k_cache, v_cache, axes,
+                                         flags))
 
     p = _keep(("store", flags, axes, _looks(_STORE, tensors)), make)
-    _done(lib().gdn_rope_store(*[t.data_ptr() for t in tensors], ctypes.byref(p), _stream(stream, q.device)))
+    st = _function("gdn_rope_store")(*[t.data_ptr() for t in tensors], p, _stream(stream, q))
+    if st != GDN_OK:
+        raise _failed(st)
 
 
 # ------------------------------------------------------------------ attention
@@ -248,7 +274,9 @@ def gdn_attn_workspace_size(q, k_cache, n_seqs) -> int:
     q's rows and heads; the lengths do not matter."""
     p = _attn_params(q, k_cache, k_cache, n_seqs, 1, None, None, 0)
     out = ctypes.c_size_t()
-    _done(lib().gdn_attn_workspace_size(ctypes.byref(p), ctypes.byref(out)))
+    st = lib().gdn_attn_workspace_size(ctypes.byref(p), ctypes.byref(out))
+    if st != GDN_OK:
+        raise _failed(st)
     return out.value
 
 
@@ -282,11 +310,12 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start, outpu
         if q.dim() != 3:
             raise _bad("q must be [n_tokens, n_q_heads, head_dim]")
         out_stride = _rows("output", output, q.dtype, q.shape)
-        return (_attn_params(q, k_cache, v_cache, n, block_table.shape[1], out_stride, scale, window),
+        return (ctypes.byref(_attn_params(q, k_cache, v_cache, n, block_table.shape[1], out_stride, scale, window)),
                 workspace.numel() * workspace.element_size())
 
     p, ws_bytes = _keep(("attn", ragged, scale, window, _looks(_ATTN, tensors)), make)
-    _done(lib().gdn_attn_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                               kv_lens.data_ptr(), token_start.data_ptr() if ragged else None,
-                               output.data_ptr(), ctypes.byref(p), workspace.data_ptr(), ws_bytes,
-                               _stream(stream, q.device)))
+    st = _function("gdn_attn_paged")(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                     kv_lens.data_ptr(), token_start.data_ptr() if ragged else None,
+                                     output.data_ptr(), p, workspace.data_ptr(), ws_bytes, _stream(stream, q))
+    if st != GDN_OK:
+        raise _failed(st)
