@@ -53,7 +53,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;               // keys per warp tile
 constexpr int kUnit = kTile * kWarps;   // keys per unit of work
 constexpr int kSms = 152;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
+constexpr int kMostParts = kSms * 3;  // CTAs of the main kernel
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite f32
@@ -181,9 +182,8 @@ struct Shape {
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
   static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
   static constexpr int kHalf = kTile * kRowBytes;  // bytes of a half tile
-  // half tiles in a warp's ring
-  static constexpr int kRing = kHalf == 2048 ? 8 : kHalf == 4096 ? 5 : kHalf == 8192 ? 6 : 3;
-  static constexpr int kCtas = kHalf == 2048 ? 3 : kHalf == 4096 ? 2 : 1;  // CTAs an SM holds
+  // half tiles in a ring, with a ring per warp
+  static constexpr int kRing = kHalf == 2048 ? 8 : kHalf == 4096 ? 5 : kHalf == 8192 ? (sizeof(T) == 4 ? 5 : 6) : 3;
   static constexpr int kSteps = kChunks / 2;       // matrix steps over D (32 bytes each)
   // the join of a CTA's warps goes through shared memory in pieces of 8 rows x kJoinCols
   static constexpr int kJoinCols = D < 128 ? D : 128;
@@ -206,18 +206,20 @@ __device__ __forceinline__ constexpr int swizzled(int r, int c) {
   return r * Shape<T, D>::kRowBytes + ((c ^ order<T>(r)) << 4);
 }
 
-template <typename T, int D, int NT>
+// NT: 8-row tiles of a warp.  RW: warps that share a ring, each with rows of its
+// own (4 / RW key groups).
+template <typename T, int D, int NT, int RW>
 struct Warp;
 
 // bf16: K and V fragments by ldmatrix, q fragments in registers.
-template <int D, int NT>
-struct Warp<__nv_bfloat16, D, NT> {
+template <int D, int NT, int RW>
+struct Warp<__nv_bfloat16, D, NT, RW> {
   using S = Shape<__nv_bfloat16, D>;
   static constexpr int kQSmem = 0;
   unsigned q[S::kSteps][NT][2];
   unsigned k_at[4], v_at[4];  // this lane's offsets in a half tile for steps 0-3; step + 4: 128 bytes on
 
-  __device__ __forceinline__ explicit Warp(int lane) {
+  __device__ __forceinline__ Warp(int lane, int) {
     const int rk = (lane & 7) + (lane >> 3 & 1) * 8, rv = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -226,12 +228,12 @@ struct Warp<__nv_bfloat16, D, NT> {
     }
   }
 
-  // row(n): q's row of column n of this warp's tile, or nullptr
+  // row(n): q's row of column n of the CTA's block, or nullptr; this warp's begin at row0
   template <typename F>
-  __device__ __forceinline__ void load_q(F row, void *, int lane) {
+  __device__ __forceinline__ void load_q(F row, void *, int lane, int row0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const __nv_bfloat16 *p = row(nt * 8 + lane / 4);
+      const __nv_bfloat16 *p = row(row0 + nt * 8 + lane / 4);
 #pragma unroll
       for (int ks = 0; ks < S::kSteps; ++ks) {
 #pragma unroll
@@ -306,14 +308,14 @@ struct Warp<__nv_bfloat16, D, NT> {
 // The tensor cores cut the low bits of a running sum at every product, so the
 // long sums are taken outside them: a product's sum starts at zero, over 32
 // elements of D (scores) or the tile's 16 keys (output), and is added in f32.
-template <int D, int NT>
-struct Warp<float, D, NT> {
+template <int D, int NT, int RW>
+struct Warp<float, D, NT, RW> {
   using S = Shape<float, D>;
   static constexpr int kQRow = 2 * D + 8;  // (hi, lo) pairs, padded
-  static constexpr int kQSmem = NT * 8 * kQRow * 4;
+  static constexpr int kQSmem = RW * NT * 8 * kQRow * 4;
   unsigned k_at[4], v_at[8], q_at;
 
-  __device__ __forceinline__ explicit Warp(int lane) {
+  __device__ __forceinline__ Warp(int lane, int row0) {
     const int rk = (lane & 7) + (lane >> 3 & 1) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) k_at[i] = swizzled<float, D>(rk, i * 2 + (lane >> 4));
@@ -321,13 +323,13 @@ struct Warp<float, D, NT> {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v_at[i] = swizzled<float, D>((i & 1) * 4 + (lane & 3), (i >> 1) * 2 + (lane >> 4)) + (lane >> 2 & 3) * 4;
-    q_at = (lane / 4) * kQRow + (lane & 3) * 2;
+    q_at = (row0 + lane / 4) * kQRow + (lane & 3) * 2;
   }
 
   template <typename F>
-  __device__ __forceinline__ void load_q(F row, void *q_smem, int) {
+  __device__ __forceinline__ void load_q(F row, void *q_smem, int, int) {
     uint2 *qs = static_cast<uint2 *>(q_smem);
-    for (int i = threadIdx.x; i < NT * 8 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < RW * NT * 8 * D; i += kThreads) {
       const float *p = row(i / D);
       const Tf32Pair x(p ? p[i % D] : 0.0f);
       qs[i / D * (kQRow / 2) + i % D] = make_uint2(x.hi, x.lo);
@@ -431,10 +433,16 @@ struct Warp<float, D, NT> {
   };
 };
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int RW>
 constexpr int smem_bytes() {
   using S = Shape<T, D>;
-  return kWarps * S::kRing * S::kHalf + S::kJoinBytes + Warp<T, D, NT>::kQSmem;
+  return kWarps * S::kRing * S::kHalf + S::kJoinBytes + Warp<T, D, NT, RW>::kQSmem;
+}
+// CTAs an SM holds: its shared memory, and registers enough for the accumulators
+template <typename T, int D, int NT, int RW>
+constexpr int ctas_per_sm() {
+  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW>() + 1024);  // + the static part
+  return by_smem > 3 ? 3 : by_smem;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -447,7 +455,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // One (request, key head, row block) item of a CTA's share, or the part of it
 // that lies in the share.
-template <int ROWS>
+template <int ROWS, int KW>
 struct Item {
   uint32_t seq;
   Request r;
@@ -471,27 +479,32 @@ struct Item {
     k1 = min(r.len, r.lo + tile1 * kUnit);
     return true;
   }
-  // Tiles of 16 keys of this part that `warp` takes: k0 + 16 (warp + 4 i).
-  __device__ __forceinline__ int tiles_of(int warp) const {
-    const int first = k0 + kTile * warp;
-    return first < k1 ? (k1 - first + kUnit - 1) / kUnit : 0;
+  // Tiles of 16 keys of this part that key group `kg` takes: k0 + 16 (kg + KW i).
+  __device__ __forceinline__ int tiles_of(int kg) const {
+    const int first = k0 + kTile * kg;
+    return first < k1 ? (k1 - first + kTile * KW - 1) / (kTile * KW) : 0;
   }
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
+template <typename T, int D, int NT, int RW>
+__global__ void __launch_bounds__(kThreads, (ctas_per_sm<T, D, NT, RW>())) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
   using S = Shape<T, D>;
-  using W = Warp<T, D, NT>;
-  constexpr int kRows = NT * 8;
-  static_assert(smem_bytes<T, D, NT>() <= 226 * 1024 / S::kCtas, "the CTAs of an SM share its memory");
+  using W = Warp<T, D, NT, RW>;
+  constexpr int kRows = RW * NT * 8;   // rows of a block
+  constexpr int KW = kWarps / RW;      // key groups
+  constexpr int kStep = kTile * KW;    // keys from a group's tile to its next
+  constexpr int kRing = S::kRing * RW;
+  static_assert(ctas_per_sm<T, D, NT, RW>() >= 1, "a CTA fits an SM's shared memory");
+  static_assert(kRing <= 32, "a bit per slot");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[kWarps], s_offset;
   __shared__ uint32_t s_seq;
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_m[kWarps][NT * 8], s_l[kWarps][NT * 8];
   __shared__ int s_bad[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned ring = smem_u32(smem) + warp * S::kRing * S::kHalf;
+  const int kg = warp / RW, rg = warp % RW, row0 = rg * NT * 8;  // key group; rows of the block
+  const unsigned ring = smem_u32(smem) + kg * kRing * S::kHalf;
   float *join = reinterpret_cast<float *>(smem + kWarps * S::kRing * S::kHalf);
   void *q_smem = smem + kWarps * S::kRing * S::kHalf + S::kJoinBytes;
 
@@ -545,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
 
   // The ring's feed runs ahead of the products, across items: `f` is the item
   // that the next half tile belongs to, `f_i` its tile.
-  Item<kRows> f;
+  Item<kRows, KW> f;
   f.seq = s_seq;
   f.in_seq = s_offset;
   f.r = request<kRows>(c, f.seq);
-  Item<kRows> it = f;
+  Item<kRows, KW> it = f;
   long long f_u = u0;
   int f_i = 0, f_n = 0, f_head = 0;
   unsigned f_slot = 0;
@@ -559,19 +572,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
   int page = 0;           // the page of the next tile (of this lane's row of it), looked up a tile ahead
   long long row_at = 0;   // byte offset of the tile's first row (of this lane's row; -1: zeros) in the caches
   constexpr int kPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;  // rows one access of the warp covers
-  const int my_row = S::kChunks >= 32 ? 0 : lane / S::kChunks, my_chunk = lane % S::kChunks;
+  constexpr int kAccesses = kTile * S::kChunks / 32 / RW;  // of this warp for a half tile
+  const int my_row = (S::kChunks >= 32 ? 0 : lane / S::kChunks) + rg * (kTile / RW), my_chunk = lane % S::kChunks;
   const long long slot_bytes = c.slot_stride * static_cast<int>(sizeof(T));
   const long long my_src = my_row * slot_bytes + my_chunk * 16;
   const unsigned my_dst = swizzled<T, D>(my_row, my_chunk);
   auto look_up = [&] {
-    const int key = f.k0 + kTile * warp + f_i * kUnit + (c.whole_tiles ? 0 : lane & 15);
+    const int key = f.k0 + kTile * kg + f_i * kStep + (c.whole_tiles ? 0 : lane & 15);
     page = key < f.k1 ? f_table[c.page_div.div(key)] : 0;
   };
-  auto next_item = [&] {  // to the next item in which this warp has a tile
+  auto next_item = [&] {  // to the next item in which this key group has a tile
     for (f_any = false; f.find(c, f_u, u1); ) {
       f_u += f.tile1 - f.tile0;
       f.in_seq += f.tile1 - f.tile0;
-      f_n = f.tiles_of(warp);
+      f_n = f.tiles_of(kg);
       if (f_n > 0) {
         f_any = true;
         f_i = 0;
@@ -589,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
       const unsigned to = ring + f_slot * S::kHalf;
       if (c.whole_tiles) {  // a tile lies in one page: rows past the end are another request's or stale, and cut out later
         if (!f_value) {
-          const int key = f.k0 + kTile * warp + f_i * kUnit;
+          const int key = f.k0 + kTile * kg + f_i * kStep;
           const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
           const bool none = static_cast<uint32_t>(page) >= c.n_pages;
           bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
@@ -598,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
         }
         const char *src = base + row_at + my_src;
 #pragma unroll
-        for (int x = 0; x < kTile * S::kChunks / 32; ++x) {
+        for (int x = 0; x < kAccesses; ++x) {
           const int row = x * 32 / S::kChunks;
           const unsigned dst = to + (my_dst ^ (order<T>(row) << 4)) + row * S::kRowBytes + (S::kChunks > 32 ? (x & 1) * 512 : 0);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src + (S::kChunks > 32 ? (x & 1) * 512 : 0)) : "memory");
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
         }
       } else {
         if (!f_value) {
-          const int key = f.k0 + kTile * warp + f_i * kUnit + (lane & 15);
+          const int key = f.k0 + kTile * kg + f_i * kStep + (lane & 15);
           const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
           const bool none = key < f.k1 && static_cast<uint32_t>(page) >= c.n_pages;
           bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
@@ -615,13 +629,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
                        : -1;
         }
 #pragma unroll 4
-        for (int x = 0; x < kTile * S::kChunks / 32; ++x) {
+        for (int x = rg * kAccesses; x < (rg + 1) * kAccesses; ++x) {
           const int row = (x * 32 + lane) / S::kChunks, ch = (x * 32 + lane) % S::kChunks;
           const long long off = __shfl_sync(kFull, row_at, row);
           cp_async_16_or_zero(to + swizzled<T, D>(row, ch), base + (off < 0 ? 0 : off) + ch * 16, off >= 0);
         }
       }
-      f_slot = f_slot + 1 == S::kRing ? 0 : f_slot + 1;
+      f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
       if (f_value) {
         if (++f_i < f_n) look_up();
         else next_item();
@@ -631,9 +645,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
     cp_async_commit();
   };
 #pragma unroll 1
-  for (int h = 0; h < S::kRing - 1; ++h) fetch();
+  for (int h = 0; h < kRing - 1; ++h) fetch();
+  // Before a half tile is used: its copies are there, for every warp of the group, and all of them are done with
+  // the one before, whose slot the next copies take.
+  auto arrived = [&] {
+    cp_async_wait<kRing - 2>();
+    if constexpr (RW == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + kg), "n"(32 * RW) : "memory");
+    fetch();
+  };
 
-  W w(lane);
+  W w(lane, row0);
   unsigned slot = 0;
   for (long long u = u0; it.find(c, u, u1);) {
     const Request &r = it.r;
@@ -648,19 +672,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
       return static_cast<const T *>(c.q) + static_cast<int64_t>(r.t0 + t) * c.q_stride +
              (static_cast<int64_t>(head) * c.group + (row - t * static_cast<int>(c.group))) * D;
     };
-    w.load_q(q_row, q_smem, lane);
+    w.load_q(q_row, q_smem, lane, row0);
     // the last key each of this lane's columns sees
     int last[NT][2], token[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = min(block * kRows + nt * 8 + (lane & 3) * 2 + j, rows - 1);
+        const int row = min(block * kRows + row0 + nt * 8 + (lane & 3) * 2 + j, rows - 1);
         token[nt][j] = c.group_div.div(row);
         last[nt][j] = r.len - r.tokens + token[nt][j];
       }
-    const int t_first = c.group_div.div(block * kRows), t_last = c.group_div.div(min(block * kRows + kRows, rows) - 1);
-    // keys in [all0, all1) are seen by every row of the block
+    const int t_first = c.group_div.div(min(block * kRows + row0, rows - 1));
+    const int t_last = c.group_div.div(min(block * kRows + row0 + NT * 8, rows) - 1);
+    // keys in [all0, all1) are seen by every row of this warp
     const int all1 = min(r.len - r.tokens + t_first + 1, it.k1);
     const int all0 = c.window ? r.len - r.tokens + t_last + 1 - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
     if (W::kQSmem) __syncthreads();
@@ -677,19 +702,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    const int n_tiles = it.tiles_of(warp);
-    int key0 = it.k0 + kTile * warp;
+    const int n_tiles = it.tiles_of(kg);
+    int key0 = it.k0 + kTile * kg;
     bool bad_page = false;
 #pragma unroll 1
-    for (int i = 0; i < n_tiles; ++i, key0 += kUnit) {
+    for (int i = 0; i < n_tiles; ++i, key0 += kStep) {
       // scores
-      fetch();
-      cp_async_wait<S::kRing - 1>();
-      __syncwarp();
+      arrived();
       float s[NT][4];
       w.scores(s, ring + slot * S::kHalf, q_smem);
       bad_page |= bad_slots >> slot & 1;
-      slot = slot + 1 == S::kRing ? 0 : slot + 1;
+      slot = slot + 1 == kRing ? 0 : slot + 1;
       const bool edge = key0 + kTile > all1 || key0 < all0;
       bool grown = false;
 #pragma unroll
@@ -744,12 +767,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
         }
       const typename W::P p(s, lane);
       // output
-      __syncwarp();
-      fetch();
-      cp_async_wait<S::kRing - 1>();
-      __syncwarp();
+      arrived();
       const unsigned v_tile = ring + slot * S::kHalf;
-      slot = slot + 1 == S::kRing ? 0 : slot + 1;
+      slot = slot + 1 == kRing ? 0 : slot + 1;
       if (!edge) {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
@@ -779,10 +799,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
           }
         }
       }
-      __syncwarp();
     }
 
-    // Join the four warps.
+    // Join the key groups.
     bad_page = __any_sync(kFull, bad_page);
     if (lane == 0) s_bad[warp] = bad_page;
 #pragma unroll
@@ -813,23 +832,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
         const bool poison = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];  // rows over a page that does not exist are NaN
         if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
 #pragma unroll 1
-        for (int x = tid; x < 8 * S::kJoinCols / 4; x += kThreads) {
-          const int row = x / (S::kJoinCols / 4), d = x % (S::kJoinCols / 4) * 4, n = nt * 8 + row;
-          const int item_row = block * kRows + n;
+        for (int x = tid; x < RW * 8 * S::kJoinCols / 4; x += kThreads) {
+          const int row = x / (S::kJoinCols / 4), d = x % (S::kJoinCols / 4) * 4;
+          const int of = row / 8, in = row % 8, m_row = nt * 8 + in;  // rows of warps of, of + RW, ...
+          const int n = of * NT * 8 + m_row, item_row = block * kRows + n;
           if (item_row >= rows) break;
-          float top = s_m[0][n];
+          float top = s_m[of][m_row];
 #pragma unroll
-          for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][n]);
+          for (int i = 1; i < KW; ++i) top = fmaxf(top, s_m[i * RW + of][m_row]);
           float sum[4] = {}, den = 0.0f;
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            const float g = exp2_fast(s_m[i][n] - top);
-            const float4 y = *reinterpret_cast<const float4 *>(join + (i * 8 + row) * S::kJoinRow + d);
+          for (int i = 0; i < KW; ++i) {
+            const float g = exp2_fast(s_m[i * RW + of][m_row] - top);
+            const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + of) * 8 + in) * S::kJoinRow + d);
             sum[0] += g * y.x;
             sum[1] += g * y.y;
             sum[2] += g * y.z;
             sum[3] += g * y.w;
-            den += g * s_l[i][n];
+            den += g * s_l[i * RW + of][m_row];
           }
           if (poison) den = NAN;
           if (whole) {
@@ -861,70 +881,116 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) gdn_attn_paged
 
 // ------------------------------------------------------------ the join
 
-// CTA (x, y): row y of the item that begins in main CTA x and goes on in later
-// ones.  Each warp takes every fourth of the item's parts.
-template <typename T, int D, int NT>
+// The item that begins in main CTA blockIdx.x and goes on in later ones: CTA (x, y)
+// joins its rows y * PER .. + PER, each by 8 / PER warps that take its parts in turn.
+template <typename T, int D, int ROWS, int PER>
 __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const __grid_constant__ Call c) {
-  constexpr int kRows = NT * 8, kPer = D / 32;
-  __shared__ float s_acc[kJoinWarps][D], s_den[kJoinWarps];
+  constexpr int kTeam = kJoinWarps / PER;  // warps of a row
+  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32, kAtOnce = 32 / kLanes, kVecs = D / 4 / kLanes;
+  __shared__ float s_weight[PER][kMostParts];
+  __shared__ float4 s_acc[kJoinWarps][D / 4];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 meta = c.meta[blockIdx.x];
   if (meta.w < 0) return;
-  const Request r = request<kRows>(c, meta.x);
+  const Request r = request<ROWS>(c, meta.x);
   const int head = meta.y / r.blocks, block = meta.y - head * r.blocks;
-  const int row = blockIdx.y, item_row = block * kRows + row;
-  if (item_row >= r.tokens * static_cast<int>(c.group)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / kTeam, member = warp % kTeam;
+  const int row = blockIdx.y * PER + mine, item_row = block * ROWS + row;
+  const bool real = item_row < r.tokens * static_cast<int>(c.group);
   const int x0 = blockIdx.x, n = meta.z - x0 + 1;
-  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? meta.w : 2 * (x0 + i)) * kRows + row; };
+  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? meta.w : 2 * (x0 + i)) * ROWS + row; };
 
-  float top = kLowest;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, c.part_ml[slot(i)].x);
+  // every part's weight 2^(m - top); each warp of the row finds top and the sum for itself
+  float top = kLowest, den = 0.0f;
+  if (real) {
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, c.part_ml[slot(i)].x);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-  float acc[kPer] = {}, den = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kJoinWarps) {
-    const float2 ml = c.part_ml[slot(i)];
-    const float f = exp2_fast(ml.x - top);
-    den += f * ml.y;
-    const float *src = c.part + slot(i) * D + lane;
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = c.part_ml[slot(i)];
+      const float f = exp2_fast(ml.x - top);
+      den += f * ml.y;
+      if (member == 0) s_weight[mine][i] = f;
+    }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) acc[j] += f * src[j * 32];
+    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(kFull, den, d);
   }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) s_acc[warp][j * 32 + lane] = acc[j];
-  if (lane == 0) s_den[warp] = den;
   __syncthreads();
-  den = 0.0f;
+  float4 acc[kVecs] = {};
+  if (real) {
+#pragma unroll 4
+    for (int i = member * kAtOnce + lane / kLanes; i < n; i += kTeam * kAtOnce) {
+      const float f = s_weight[mine][i];
+      const float4 *src = reinterpret_cast<const float4 *>(c.part + slot(i) * D) + lane % kLanes;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) den += s_den[w];
+      for (int j = 0; j < kVecs; ++j) {
+        const float4 y = src[j * 32];
+        acc[j].x += f * y.x;
+        acc[j].y += f * y.y;
+        acc[j].z += f * y.z;
+        acc[j].w += f * y.w;
+      }
+    }
+    if (kAtOnce == 2) {
+      acc[0].x += __shfl_xor_sync(kFull, acc[0].x, 16);
+      acc[0].y += __shfl_xor_sync(kFull, acc[0].y, 16);
+      acc[0].z += __shfl_xor_sync(kFull, acc[0].z, 16);
+      acc[0].w += __shfl_xor_sync(kFull, acc[0].w, 16);
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      if (lane < kLanes) s_acc[warp][j * 32 + lane] = acc[j];
+  }
+  __syncthreads();
+  if (!real) return;
   const int t = c.group_div.div(item_row);
   T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
          (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D;
-  const bool empty = r.len - r.tokens + t < 0;
-  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+  const bool empty = r.len - r.tokens + t < 0 && !isnan(den);
+  for (int d = member * 32 + lane; d < D; d += 32 * kTeam) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += s_acc[w][d];
-    Act<T>::put(o + d, empty && !isnan(den) ? 0.0f : sum / den);
+    for (int w = 0; w < kTeam; ++w) sum += reinterpret_cast<const float *>(s_acc[mine * kTeam + w])[d];
+    Act<T>::put(o + d, empty ? 0.0f : sum / den);
   }
 }
 
 // ------------------------------------------------------------ host
 
-int row_tiles(const gdn_attn_params &p) {
+// Rows that a request's newest tokens take per key head, on average: what the
+// shape of a call is chosen by (longer windows take several row blocks).
+uint64_t rows_of(const gdn_attn_params &p) {
   const uint64_t window = (p.n_tokens + static_cast<uint64_t>(p.n_seqs) - 1) / p.n_seqs;
-  return window * (p.n_q_heads / p.n_kv_heads) <= 8 ? 1 : 2;
+  return window * (p.n_q_heads / p.n_kv_heads);
 }
 
-// calls f(type, D, NT) with the call's compile-time values
+template <typename T, int D_, int NT_, int RW_>
+struct Pick {
+  using type = T;
+  static constexpr int D = D_, NT = NT_, RW = RW_, rows = NT_ * RW_ * 8, ctas = kSms * ctas_per_sm<T, D_, NT_, RW_>();
+};
+
+// Calls f with the Pick of the call: the fewest rows per block that hold its
+// rows.  A block of 8 costs what the cache's bytes cost; more rows raise the
+// work per byte, first on a warp's second tile, then on more warps per ring.
 template <typename F>
 auto dispatch(const gdn_attn_params &p, F f) {
+  const uint64_t rows = rows_of(p);
   auto by_rows = [&](auto t, auto d) {
-    // the rings and q of 16 rows do not fit an SM's shared memory at 1 KB per key
-    constexpr int most = sizeof(t) * d() >= 1024 ? 1 : 2;
-    return row_tiles(p) == 1 ? f(t, d, std::integral_constant<int, 1>{}) : f(t, d, std::integral_constant<int, most>{});
+    using T = decltype(t);
+    constexpr int D = d();
+    if constexpr (sizeof(T) * D >= 1024) {  // 1 KB per key: no room for more than 8 rows of q beside the rings
+      return f(Pick<T, D, 1, 1>{});
+    } else if constexpr (D == 256) {  // 16 columns' accumulators and q would not fit a thread's registers
+      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2>{}) : f(Pick<T, D, 1, 4>{});
+    } else if constexpr (sizeof(T) == 4) {
+      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
+    } else {
+      return rows <= 8    ? f(Pick<T, D, 1, 1>{})
+             : rows <= 16 ? f(Pick<T, D, 2, 1>{})
+             : rows <= 32 ? f(Pick<T, D, 2, 2>{})
+                          : f(Pick<T, D, 2, 4>{});
+    }
   };
   auto by_dim = [&](auto t) {
     return p.head_dim == 64    ? by_rows(t, std::integral_constant<int, 64>{})
@@ -939,10 +1005,10 @@ size_t part_floats(int ctas, int rows, int d) { return static_cast<size_t>(2) * 
 }  // namespace
 
 size_t attn_workspace_bytes(const gdn_attn_params &p) {
-  return dispatch(p, [&](auto t, auto d, auto nt) {
-    constexpr int ctas = kSms * Shape<decltype(t), d()>::kCtas;
-    return part_floats(ctas, nt() * 8, d()) * 4 + static_cast<size_t>(2) * ctas * nt() * 8 * sizeof(float2) +
-           ctas * sizeof(int4);
+  return dispatch(p, [&](auto pick) {
+    using P = decltype(pick);
+    return part_floats(P::ctas, P::rows, P::D) * 4 + static_cast<size_t>(2) * P::ctas * P::rows * sizeof(float2) +
+           P::ctas * sizeof(int4);
   });
 }
 
@@ -973,21 +1039,25 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   c.page_div = FastDiv(p.page_size);
   c.group_div = FastDiv(c.group);
   c.whole_tiles = p.page_size % kTile == 0;
-  return dispatch(p, [&](auto t, auto d, auto nt) {
-    using T = decltype(t);
-    constexpr int D = d(), NT = nt(), ctas = kSms * Shape<T, D>::kCtas, smem = smem_bytes<T, D, NT>();
-    // widest alignment first: sums, (maximum, sum) pairs, item records
+  return dispatch(p, [&](auto pick) {
+    using P = decltype(pick);
+    using T = typename P::type;
+    constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW>();
+    static_assert(P::ctas <= kMostParts, "a part per CTA");
     c.meta = static_cast<int4 *>(a.workspace);
-    c.part = reinterpret_cast<float *>(c.meta + ctas);
-    c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(ctas, NT * 8, D));
-    cudaError_t e = cudaFuncSetAttribute(gdn_attn_paged_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    c.part = reinterpret_cast<float *>(c.meta + P::ctas);
+    c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
+    const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW>;
+    cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    gdn_attn_paged_kernel<T, D, NT><<<ctas, kThreads, smem, stream>>>(c);
+    main<<<P::ctas, kThreads, smem, stream>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // The join may be set up while the main kernel still runs; it waits for its end before it reads.
+    // The join may be set up while the main kernel still runs; it waits for its end before it reads.  Few items
+    // have many parts each: a CTA per row; many have few: a warp per row.
+    const bool few = static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, NT * 8);
+    cfg.gridDim = dim3(P::ctas, few ? P::rows : P::rows / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -995,7 +1065,8 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_attn_join_kernel<T, D, NT>, static_cast<const Call>(c));
+    return cudaLaunchKernelEx(&cfg, few ? gdn_attn_join_kernel<T, P::D, P::rows, 1> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
+                              static_cast<const Call>(c));
   });
 }
 
