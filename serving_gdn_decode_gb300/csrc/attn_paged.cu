@@ -48,10 +48,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;               // keys per warp tile
-constexpr int kUnit = kTile * kWarps;   // keys per unit of work
+constexpr int kTile = 16;  // keys per tile
+constexpr int kUnit = 64;  // keys per unit of work
 constexpr int kSms = 152;
 constexpr int kJoinWarps = 8;
 constexpr int kMostParts = kSms * 3;  // CTAs of the main kernel
@@ -74,33 +72,30 @@ __device__ __forceinline__ void ldmatrix_x4_trans(unsigned (&r)[4], unsigned add
 }
 __device__ __forceinline__ unsigned movmatrix_trans(unsigned x) {
   unsigned y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
 // c += a (16 x 16) b (16 x 8), bf16
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // c += a (16 x 8) b (8 x 8), TF32
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ unsigned to_tf32(float x) {
-  unsigned y;
-  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(y) : "f"(x));
-  return y;
-}
-// x = hi + lo up to 2^-22 |x|, both TF32, rounded to nearest.
+// x = hi + lo up to 2^-21 |x|, both with TF32's 10 mantissa bits: hi is x rounded to nearest (a carry into the
+// exponent is the next binade), lo the exact rest with its low bits cut, which leans to neither side since the
+// rest has either sign.  A NaN that the carry turns into a zero in hi stays in lo.
 struct Tf32Pair {
   unsigned hi, lo;
   __device__ __forceinline__ explicit Tf32Pair(float x) {
-    hi = to_tf32(x);
-    lo = to_tf32(x - __uint_as_float(hi));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
   }
 };
 
@@ -182,13 +177,12 @@ struct Shape {
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
   static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
   static constexpr int kHalf = kTile * kRowBytes;  // bytes of a half tile
-  // half tiles in a ring, with a ring per warp
-  static constexpr int kRing = kHalf == 2048 ? 8 : kHalf == 4096 ? 5 : kHalf == 8192 ? (sizeof(T) == 4 ? 5 : 6) : 3;
+  // half tiles in a CTA's rings together
+  static constexpr int kSlots = kHalf == 2048 ? 32 : kHalf == 4096 ? (sizeof(T) == 4 ? 12 : 20) : kHalf == 8192 ? (sizeof(T) == 4 ? 20 : 24) : 12;
   static constexpr int kSteps = kChunks / 2;       // matrix steps over D (32 bytes each)
   // the join of a CTA's warps goes through shared memory in pieces of 8 rows x kJoinCols
   static constexpr int kJoinCols = D < 128 ? D : 128;
   static constexpr int kJoinRow = kJoinCols + 4;  // padded: a fragment's rows fall on different banks
-  static constexpr int kJoinBytes = kWarps * 8 * kJoinRow * 4;
 };
 
 // A half tile in shared memory: row r's chunk c lies at r * kRowBytes +
@@ -207,7 +201,7 @@ __device__ __forceinline__ constexpr int swizzled(int r, int c) {
 }
 
 // NT: 8-row tiles of a warp.  RW: warps that share a ring, each with rows of its
-// own (4 / RW key groups).
+// own.  A CTA has WARPS warps, WARPS / RW key groups with a ring each.
 template <typename T, int D, int NT, int RW>
 struct Warp;
 
@@ -243,24 +237,28 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
     }
   }
 
-  // s = K Q^T of the tile's 16 keys; two chains of products, for their latency
+  // s = K Q^T of the tile's 16 keys; several chains of products, for their latency
   __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile, const void *) const {
-    float t[NT][4];
+    constexpr int kChains = NT == 1 ? 4 : 2;
+    float t[kChains][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < kChains; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = t[nt][j] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) t[i][nt][0] = t[i][nt][1] = t[i][nt][2] = t[i][nt][3] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < S::kSteps; ++ks) {
       unsigned a[4];
       ldmatrix_x4(a, k_tile + k_at[ks & 3] + (ks >> 2) * 128);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? t[nt] : s[nt], a, q[ks][nt][0], q[ks][nt][1]);
+      for (int nt = 0; nt < NT; ++nt) mma_bf16(t[ks % kChains][nt], a, q[ks][nt][0], q[ks][nt][1]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j];
+      for (int j = 0; j < 4; ++j) {
+        s[nt][j] = t[0][nt][j] + t[1][nt][j];
+        if (kChains == 4) s[nt][j] += t[kChains - 2][nt][j] + t[kChains - 1][nt][j];
+      }
   }
 
   // The B fragments of P^T from the score tile's layout: hi and lo halves.
@@ -329,7 +327,7 @@ struct Warp<float, D, NT, RW> {
   template <typename F>
   __device__ __forceinline__ void load_q(F row, void *q_smem, int, int) {
     uint2 *qs = static_cast<uint2 *>(q_smem);
-    for (int i = threadIdx.x; i < RW * NT * 8 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < RW * NT * 8 * D; i += blockDim.x) {
       const float *p = row(i / D);
       const Tf32Pair x(p ? p[i % D] : 0.0f);
       qs[i / D * (kQRow / 2) + i % D] = make_uint2(x.hi, x.lo);
@@ -433,15 +431,18 @@ struct Warp<float, D, NT, RW> {
   };
 };
 
-template <typename T, int D, int NT, int RW>
+template <typename T, int D, int WARPS>
+constexpr int join_bytes() {
+  return WARPS * 8 * Shape<T, D>::kJoinRow * 4;
+}
+template <typename T, int D, int NT, int RW, int WARPS>
 constexpr int smem_bytes() {
-  using S = Shape<T, D>;
-  return kWarps * S::kRing * S::kHalf + S::kJoinBytes + Warp<T, D, NT, RW>::kQSmem;
+  return Shape<T, D>::kSlots * Shape<T, D>::kHalf + join_bytes<T, D, WARPS>() + Warp<T, D, NT, RW>::kQSmem;
 }
 // CTAs an SM holds: its shared memory, and registers enough for the accumulators
-template <typename T, int D, int NT, int RW>
+template <typename T, int D, int NT, int RW, int WARPS>
 constexpr int ctas_per_sm() {
-  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW>() + 1024);  // + the static part
+  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW, WARPS>() + 1024);  // + the static part
   return by_smem > 3 ? 3 : by_smem;
 }
 
@@ -486,27 +487,29 @@ struct Item {
   }
 };
 
-template <typename T, int D, int NT, int RW>
-__global__ void __launch_bounds__(kThreads, (ctas_per_sm<T, D, NT, RW>())) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
+template <typename T, int D, int NT, int RW, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>())) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
   using S = Shape<T, D>;
   using W = Warp<T, D, NT, RW>;
   constexpr int kRows = RW * NT * 8;   // rows of a block
-  constexpr int KW = kWarps / RW;      // key groups
+  constexpr int KW = WARPS / RW;       // key groups
+  constexpr int kThreads = 32 * WARPS;
   constexpr int kStep = kTile * KW;    // keys from a group's tile to its next
-  constexpr int kRing = S::kRing * RW;
-  static_assert(ctas_per_sm<T, D, NT, RW>() >= 1, "a CTA fits an SM's shared memory");
+  constexpr int kRing = S::kSlots / KW;
+  static_assert(kUnit % kStep == 0, "a unit is the same number of tiles to every group");
+  static_assert(ctas_per_sm<T, D, NT, RW, WARPS>() >= 1, "a CTA fits an SM's shared memory");
   static_assert(kRing <= 32, "a bit per slot");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kWarps], s_offset;
+  __shared__ long long s_scan[WARPS], s_offset;
   __shared__ uint32_t s_seq;
-  __shared__ float s_m[kWarps][NT * 8], s_l[kWarps][NT * 8];
-  __shared__ int s_bad[kWarps];
+  __shared__ float s_m[WARPS][NT * 8], s_l[WARPS][NT * 8];
+  __shared__ int s_bad[WARPS];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kg = warp / RW, rg = warp % RW, row0 = rg * NT * 8;  // key group; rows of the block
   const unsigned ring = smem_u32(smem) + kg * kRing * S::kHalf;
-  float *join = reinterpret_cast<float *>(smem + kWarps * S::kRing * S::kHalf);
-  void *q_smem = smem + kWarps * S::kRing * S::kHalf + S::kJoinBytes;
+  float *join = reinterpret_cast<float *>(smem + S::kSlots * S::kHalf);
+  void *q_smem = smem + S::kSlots * S::kHalf + join_bytes<T, D, WARPS>();
 
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<T, D, NT, RW>())) gdn_a
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
@@ -829,7 +832,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<T, D, NT, RW>())) gdn_a
           for (int j = 0; j < 4; ++j)
             join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * S::kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
         __syncthreads();
-        const bool poison = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];  // rows over a page that does not exist are NaN
+        bool poison = false;  // rows over a page that does not exist are NaN
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) poison |= s_bad[i] != 0;
         if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
 #pragma unroll 1
         for (int x = tid; x < RW * 8 * S::kJoinCols / 4; x += kThreads) {
@@ -964,10 +969,11 @@ uint64_t rows_of(const gdn_attn_params &p) {
   return window * (p.n_q_heads / p.n_kv_heads);
 }
 
-template <typename T, int D_, int NT_, int RW_>
+template <typename T, int D_, int NT_, int RW_, int WARPS_ = 4>
 struct Pick {
   using type = T;
-  static constexpr int D = D_, NT = NT_, RW = RW_, rows = NT_ * RW_ * 8, ctas = kSms * ctas_per_sm<T, D_, NT_, RW_>();
+  static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, rows = NT_ * RW_ * 8;
+  static constexpr int ctas = kSms * ctas_per_sm<T, D_, NT_, RW_, WARPS_>();
 };
 
 // Calls f with the Pick of the call: the fewest rows per block that hold its
@@ -982,7 +988,7 @@ auto dispatch(const gdn_attn_params &p, F f) {
     if constexpr (sizeof(T) * D >= 1024) {  // 1 KB per key: no room for more than 8 rows of q beside the rings
       return f(Pick<T, D, 1, 1>{});
     } else if constexpr (D == 256) {  // 16 columns' accumulators and q would not fit a thread's registers
-      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2>{}) : f(Pick<T, D, 1, 4>{});
+      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8>{});
     } else if constexpr (sizeof(T) == 4) {
       return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
     } else {
@@ -1042,15 +1048,15 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   return dispatch(p, [&](auto pick) {
     using P = decltype(pick);
     using T = typename P::type;
-    constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW>();
+    constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW, P::WARPS>();
     static_assert(P::ctas <= kMostParts, "a part per CTA");
     c.meta = static_cast<int4 *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.meta + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
-    const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW>;
+    const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW, P::WARPS>;
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    main<<<P::ctas, kThreads, smem, stream>>>(c);
+    main<<<P::ctas, 32 * P::WARPS, smem, stream>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // The join may be set up while the main kernel still runs; it waits for its end before it reads.  Few items
