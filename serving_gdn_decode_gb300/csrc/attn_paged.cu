@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kTile = 16;  // keys per tile
 constexpr int kUnit = 64;  // keys per unit of work
+constexpr int kItemUnits = 2;  // what an item's begin and end cost beside its keys, in units
 constexpr int kSms = 152;
 constexpr int kJoinWarps = 8;
 constexpr int kMostParts = kSms * 3;  // CTAs of the main kernel
@@ -125,10 +126,10 @@ struct Request {
   int t0, tokens;   // its rows of q
   int len, lo;      // its keys: those that at least one token sees lie in [lo, len)
   int blocks;       // row blocks per key head
-  int tiles;        // units per (key head, row block); 1 when there is no key
+  int tiles;        // units of keys per (key head, row block); 1 when there is no key
   bool bad;
   __device__ __forceinline__ long long units(const Call &c) const {
-    return tokens > 0 ? static_cast<long long>(c.n_kv) * blocks * tiles : 0;
+    return tokens > 0 ? static_cast<long long>(c.n_kv) * blocks * (tiles + kItemUnits) : 0;
   }
 };
 
@@ -460,25 +461,39 @@ template <int ROWS, int KW>
 struct Item {
   uint32_t seq;
   Request r;
-  long long in_seq;      // units of the request before the item's part
+  long long in_seq;      // units of the request before the share's next one
   int item;              // head * r.blocks + block
-  int tile0, tile1;      // its units
+  int units;             // of the item in this share
+  int tile0, tile1;      // its units of keys
   int k0, k1;            // its keys
 
-  // Whether [u, u1) begins with an item; the request at or after `seq` that holds unit in_seq.
-  __device__ __forceinline__ bool find(const Call &c, long long u, long long u1) {
-    if (u >= u1) return false;
-    while (in_seq >= r.units(c)) {
-      in_seq = 0;
-      if (++seq >= c.n_seqs) return false;
-      r = request<ROWS>(c, seq);
+  // The next part of the share: [u, u1) are the share's units still to come, the first of them unit in_seq of
+  // request seq.  An item's first kItemUnits units hold no keys.
+  __device__ __forceinline__ bool find(const Call &c, long long &u, long long u1) {
+    while (u < u1) {
+      while (in_seq >= r.units(c)) {
+        in_seq = 0;
+        if (++seq >= c.n_seqs) return false;
+        r = request<ROWS>(c, seq);
+      }
+      const int all = r.tiles + kItemUnits;
+      item = static_cast<int>(in_seq / all);
+      const int at = static_cast<int>(in_seq - static_cast<long long>(item) * all);
+      units = static_cast<int>(min(static_cast<long long>(all - at), u1 - u));
+      tile0 = max(0, at - kItemUnits);
+      tile1 = at + units - kItemUnits;
+      if (tile1 > tile0) {
+        k0 = r.lo + tile0 * kUnit;
+        k1 = min(r.len, r.lo + tile1 * kUnit);
+        return true;
+      }
+      pass(u);
     }
-    item = static_cast<int>(in_seq / r.tiles);
-    tile0 = static_cast<int>(in_seq - static_cast<long long>(item) * r.tiles);
-    tile1 = static_cast<int>(min(static_cast<long long>(r.tiles), tile0 + (u1 - u)));
-    k0 = r.lo + tile0 * kUnit;
-    k1 = min(r.len, r.lo + tile1 * kUnit);
-    return true;
+    return false;
+  }
+  __device__ __forceinline__ void pass(long long &u) {
+    u += units;
+    in_seq += units;
   }
   // Tiles of 16 keys of this part that key group `kg` takes: k0 + 16 (kg + KW i).
   __device__ __forceinline__ int tiles_of(int kg) const {
@@ -586,8 +601,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
   };
   auto next_item = [&] {  // to the next item in which this key group has a tile
     for (f_any = false; f.find(c, f_u, u1); ) {
-      f_u += f.tile1 - f.tile0;
-      f.in_seq += f.tile1 - f.tile0;
+      f.pass(f_u);
       f_n = f.tiles_of(kg);
       if (f_n > 0) {
         f_any = true;
@@ -821,7 +835,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
         }
       }
     const bool whole = it.tile0 == 0 && it.tile1 == r.tiles;
-    const int part_slot = 2 * cta + (u == u0 ? 0 : 1);
+    const int part_slot = 2 * cta + (u == u0 ? 0 : 1);  // an item that goes on from the CTA before is the share's first
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -875,11 +889,10 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
       }
     }
     if (!whole && it.tile0 == 0 && tid == 0) {
-      const long long end = u + r.tiles - 1;  // the item's last unit
+      const long long end = u + it.units + (r.tiles - it.tile1) - 1;  // the item's last unit
       c.meta[cta] = make_int4(static_cast<int>(it.seq), it.item, static_cast<int>(((end + 1) * ctas - 1) / total), part_slot);
     }
-    u += it.tile1 - it.tile0;
-    it.in_seq += it.tile1 - it.tile0;
+    it.pass(u);
   }
   cp_async_wait<0>();
 }
