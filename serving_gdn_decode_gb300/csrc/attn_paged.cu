@@ -53,7 +53,7 @@ constexpr int kUnit = 64;  // keys per unit of work
 constexpr int kItemUnits = 2;  // what an item's begin and end cost beside its keys, in units
 constexpr int kSms = 152;
 constexpr int kJoinWarps = 8;
-constexpr int kMostParts = kSms * 3;  // CTAs of the main kernel
+
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite f32
@@ -107,13 +107,24 @@ __device__ __forceinline__ void cp_async_16_or_zero(unsigned smem, const void *g
 
 // ------------------------------------------------------------ the call, as the kernels see it
 
+// An item that begins in one CTA and goes on in later ones: what the join needs to know of it.
+struct alignas(16) Split {
+  int slot;      // of its first part; -1: no item is split here
+  int last;      // the last CTA that has a part of it
+  int row0, rows;  // its first row, and the rows of its key head: row = token * group + query head
+  int t0;        // the request's first row of q
+  int head0;     // its key head's first query head
+  int before;    // keys that are before the request's window of tokens; below 0, its first tokens see none
+  int unused;
+};
+
 struct Call {
   const void *q, *k, *v;
   const int32_t *table, *kv_lens, *token_start;
   void *out;
   float *part;     // [2 * ctas][rows][D] unnormalised sums
   float2 *part_ml; // [2 * ctas][rows] running maximum (log2 domain) and sum
-  int4 *meta;      // [ctas] the split item that begins in the CTA: request, head and row block, last CTA, slot of its part (-1: none)
+  Split *splits;   // [ctas] the split item that begins in the CTA
   uint32_t n_seqs, n_tokens, n_kv, group, max_pages, page_size, n_pages, window;
   float scale_log2;
   int64_t q_stride, out_stride, page_stride, head_stride, slot_stride;
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
   if (bad && blockIdx.x == 0) report(GDN_DEVICE_BAD_REQUEST);
   const int ctas = static_cast<int>(min(total, static_cast<long long>(gridDim.x)));
   const int cta = blockIdx.x;
-  if (tid == 0) c.meta[cta] = make_int4(0, 0, 0, -1);
+  if (tid == 0) c.splits[cta].slot = -1;
   if (cta >= ctas) return;
   const long long u0 = share_start(total, ctas, cta), u1 = share_start(total, ctas, cta + 1);
   if (u0 >= before && u0 < before + mine) {
@@ -890,7 +901,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
     }
     if (!whole && it.tile0 == 0 && tid == 0) {
       const long long end = u + it.units + (r.tiles - it.tile1) - 1;  // the item's last unit
-      c.meta[cta] = make_int4(static_cast<int>(it.seq), it.item, static_cast<int>(((end + 1) * ctas - 1) / total), part_slot);
+      c.splits[cta] = Split{part_slot, static_cast<int>(((end + 1) * ctas - 1) / total), block * kRows, rows, r.t0,
+                            head * static_cast<int>(c.group), r.len - r.tokens, 0};
     }
     it.pass(u);
   }
@@ -900,75 +912,77 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
 // ------------------------------------------------------------ the join
 
 // The item that begins in main CTA blockIdx.x and goes on in later ones: CTA (x, y)
-// joins its rows y * PER .. + PER, each by 8 / PER warps that take its parts in turn.
+// joins its rows y * PER .. + PER, each by 8 / PER warps that take its parts in
+// turn, a part by D / 4 lanes.
 template <typename T, int D, int ROWS, int PER>
 __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const __grid_constant__ Call c) {
-  constexpr int kTeam = kJoinWarps / PER;  // warps of a row
-  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32, kAtOnce = 32 / kLanes, kVecs = D / 4 / kLanes;
-  __shared__ float s_weight[PER][kMostParts];
-  __shared__ float4 s_acc[kJoinWarps][D / 4];
+  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32, kVecs = D / 4 / kLanes;
+  constexpr int kTeams = kJoinWarps * (32 / kLanes), kTeam = kTeams / PER;  // groups of lanes: in all, of a row
+  constexpr int kAhead = 8;                                                 // parts a group has on their way
+  __shared__ float4 s_acc[kTeams][D / 4];
+  __shared__ float s_m[kTeams], s_den[kTeams];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int4 meta = c.meta[blockIdx.x];
-  if (meta.w < 0) return;
-  const Request r = request<ROWS>(c, meta.x);
-  const int head = meta.y / r.blocks, block = meta.y - head * r.blocks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / kTeam, member = warp % kTeam;
-  const int row = blockIdx.y * PER + mine, item_row = block * ROWS + row;
-  const bool real = item_row < r.tokens * static_cast<int>(c.group);
-  const int x0 = blockIdx.x, n = meta.z - x0 + 1;
-  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? meta.w : 2 * (x0 + i)) * ROWS + row; };
-
-  // every part's weight 2^(m - top); each warp of the row finds top and the sum for itself
-  float top = kLowest, den = 0.0f;
-  if (real) {
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, c.part_ml[slot(i)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = c.part_ml[slot(i)];
-      const float f = exp2_fast(ml.x - top);
-      den += f * ml.y;
-      if (member == 0) s_weight[mine][i] = f;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(kFull, den, d);
-  }
-  __syncthreads();
+  const Split sp = c.splits[blockIdx.x];
+  if (sp.slot < 0) return;
+  const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, mine = team / kTeam, member = team % kTeam;
+  const int row = blockIdx.y * PER + mine, item_row = sp.row0 + row;
+  const int x0 = blockIdx.x, n = sp.last - x0 + 1;
   float4 acc[kVecs] = {};
-  if (real) {
-#pragma unroll 4
-    for (int i = member * kAtOnce + lane / kLanes; i < n; i += kTeam * kAtOnce) {
-      const float f = s_weight[mine][i];
-      const float4 *src = reinterpret_cast<const float4 *>(c.part + slot(i) * D) + lane % kLanes;
+  float m = kLowest, den = 0.0f;
+  for (int i0 = member; i0 < n; i0 += kTeam * kAhead) {
+    float2 ml[kAhead];
+    float4 y[kAhead][kVecs];
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const float4 y = src[j * 32];
-        acc[j].x += f * y.x;
-        acc[j].y += f * y.y;
-        acc[j].z += f * y.z;
-        acc[j].w += f * y.w;
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * kTeam;
+      if (i < n && item_row < sp.rows) {
+        const size_t at = static_cast<size_t>(i == 0 ? sp.slot : 2 * (x0 + i)) * ROWS + row;
+        ml[a] = c.part_ml[at];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) y[a][j] = *(reinterpret_cast<const float4 *>(c.part + at * D) + j * kLanes + lane);
+      } else {
+        ml[a] = make_float2(kLowest, 0.0f);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) y[a][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
-    if (kAtOnce == 2) {
-      acc[0].x += __shfl_xor_sync(kFull, acc[0].x, 16);
-      acc[0].y += __shfl_xor_sync(kFull, acc[0].y, 16);
-      acc[0].z += __shfl_xor_sync(kFull, acc[0].z, 16);
-      acc[0].w += __shfl_xor_sync(kFull, acc[0].w, 16);
-    }
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      if (lane < kLanes) s_acc[warp][j * 32 + lane] = acc[j];
+    for (int a = 0; a < kAhead; ++a) {
+      const float top = fmaxf(m, ml[a].x), f = exp2_fast(ml[a].x - top), g = exp2_fast(m - top);
+      den = den * g + f * ml[a].y;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        acc[j].x = acc[j].x * g + f * y[a][j].x;
+        acc[j].y = acc[j].y * g + f * y[a][j].y;
+        acc[j].z = acc[j].z * g + f * y[a][j].z;
+        acc[j].w = acc[j].w * g + f * y[a][j].w;
+      }
+      m = top;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) s_acc[team][j * kLanes + lane] = acc[j];
+  if (lane == 0) {
+    s_m[team] = m;
+    s_den[team] = den;
   }
   __syncthreads();
-  if (!real) return;
+  if (item_row >= sp.rows) return;
+  float top = kLowest;
+#pragma unroll
+  for (int w = 0; w < kTeam; ++w) top = fmaxf(top, s_m[mine * kTeam + w]);
+  den = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kTeam; ++w) den += exp2_fast(s_m[mine * kTeam + w] - top) * s_den[mine * kTeam + w];
   const int t = c.group_div.div(item_row);
-  T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
-         (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D;
-  const bool empty = r.len - r.tokens + t < 0 && !isnan(den);
-  for (int d = member * 32 + lane; d < D; d += 32 * kTeam) {
+  T *o = static_cast<T *>(c.out) + static_cast<int64_t>(sp.t0 + t) * c.out_stride +
+         static_cast<int64_t>(sp.head0 + (item_row - t * static_cast<int>(c.group))) * D;
+  const bool empty = sp.before + t < 0 && !isnan(den);
+  for (int d = member * kLanes + lane; d < D; d += kLanes * kTeam) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kTeam; ++w) sum += reinterpret_cast<const float *>(s_acc[mine * kTeam + w])[d];
+    for (int w = 0; w < kTeam; ++w)
+      sum += exp2_fast(s_m[mine * kTeam + w] - top) * reinterpret_cast<const float *>(s_acc[mine * kTeam + w])[d];
     Act<T>::put(o + d, empty ? 0.0f : sum / den);
   }
 }
@@ -1027,7 +1041,7 @@ size_t attn_workspace_bytes(const gdn_attn_params &p) {
   return dispatch(p, [&](auto pick) {
     using P = decltype(pick);
     return part_floats(P::ctas, P::rows, P::D) * 4 + static_cast<size_t>(2) * P::ctas * P::rows * sizeof(float2) +
-           P::ctas * sizeof(int4);
+           P::ctas * sizeof(Split);
   });
 }
 
@@ -1062,9 +1076,8 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     using P = decltype(pick);
     using T = typename P::type;
     constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW, P::WARPS>();
-    static_assert(P::ctas <= kMostParts, "a part per CTA");
-    c.meta = static_cast<int4 *>(a.workspace);
-    c.part = reinterpret_cast<float *>(c.meta + P::ctas);
+    c.splits = static_cast<Split *>(a.workspace);
+    c.part = reinterpret_cast<float *>(c.splits + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
     const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW, P::WARPS>;
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
