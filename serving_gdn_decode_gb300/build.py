@@ -1,8 +1,10 @@
-"""Build libgdn_gb300.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libgdn_gb300.so (the C-ABI library) in-tree with nvcc for sm_103a,
+and the compiled torch binding of the full-attention operators beside it.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
 shared library next to this file.  ptxas register/spill reports go to
-``_build/ptxas.log``.  Run as ``python -m serving_gdn_decode_gb300.build``.
+``_build/ptxas.log``.  ``csrc/paged_binding.cpp`` compiles with g++ against the
+installed torch's headers.  Run as ``python -m serving_gdn_decode_gb300.build``.
 """
 from __future__ import annotations
 
@@ -12,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libgdn_gb300.so")
+BINDING = os.path.join(HERE, "_paged_binding.so")
+BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -40,13 +45,13 @@ def _sources() -> list[str]:
 def _deps() -> list[str]:
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "gdn.h"),
-                                                         os.path.abspath(__file__)]
+                                                         os.path.abspath(__file__), BINDING_SRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -59,13 +64,47 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _torch_root() -> str:
+    import importlib.util
+    spec = importlib.util.find_spec("torch")  # its place only: importing it takes seconds
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the binding of the full-attention operators needs its headers")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _compile_binding() -> str:
+    root = _torch_root()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "paged_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-I", os.path.join(ROOT, "include"), "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    libs = os.path.join(_torch_root(), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-L", libs, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
+        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"==== {os.path.basename(src)}\n{log}\n")
@@ -75,6 +114,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         print(f"built {LIB}")
     return LIB

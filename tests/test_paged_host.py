@@ -252,71 +252,97 @@ def test_attn_workspace_size(L):
 # ------------------------------------------------------------------ the torch binding
 
 
-def test_binding_refuses_before_calling():
+def shapes(op):
+    """Arguments of a call that is right but for being on the host: refused as such, after every other check."""
+    import torch
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    if op == "kv_plan":
+        return dict(ctx_lens=i(2), new_lens=i(2), owned=i(2), free_pages=i(4), n_free=i(1), block_table=i(2, 3),
+                    page_size=8, n_pages=5, kv_lens=i(2), owned_out=i(2), n_free_out=i(1), token_start=i(3),
+                    slot_map=i(7), positions=i(7))
+    f = torch.zeros
+    if op == "rope":
+        return dict(q=f(2, 4, 64), k=f(2, 1, 64), positions=i(3, 2), cos_sin=f(9, 32), q_out=f(2, 4, 64),
+                    k_out=f(2, 1, 64), axes=[0, 2] * 8)
+    if op == "rope_store":
+        return dict(q=f(2, 4, 64), k=f(2, 2, 64), v=f(2, 2, 64), positions=i(2), cos_sin=f(9, 64), slot_map=i(2),
+                    k_cache=f(5, 2, 8, 64), v_cache=f(5, 2, 8, 64), q_out=f(2, 4, 64))
+    return dict(q=f(2, 4, 64), k_cache=f(5, 2, 8, 64), v_cache=f(5, 2, 8, 64), block_table=i(2, 3), kv_lens=i(2),
+                token_start=i(3), output=f(2, 4, 64), workspace=f(10))
+
+
+def call(op, **change):
+    import serving_gdn_decode_gb300 as gdn
+    a = shapes(op)
+    a.update(change)
+    return getattr(gdn, "gdn_" + op)(**a)
+
+
+@pytest.mark.parametrize("op", ["kv_plan", "rope", "rope_store", "attn_paged"])
+def test_binding_takes_cuda_tensors_only(L, op):
+    import torch
+    with pytest.raises(nat.GdnError, match="must be a CUDA tensor") as e:
+        call(op)
+    assert e.value.status == nat.GDN_ERR_INVALID_ARGUMENT
+    for name, x in shapes(op).items():
+        if isinstance(x, torch.Tensor):
+            with pytest.raises(TypeError, match=name):
+                call(op, **{name: [1, 2]})
+            with pytest.raises(nat.GdnError, match=name):
+                call(op, **{name: x.to(torch.float64) if name != "workspace" else torch.zeros(4, 4).t()[::2]})
+
+
+def test_binding_shape_rules(L):
+    import torch
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    f = torch.zeros
+
+    def refuse(op, text, **change):
+        with pytest.raises(nat.GdnError, match=text):
+            call(op, **change)
+
+    refuse("kv_plan", "new_lens", new_lens=i(3))
+    refuse("kv_plan", "block_table", block_table=i(6))
+    refuse("kv_plan", "block_table", block_table=i(3, 2).t())
+    refuse("kv_plan", "token_start", token_start=i(2))
+    refuse("kv_plan", "positions", positions=i(6))
+    refuse("kv_plan", "n_free", n_free=i(2))
+    refuse("kv_plan", "page_size", page_size=-1)
+    refuse("rope", "k must", k=f(3, 1, 64))
+    refuse("rope", "k must", k=f(2, 64))
+    refuse("rope", "q must", q=f(2, 64, 4).transpose(1, 2))
+    refuse("rope", "q_out", q_out=f(2, 3, 64))
+    refuse("rope", "k_out", k_out=f(2, 1, 64).bfloat16())
+    refuse("rope", "positions", positions=i(3, 1))
+    refuse("rope", "positions", positions=i(2, 3).t())
+    refuse("rope", "cos_sin", cos_sin=f(32, 9).t())
+    refuse("rope", "axes has 3", axes=bytes(3))
+    refuse("rope_store", "slot_map", slot_map=i(3))
+    refuse("rope_store", "v must", v=f(2, 1, 64))
+    refuse("rope_store", "expected 2 of 64", k_cache=f(5, 3, 8, 64), v_cache=f(5, 3, 8, 64))
+    refuse("rope_store", "one layout", v_cache=f(5, 8, 2, 64).transpose(1, 2))
+    refuse("attn_paged", "f32 or bf16", q=f(2, 4, 64).half())
+    refuse("attn_paged", "q must", q=f(2, 8, 64)[:, ::2])
+    refuse("attn_paged", "expected 2 of 64", k_cache=f(5, 2, 8, 32), v_cache=f(5, 2, 8, 32))
+    refuse("attn_paged", "contiguous rows", k_cache=f(5, 2, 64, 8).transpose(2, 3), v_cache=f(5, 2, 64, 8).transpose(2, 3))
+    refuse("attn_paged", "token_start", token_start=i(2))
+    refuse("attn_paged", "output", output=f(2, 4, 32))
+    refuse("attn_paged", "window", window=-1)
+    # strided rows, other cache orders and a missing token_start are fine (refused for being on the host only)
+    for change in (dict(q=f(2, 10, 64)[:, 3:7]), dict(k_cache=f(5, 8, 2, 64).transpose(1, 2), v_cache=f(5, 8, 2, 64).transpose(1, 2)),
+                   dict(token_start=None), dict(output=f(4, 4, 64)[::2])):
+        refuse("attn_paged", "must be a CUDA tensor", **change)
+
+
+def test_binding_workspace_size(L):
     import torch
 
     import serving_gdn_decode_gb300 as gdn
-    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
-    q, kc, out = torch.zeros(2, 4, 64), torch.zeros(5, 2, 8, 64), torch.zeros(2, 4, 64)
-    with pytest.raises(nat.GdnError, match="must be a CUDA tensor"):
-        gdn.gdn_attn_paged(q, kc, kc, i(2, 3), i(2), None, out, torch.zeros(10))
-    with pytest.raises(nat.GdnError, match="must be a CUDA tensor"):
-        gdn.gdn_rope(q, q, i(2), torch.zeros(9, 64), out, out)
-    with pytest.raises(TypeError, match="slot_map"):
-        gdn.gdn_rope_store(q, q, q, i(2), torch.zeros(9, 64), [0, 1], kc, kc, out)
-    with pytest.raises(TypeError, match="n_free"):
-        gdn.gdn_kv_plan(i(2), i(2), i(2), i(4), 4, i(2, 3), 8, 5, i(2), i(2), i(1), i(3), i(2), i(2))
-
-
-def test_binding_shape_rules():
-    """The marshalling's own checks, on host tensors (which the calls refuse)."""
-    import torch
-
-    from serving_gdn_decode_gb300 import paged
-    q, kc = torch.zeros(2, 4, 64), torch.zeros(5, 2, 8, 64)
-    p = paged._attn_params(q, kc, kc, 3, 7, None, None, 9)
-    assert (p.head_dim, p.n_q_heads, p.n_kv_heads, p.page_size, p.n_pages, p.max_pages, p.window) == (64, 4, 2, 8, 5, 7, 9)
-    assert (p.cache_page_stride, p.cache_head_stride, p.cache_slot_stride) == (1024, 512, 64)
-    assert p.scale == pytest.approx(0.125) and (p.q_stride, p.out_stride) == (256, 256)
-    nhd = torch.zeros(5, 8, 2, 64).transpose(1, 2)
-    p = paged._attn_params(q, nhd, nhd, 3, 7, None, 0.5, 0)
-    assert (p.cache_page_stride, p.cache_head_stride, p.cache_slot_stride, p.scale) == (1024, 64, 128, 0.5)
-    wide = torch.zeros(2, 10, 64)[:, 3:7]
-    assert paged._attn_params(wide, kc, kc, 1, 1, None, None, 0).q_stride == 640
-    for bad in (torch.zeros(2, 64, 4).transpose(1, 2), torch.zeros(2, 8, 64)[:, ::2], torch.zeros(4, 64)):
-        with pytest.raises(nat.GdnError):
-            paged._attn_params(bad, kc, kc, 1, 1, None, None, 0)
-    with pytest.raises(nat.GdnError, match="f32 or bf16"):
-        paged._attn_params(q.half(), kc, kc, 1, 1, None, None, 0)
-    with pytest.raises(nat.GdnError, match="k_cache"):
-        paged._attn_params(q.bfloat16(), kc, kc, 1, 1, None, None, 0)
-    with pytest.raises(nat.GdnError, match="one layout"):
-        paged._attn_params(q, kc, nhd, 1, 1, None, None, 0)
-    with pytest.raises(nat.GdnError, match="expected 2 of 64"):
-        paged._attn_params(q, torch.zeros(5, 2, 8, 128), torch.zeros(5, 2, 8, 128), 1, 1, None, None, 0)
-    k, pos, cs = torch.zeros(2, 2, 64), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(9, 32)
-    p = paged._rope_params(q, k, None, pos, cs, q, k, None, None, None, bytes([2] * 16), 1)
-    assert (p.n_axes, p.positions_stride, p.rot_dim, p.n_positions, p.flags, p.axis_of_pair[15]) == (3, 2, 32, 9, 1, 2)
-    for change, text in ((dict(axes=bytes(3)), "axes has 3"), (dict(positions=pos.long()), "positions"),
-                         (dict(positions=pos[:, :1]), "positions"), (dict(cos_sin=cs.double()), "cos_sin"),
-                         (dict(cos_sin=cs.t()), "cos_sin"), (dict(q_out=torch.zeros(2, 3, 64)), "q_out"),
-                         (dict(k_out=k.bfloat16()), "k_out")):
-        a = dict(q=q, k=k, v=None, positions=pos, cos_sin=cs, q_out=q, k_out=k, slot_map=None, k_cache=None,
-                 v_cache=None, axes=bytes(16), flags=0)
-        a.update(change)
-        with pytest.raises(nat.GdnError, match=text):
-            paged._rope_params(**a)
-
-
-def test_kept_params_are_bounded(monkeypatch):
-    """The kept structs depend on shapes only and cannot grow without end."""
-    from serving_gdn_decode_gb300 import paged
-    monkeypatch.setattr(paged, "_kept", {})
-    monkeypatch.setattr(paged, "_MAX_KEPT", 8)
-    for i in range(50):
-        assert paged._keep(i, lambda: i) == i
-        assert paged._keep(i, lambda: -1) == i
-        assert len(paged._kept) <= 8
+    q, kc = torch.zeros(6, 8, 128, dtype=torch.bfloat16), torch.zeros(50, 2, 16, 128, dtype=torch.bfloat16)
+    assert gdn.gdn_attn_workspace_size(q, kc, 4) == workspace_size(L)[1]
+    with pytest.raises(nat.GdnError) as e:
+        gdn.gdn_attn_workspace_size(q[..., :96].contiguous(), kc[..., :96], 4)
+    assert e.value.status == nat.GDN_ERR_UNSUPPORTED
 
 
 def test_fast_division_is_exact():
