@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
   float *join = reinterpret_cast<float *>(smem + S::kSlots * S::kHalf);
   void *q_smem = smem + S::kSlots * S::kHalf + join_bytes<T, D, WARPS>();
 
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  begin_in_order();
 
   // This CTA's share of the units: the prefix sum of the requests' units, a
   // contiguous run of requests per thread.
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const __
   constexpr int kAhead = 8;                                                 // parts a group has on their way
   __shared__ float4 s_acc[kTeams][D / 4];
   __shared__ float s_m[kTeams], s_den[kTeams];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  begin_in_order();
   const Split sp = c.splits[blockIdx.x];
   if (sp.slot < 0) return;
   const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, mine = team / kTeam, member = team % kTeam;
@@ -1082,23 +1082,12 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW, P::WARPS>;
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    main<<<P::ctas, 32 * P::WARPS, smem, stream>>>(c);
-    e = cudaGetLastError();
+    e = launch_in_order(main, dim3(P::ctas), 32 * P::WARPS, smem, stream, c);
     if (e != cudaSuccess) return e;
-    // The join may be set up while the main kernel still runs; it waits for its end before it reads.  Few items
-    // have many parts each: a CTA per row; many have few: a warp per row.
+    // Few items have many parts each: a CTA per row; many have few: a warp per row.
     const bool few = static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P::ctas, few ? P::rows : P::rows / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few ? gdn_attn_join_kernel<T, P::D, P::rows, 1> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
-                              static_cast<const Call>(c));
+    return launch_in_order(few ? gdn_attn_join_kernel<T, P::D, P::rows, 1> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
+                           dim3(P::ctas, few ? P::rows : P::rows / kJoinWarps), 32 * kJoinWarps, 0, stream, c);
   });
 }
 

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_plan_kernel(const PlanArgs a,
 
   const gdn_kv_plan_params &p = a.p;
   const int tid = threadIdx.x;
+  begin_in_order();
   const long long page = p.page_size;
   // this CTA's share of the slots
   const uint32_t per = (p.n_slots + gridDim.x - 1) / gridDim.x;
@@ -202,8 +203,7 @@ cudaError_t launch_kv_plan(const PlanArgs &a, cudaStream_t stream) {
   uint32_t ctas = (a.p.n_slots + kTokensPerCta - 1) / kTokensPerCta;
   if (ctas < 1) ctas = 1;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  gdn_kv_plan_kernel<<<ctas, kThreads, 0, stream>>>(a, FastDiv(a.p.page_size));
-  return cudaGetLastError();
+  return launch_in_order(gdn_kv_plan_kernel, dim3(ctas), kThreads, 0, stream, a, FastDiv(a.p.page_size));
 }
 
 cudaError_t kv_plan_status(unsigned int *bits, bool reset, cudaStream_t stream) {

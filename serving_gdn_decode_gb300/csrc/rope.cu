@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
   // the warp's rows at a time (one where a head has more places than the warp has lanes)
   const uint32_t at_once = places < 32 ? 32 / places : 1, my_row = places < 32 ? lane / places : 0;
   const bool active = my_row < at_once;
+  begin_in_order();
   const uint32_t n_units = p.n_tokens * dv.n_parts;  // below 2^31: parts > 1 only with few tokens
 
   for (uint32_t j = places < 32 ? lane - my_row * places : lane; j < places; j += 32) {
@@ -245,8 +246,7 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
     dv.place_axis[j] = one ? x[0] : kMixed;
   }
   const uint64_t ctas = (static_cast<uint64_t>(p.n_tokens) * dv.n_parts + kWarps - 1) / kWarps;
-  gdn_rope_kernel<T, E><<<static_cast<uint32_t>(ctas), kThreads, 0, stream>>>(a, dv);
-  return cudaGetLastError();
+  return launch_in_order(gdn_rope_kernel<T, E>, dim3(static_cast<uint32_t>(ctas)), kThreads, 0, stream, a, dv);
 }
 
 // Whether every access of E elements is aligned and none crosses the rotated
