@@ -130,6 +130,7 @@ struct Call {
   int64_t q_stride, out_stride, page_stride, head_stride, slot_stride;
   FastDiv page_div, group_div;
   bool whole_tiles;  // pages hold whole 16-key tiles
+  bool out_wide;     // output rows are aligned to four elements
 };
 
 // A request's share of the work.
@@ -177,9 +178,13 @@ __device__ __forceinline__ Request request(const Call &c, uint32_t s) {
   return r;
 }
 
+// a / b for a >= 0, in 32 bits where they hold a (64-bit division is a long subroutine).
+__device__ __forceinline__ long long divide(long long a, uint32_t b) {
+  return a >> 32 ? a / b : static_cast<uint32_t>(a) / b;
+}
 // CTA x of `ctas` takes units [start(x), start(x + 1)).
 __device__ __forceinline__ long long share_start(long long total, int ctas, int x) {
-  return total * x / ctas;
+  return divide(total * x, ctas);
 }
 
 // ------------------------------------------------------------ per-type pieces
@@ -458,6 +463,25 @@ constexpr int ctas_per_sm() {
   return by_smem > 3 ? 3 : by_smem;
 }
 
+// Four neighbouring results, rounded once; in one store where rows are aligned to it.
+__device__ __forceinline__ void put4(float *o, const float (&x)[4], bool wide) {
+  if (wide) {
+    *reinterpret_cast<float4 *>(o) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = x[e];
+  }
+}
+__device__ __forceinline__ void put4(__nv_bfloat16 *o, const float (&x)[4], bool wide) {
+  if (wide) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = __float2bfloat16_rn(x[e]);
+  }
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -488,7 +512,7 @@ struct Item {
         r = request<ROWS>(c, seq);
       }
       const int all = r.tiles + kItemUnits;
-      item = static_cast<int>(in_seq / all);
+      item = static_cast<int>(divide(in_seq, all));
       const int at = static_cast<int>(in_seq - static_cast<long long>(item) * all);
       units = static_cast<int>(min(static_cast<long long>(all - at), u1 - u));
       tile0 = max(0, at - kItemUnits);
@@ -624,6 +648,27 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
       }
     }
   };
+  // q of the item, for its first use a whole tile later
+  int head = 0, block = 0;
+  W w(lane, row0);
+  auto begin_q = [&] {
+    head = it.item / it.r.blocks;
+    block = it.item - head * it.r.blocks;
+    // Column n of the score tile is row block * kRows + n of the item: token row / group, query head row % group.
+    const int rows = it.r.tokens * static_cast<int>(c.group);
+    auto q_row = [&](int n) -> const T * {
+      const int row = block * kRows + n;
+      if (row >= rows) return nullptr;
+      const int t = c.group_div.div(row);
+      return static_cast<const T *>(c.q) + static_cast<int64_t>(it.r.t0 + t) * c.q_stride +
+             (static_cast<int64_t>(head) * c.group + (row - t * static_cast<int>(c.group))) * D;
+    };
+    w.load_q(q_row, q_smem, lane, row0);
+  };
+  long long u = u0;
+  bool more = it.find(c, u, u1);
+  if (more) begin_q();
+
   next_item();
   auto fetch = [&] {  // the next half tile: K of a tile, then its V
     if (f_any) {
@@ -685,22 +730,10 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
     fetch();
   };
 
-  W w(lane, row0);
   unsigned slot = 0;
-  for (long long u = u0; it.find(c, u, u1);) {
+  while (more) {
     const Request &r = it.r;
-    const int head = it.item / r.blocks, block = it.item - head * r.blocks;
-
-    // Column n of the score tile is row block * kRows + n of the item: token row / group, query head row % group.
     const int rows = r.tokens * static_cast<int>(c.group);
-    auto q_row = [&](int n) -> const T * {
-      const int row = block * kRows + n;
-      if (row >= rows) return nullptr;
-      const int t = c.group_div.div(row);
-      return static_cast<const T *>(c.q) + static_cast<int64_t>(r.t0 + t) * c.q_stride +
-             (static_cast<int64_t>(head) * c.group + (row - t * static_cast<int>(c.group))) * D;
-    };
-    w.load_q(q_row, q_smem, lane, row0);
     // the last key each of this lane's columns sees
     int last[NT][2], token[NT][2];
 #pragma unroll
@@ -883,13 +916,15 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
           }
           if (poison) den = NAN;
           if (whole) {
+            const float inv = 1.0f / den;
             const int t = c.group_div.div(item_row);
             // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
             const bool empty = r.len - r.tokens + t < 0 && !poison;
             T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
                    (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d0 + d;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Act<T>::put(o + e, empty ? 0.0f : sum[e] / den);
+            for (int e = 0; e < 4; ++e) sum[e] = empty ? 0.0f : sum[e] * inv;
+            put4(o, sum, c.out_wide);
           } else {
             const size_t at = static_cast<size_t>(part_slot) * kRows + n;
             *reinterpret_cast<float4 *>(c.part + at * D + d0 + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
@@ -905,6 +940,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
                             head * static_cast<int>(c.group), r.len - r.tokens, 0};
     }
     it.pass(u);
+    more = it.find(c, u, u1);
+    if (more) begin_q();
   }
   cp_async_wait<0>();
 }
@@ -1072,6 +1109,8 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   c.page_div = FastDiv(p.page_size);
   c.group_div = FastDiv(c.group);
   c.whole_tiles = p.page_size % kTile == 0;
+  const uintptr_t four = p.dtype == GDN_DTYPE_BF16 ? 8 : 16;
+  c.out_wide = reinterpret_cast<uintptr_t>(a.output) % four == 0 && p.out_stride % 4 == 0;
   return dispatch(p, [&](auto pick) {
     using P = decltype(pick);
     using T = typename P::type;
