@@ -48,8 +48,9 @@
 namespace gdn {
 namespace {
 
-constexpr int kTile = 16;  // keys per tile
+constexpr int kSub = 16;   // keys of a matrix tile
 constexpr int kUnit = 64;  // keys per unit of work
+constexpr int kMostTile = 32;  // largest tile of a key group
 constexpr int kItemUnits = 2;  // what an item's begin and end cost beside its keys, in units
 constexpr int kSms = 152;
 constexpr int kJoinWarps = 8;
@@ -129,7 +130,7 @@ struct Call {
   float scale_log2;
   int64_t q_stride, out_stride, page_stride, head_stride, slot_stride;
   FastDiv page_div, group_div;
-  bool whole_tiles;  // pages hold whole 16-key tiles
+  bool whole_tiles;  // pages hold whole tiles
   bool out_wide;     // output rows are aligned to four elements
 };
 
@@ -170,7 +171,7 @@ __device__ __forceinline__ Request request(const Call &c, uint32_t s) {
   }
   r.len = len;
   const long long lo = c.window ? static_cast<long long>(len) - r.tokens + 1 - c.window : 0;
-  r.lo = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0) / kTile * kTile;  // tiles begin at multiples of 16
+  r.lo = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0) / kMostTile * kMostTile;  // tiles begin at multiples of their size
   const long long rows = static_cast<long long>(r.tokens) * c.group;
   r.blocks = static_cast<int>((rows + ROWS - 1) / ROWS);
   const int tiles = (len - r.lo + kUnit - 1) / kUnit;
@@ -189,13 +190,19 @@ __device__ __forceinline__ long long share_start(long long total, int ctas, int 
 
 // ------------------------------------------------------------ per-type pieces
 
-template <typename T, int D>
+// KT: matrix tiles of 16 keys in a tile, the step of a key group.
+template <typename T, int D, int KT>
 struct Shape {
+  static constexpr int kTile = kSub * KT;
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
   static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
   static constexpr int kHalf = kTile * kRowBytes;  // bytes of a half tile
   // half tiles in a CTA's rings together
-  static constexpr int kSlots = kHalf == 2048 ? 32 : kHalf == 4096 ? (sizeof(T) == 4 ? 12 : 20) : kHalf == 8192 ? (sizeof(T) == 4 ? 20 : 24) : 12;
+  static constexpr int kSlots16 = kRowBytes == 128   ? 32
+                                  : kRowBytes == 256 ? (sizeof(T) == 4 ? 12 : 20)
+                                  : kRowBytes == 512 ? (sizeof(T) == 4 ? 20 : 24)
+                                                     : 12;
+  static constexpr int kSlots = kSlots16 / KT;
   static constexpr int kSteps = kChunks / 2;       // matrix steps over D (32 bytes each)
   // the join of a CTA's warps goes through shared memory in pieces of 8 rows x kJoinCols
   static constexpr int kJoinCols = D < 128 ? D : 128;
@@ -214,7 +221,7 @@ __device__ __host__ constexpr int order(int r) {
 }
 template <typename T, int D>
 __device__ __forceinline__ constexpr int swizzled(int r, int c) {
-  return r * Shape<T, D>::kRowBytes + ((c ^ order<T>(r)) << 4);
+  return r * D * static_cast<int>(sizeof(T)) + ((c ^ order<T>(r)) << 4);
 }
 
 // NT: 8-row tiles of a warp.  RW: warps that share a ring, each with rows of its
@@ -225,7 +232,7 @@ struct Warp;
 // bf16: K and V fragments by ldmatrix, q fragments in registers.
 template <int D, int NT, int RW>
 struct Warp<__nv_bfloat16, D, NT, RW> {
-  using S = Shape<__nv_bfloat16, D>;
+  using S = Shape<__nv_bfloat16, D, 1>;
   static constexpr int kQSmem = 0;
   unsigned q[S::kSteps][NT][2];
   unsigned k_at[4], v_at[4];  // this lane's offsets in a half tile for steps 0-3; step + 4: 128 bytes on
@@ -281,7 +288,7 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
   // The B fragments of P^T from the score tile's layout: hi and lo halves.
   struct P {
     unsigned hi[NT][2], lo[NT][2];
-    __device__ __forceinline__ P(const float (&p)[NT][4], int) {
+    __device__ __forceinline__ void take(const float (&p)[NT][4], int) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -325,7 +332,7 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
 // elements of D (scores) or the tile's 16 keys (output), and is added in f32.
 template <int D, int NT, int RW>
 struct Warp<float, D, NT, RW> {
-  using S = Shape<float, D>;
+  using S = Shape<float, D, 1>;
   static constexpr int kQRow = 2 * D + 8;  // (hi, lo) pairs, padded
   static constexpr int kQSmem = RW * NT * 8 * kQRow * 4;
   unsigned k_at[4], v_at[8], q_at;
@@ -390,7 +397,7 @@ struct Warp<float, D, NT, RW> {
 
   struct P {
     unsigned hi[NT][4], lo[NT][4];  // [key / 4]
-    __device__ __forceinline__ P(const float (&p)[NT][4], int lane) {
+    __device__ __forceinline__ void take(const float (&p)[NT][4], int lane) {
       // value (key, row) is with lane (key % 8) * 4 + row / 2, in register key / 8 * 2 + row % 2
       const int src = (lane & 3) * 4 + (lane >> 3);
       const bool odd = lane >> 2 & 1;
@@ -450,16 +457,16 @@ struct Warp<float, D, NT, RW> {
 
 template <typename T, int D, int WARPS>
 constexpr int join_bytes() {
-  return WARPS * 8 * Shape<T, D>::kJoinRow * 4;
+  return WARPS * 8 * Shape<T, D, 1>::kJoinRow * 4;
 }
-template <typename T, int D, int NT, int RW, int WARPS>
+template <typename T, int D, int NT, int RW, int WARPS, int KT>
 constexpr int smem_bytes() {
-  return Shape<T, D>::kSlots * Shape<T, D>::kHalf + join_bytes<T, D, WARPS>() + Warp<T, D, NT, RW>::kQSmem;
+  return Shape<T, D, KT>::kSlots * Shape<T, D, KT>::kHalf + join_bytes<T, D, WARPS>() + Warp<T, D, NT, RW>::kQSmem;
 }
 // CTAs an SM holds: its shared memory, and registers enough for the accumulators
-template <typename T, int D, int NT, int RW, int WARPS>
+template <typename T, int D, int NT, int RW, int WARPS, int KT>
 constexpr int ctas_per_sm() {
-  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW, WARPS>() + 1024);  // + the static part
+  const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW, WARPS, KT>() + 1024);  // + the static part
   return by_smem > 3 ? 3 : by_smem;
 }
 
@@ -492,7 +499,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // One (request, key head, row block) item of a CTA's share, or the part of it
 // that lies in the share.
-template <int ROWS, int KW>
+template <int ROWS, int KW, int TILE>
 struct Item {
   uint32_t seq;
   Request r;
@@ -530,24 +537,25 @@ struct Item {
     u += units;
     in_seq += units;
   }
-  // Tiles of 16 keys of this part that key group `kg` takes: k0 + 16 (kg + KW i).
+  // Tiles of this part that key group `kg` takes: k0 + TILE (kg + KW i).
   __device__ __forceinline__ int tiles_of(int kg) const {
-    const int first = k0 + kTile * kg;
-    return first < k1 ? (k1 - first + kTile * KW - 1) / (kTile * KW) : 0;
+    const int first = k0 + TILE * kg;
+    return first < k1 ? (k1 - first + TILE * KW - 1) / (TILE * KW) : 0;
   }
 };
 
-template <typename T, int D, int NT, int RW, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>())) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
-  using S = Shape<T, D>;
+template <typename T, int D, int NT, int RW, int WARPS, int KT>
+__global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, KT>())) gdn_attn_paged_kernel(const __grid_constant__ Call c) {
+  using S = Shape<T, D, KT>;
   using W = Warp<T, D, NT, RW>;
+  constexpr int kTile = S::kTile;
   constexpr int kRows = RW * NT * 8;   // rows of a block
   constexpr int KW = WARPS / RW;       // key groups
   constexpr int kThreads = 32 * WARPS;
   constexpr int kStep = kTile * KW;    // keys from a group's tile to its next
   constexpr int kRing = S::kSlots / KW;
   static_assert(kUnit % kStep == 0, "a unit is the same number of tiles to every group");
-  static_assert(ctas_per_sm<T, D, NT, RW, WARPS>() >= 1, "a CTA fits an SM's shared memory");
+  static_assert(ctas_per_sm<T, D, NT, RW, WARPS, KT>() >= 1, "a CTA fits an SM's shared memory");
   static_assert(kRing <= 32, "a bit per slot");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[WARPS], s_offset;
@@ -611,11 +619,11 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
 
   // The ring's feed runs ahead of the products, across items: `f` is the item
   // that the next half tile belongs to, `f_i` its tile.
-  Item<kRows, KW> f;
+  Item<kRows, KW, kTile> f;
   f.seq = s_seq;
   f.in_seq = s_offset;
   f.r = request<kRows>(c, f.seq);
-  Item<kRows, KW> it = f;
+  Item<kRows, KW, kTile> it = f;
   long long f_u = u0;
   int f_i = 0, f_n = 0, f_head = 0;
   unsigned f_slot = 0;
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
   const long long my_src = my_row * slot_bytes + my_chunk * 16;
   const unsigned my_dst = swizzled<T, D>(my_row, my_chunk);
   auto look_up = [&] {
-    const int key = f.k0 + kTile * kg + f_i * kStep + (c.whole_tiles ? 0 : lane & 15);
+    const int key = f.k0 + kTile * kg + f_i * kStep + (c.whole_tiles ? 0 : lane & (kTile - 1));
     page = key < f.k1 ? f_table[c.page_div.div(key)] : 0;
   };
   auto next_item = [&] {  // to the next item in which this key group has a tile
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
         }
       } else {
         if (!f_value) {
-          const int key = f.k0 + kTile * kg + f_i * kStep + (lane & 15);
+          const int key = f.k0 + kTile * kg + f_i * kStep + (lane & (kTile - 1));
           const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
           const bool none = key < f.k1 && static_cast<uint32_t>(page) >= c.n_pages;
           bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
@@ -770,37 +778,46 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
     for (int i = 0; i < n_tiles; ++i, key0 += kStep) {
       // scores
       arrived();
-      float s[NT][4];
-      w.scores(s, ring + slot * S::kHalf, q_smem);
+      float s[KT][NT][4];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) w.scores(s[kt], ring + slot * S::kHalf + kt * kSub * S::kRowBytes, q_smem);
       bad_page |= bad_slots >> slot & 1;
       slot = slot + 1 == kRing ? 0 : slot + 1;
       const bool edge = key0 + kTile > all1 || key0 < all0;
       bool grown = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] *= c.scale_log2;
-      if (edge) {
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = key0 + lane / 4 + (j >> 1) * 8, hi = min(last[nt][j & 1], it.k1 - 1);
-            const long long lo = c.window ? static_cast<long long>(last[nt][j & 1]) - c.window : -1;
-            if (key > hi || key <= lo) s[nt][j] = -INFINITY;
-          }
+          for (int j = 0; j < 4; ++j) s[kt][nt][j] *= c.scale_log2;
+      if (edge) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int key = key0 + kt * kSub + lane / 4 + (j >> 1) * 8, hi = min(last[nt][j & 1], it.k1 - 1);
+              const long long lo = c.window ? static_cast<long long>(last[nt][j & 1]) - c.window : -1;
+              if (key > hi || key <= lo) s[kt][nt][j] = -INFINITY;
+            }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) grown |= s[nt][j] > m[nt][j & 1] + 8.0f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) grown |= s[kt][nt][j] > m[nt][j & 1] + 8.0f;
       if (__any_sync(kFull, grown)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float g[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(s[nt][j], s[nt][j + 2]);
+            float top = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+            for (int kt = 1; kt < KT; ++kt) top = fmaxf(top, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -819,14 +836,18 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          s[nt][j] = exp2_fast(s[nt][j] - m[nt][j]);
-          s[nt][j + 2] = exp2_fast(s[nt][j + 2] - m[nt][j]);
-          l[nt][j] += s[nt][j] + s[nt][j + 2];
-        }
-      const typename W::P p(s, lane);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s[kt][nt][j] = exp2_fast(s[kt][nt][j] - m[nt][j]);
+            s[kt][nt][j + 2] = exp2_fast(s[kt][nt][j + 2] - m[nt][j]);
+            l[nt][j] += s[kt][nt][j] + s[kt][nt][j + 2];
+          }
+      typename W::P p[KT];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) p[kt].take(s[kt], lane);
       // output
       arrived();
       const unsigned v_tile = ring + slot * S::kHalf;
@@ -834,9 +855,12 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
       if (!edge) {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
-          const typename W::V v(w, v_tile, md);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p, nt);
+          for (int kt = 0; kt < KT; ++kt) {
+            const typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
+          }
         }
       } else {
         // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite
@@ -847,15 +871,18 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS>(
           const int lo = c.window ? hi - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
 #pragma unroll
           for (int md = 0; md < D / 16; ++md) {
-            typename W::V v(w, v_tile, md);
-            v.keep(lo, min(hi, it.k1 - key0), lane);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              v.mma(y, p, nt);
+            for (int kt = 0; kt < KT; ++kt) {
+              typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+              v.keep(lo - kt * kSub, min(hi, it.k1 - key0) - kt * kSub, lane);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (token[nt][j & 1] == t) acc[md][nt][j] += y[j];
+              for (int nt = 0; nt < NT; ++nt) {
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                v.mma(y, p[kt], nt);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (token[nt][j & 1] == t) acc[md][nt][j] += y[j];
+              }
             }
           }
         }
@@ -1033,11 +1060,11 @@ uint64_t rows_of(const gdn_attn_params &p) {
   return window * (p.n_q_heads / p.n_kv_heads);
 }
 
-template <typename T, int D_, int NT_, int RW_, int WARPS_ = 4>
+template <typename T, int D_, int NT_, int RW_, int WARPS_ = 4, int KT_ = 1>
 struct Pick {
   using type = T;
-  static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, rows = NT_ * RW_ * 8;
-  static constexpr int ctas = kSms * ctas_per_sm<T, D_, NT_, RW_, WARPS_>();
+  static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, KT = KT_, rows = NT_ * RW_ * 8;
+  static constexpr int ctas = kSms * ctas_per_sm<T, D_, NT_, RW_, WARPS_, KT_>();
 };
 
 // Calls f with the Pick of the call: the fewest rows per block that hold its
@@ -1052,14 +1079,14 @@ auto dispatch(const gdn_attn_params &p, F f) {
     if constexpr (sizeof(T) * D >= 1024) {  // 1 KB per key: no room for more than 8 rows of q beside the rings
       return f(Pick<T, D, 1, 1>{});
     } else if constexpr (D == 256) {  // 16 columns' accumulators and q would not fit a thread's registers
-      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8>{});
+      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8, 2>{});
     } else if constexpr (sizeof(T) == 4) {
       return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
     } else {
       return rows <= 8    ? f(Pick<T, D, 1, 1>{})
              : rows <= 16 ? f(Pick<T, D, 2, 1>{})
-             : rows <= 32 ? f(Pick<T, D, 2, 2>{})
-                          : f(Pick<T, D, 2, 4>{});
+             : rows <= 32 ? f(Pick<T, D, 2, 2, 4, 2>{})
+                          : f(Pick<T, D, 2, 4, 4, 2>{});
     }
   };
   auto by_dim = [&](auto t) {
@@ -1108,25 +1135,25 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   c.slot_stride = p.cache_slot_stride;
   c.page_div = FastDiv(p.page_size);
   c.group_div = FastDiv(c.group);
-  c.whole_tiles = p.page_size % kTile == 0;
   const uintptr_t four = p.dtype == GDN_DTYPE_BF16 ? 8 : 16;
   c.out_wide = reinterpret_cast<uintptr_t>(a.output) % four == 0 && p.out_stride % 4 == 0;
   return dispatch(p, [&](auto pick) {
     using P = decltype(pick);
     using T = typename P::type;
-    constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW, P::WARPS>();
+    constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW, P::WARPS, P::KT>();
+    c.whole_tiles = p.page_size % (kSub * P::KT) == 0;
     c.splits = static_cast<Split *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.splits + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
-    const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW, P::WARPS>;
+    const auto main = gdn_attn_paged_kernel<T, P::D, P::NT, P::RW, P::WARPS, P::KT>;
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_in_order(main, dim3(P::ctas), 32 * P::WARPS, smem, stream, c);
     if (e != cudaSuccess) return e;
-    // Few items have many parts each: a CTA per row; many have few: a warp per row.
+    // Few items have many parts each: four warps per row; many have few: a warp per row.
     const bool few = static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas;
-    return launch_in_order(few ? gdn_attn_join_kernel<T, P::D, P::rows, 1> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
-                           dim3(P::ctas, few ? P::rows : P::rows / kJoinWarps), 32 * kJoinWarps, 0, stream, c);
+    return launch_in_order(few ? gdn_attn_join_kernel<T, P::D, P::rows, 2> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
+                           dim3(P::ctas, P::rows / (few ? 2 : kJoinWarps)), 32 * kJoinWarps, 0, stream, c);
   });
 }
 
