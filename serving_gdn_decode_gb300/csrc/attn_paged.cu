@@ -554,7 +554,6 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
   constexpr int kThreads = 32 * WARPS;
   constexpr int kStep = kTile * KW;    // keys from a group's tile to its next
   constexpr int kRing = S::kSlots / KW;
-  static_assert(kUnit % kStep == 0, "a unit is the same number of tiles to every group");
   static_assert(ctas_per_sm<T, D, NT, RW, WARPS, KT>() >= 1, "a CTA fits an SM's shared memory");
   static_assert(kRing <= 32, "a bit per slot");
   extern __shared__ __align__(128) unsigned char smem[];
@@ -1083,7 +1082,9 @@ auto dispatch(const gdn_attn_params &p, F f) {
     } else if constexpr (sizeof(T) == 4) {
       return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
     } else {
-      return rows <= 8    ? f(Pick<T, D, 1, 1>{})
+      // at 128 bytes a key, steps of 32 keys halve what a step costs beside its loads (64 requests up to 8192
+      // keys, 32/8 heads: 89.1 -> 85.4 us); at 256 bytes they cost registers (81.0 -> 85.4 us)
+      return rows <= 8    ? f(Pick<T, D, 1, 1, 4, D == 64 ? 2 : 1>{})
              : rows <= 16 ? f(Pick<T, D, 2, 1>{})
              : rows <= 32 ? f(Pick<T, D, 2, 2, 4, 2>{})
                           : f(Pick<T, D, 2, 4, 4, 2>{});

@@ -10,7 +10,7 @@
 // in this step, free_pages[n_free - 1 - rank].
 //
 // One launch and no waiting between CTAs: every CTA computes the same two
-// prefix sums for itself, 1024 requests at a time, and writes its own share of
+// prefix sums for itself, 256 or 1024 requests at a time, and writes its own share of
 // the tokens, the new table entries and the per-request outputs.  Nothing a
 // CTA reads is written by another (a table entry that exists before the call
 // is only read, a new one only written; a new page's number comes from the
@@ -28,45 +28,39 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 1024;          // requests per scan round
-constexpr uint32_t kTokensPerCta = 2048;  // slots a CTA fills before another CTA is added
+constexpr uint32_t kTokensPerCta = 512;  // slots a CTA fills before another CTA is added
 constexpr uint32_t kMaxCtas = 152;
 
 struct Pair {
   long long tokens, pages;
 };
 
-// Exclusive prefix sums over the CTA's threads of x; *total: the sums over all.
-__device__ __forceinline__ Pair block_scan(Pair x, Pair *warp_sum /* 32 in shared memory */, Pair *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Pair inc = x;
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {  // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc.tokens, d);
-    const long long p = __shfl_up_sync(0xffffffffu, inc.pages, d);
+    const long long t = __shfl_up_sync(0xffffffffu, x.tokens, d);
+    const long long p = __shfl_up_sync(0xffffffffu, x.pages, d);
     if (lane >= d) {
-      inc.tokens += t;
-      inc.pages += p;
+      x.tokens += t;
+      x.pages += p;
     }
   }
+  return x;
+}
+
+// Exclusive prefix sums over the CTA's threads of x; *total: the sums over all.
+// Every warp adds the warps' sums up for itself: one barrier.
+template <int THREADS>
+__device__ __forceinline__ Pair block_scan(Pair x, Pair *warp_sum /* THREADS / 32 in shared memory */, Pair *total) {
+  constexpr int kWarps = THREADS / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Pair inc = warp_scan(x, lane);
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    Pair w = warp_sum[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, w.tokens, d);
-      const long long p = __shfl_up_sync(0xffffffffu, w.pages, d);
-      if (lane >= d) {
-        w.tokens += t;
-        w.pages += p;
-      }
-    }
-    warp_sum[lane] = w;
-  }
-  __syncthreads();
-  const Pair before = warp ? warp_sum[warp - 1] : Pair{0, 0};
-  *total = warp_sum[31];
+  const Pair w = warp_scan(lane < kWarps ? warp_sum[lane] : Pair{0, 0}, lane);
+  *total = Pair{__shfl_sync(0xffffffffu, w.tokens, kWarps - 1), __shfl_sync(0xffffffffu, w.pages, kWarps - 1)};
+  Pair before{__shfl_sync(0xffffffffu, w.tokens, warp ? warp - 1 : 0), __shfl_sync(0xffffffffu, w.pages, warp ? warp - 1 : 0)};
+  if (warp == 0) before = Pair{0, 0};
   return Pair{before.tokens + inc.tokens - x.tokens, before.pages + inc.pages - x.pages};
 }
 
@@ -83,6 +77,7 @@ __device__ __forceinline__ int last_at_or_before(const int *start, int n, int x)
 
 __device__ __forceinline__ int to_int(long long x) { return static_cast<int>(x < INT_MAX ? x : INT_MAX); }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) gdn_kv_plan_kernel(const PlanArgs a, const FastDiv page_div) {
   __shared__ Pair warp_sum[32];
   __shared__ int s_start[kThreads], s_rank[kThreads], s_ctx[kThreads], s_owned[kThreads];
@@ -124,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_plan_kernel(const PlanArgs a,
     if (!fits) bad |= GDN_DEVICE_BAD_REQUEST;
 
     Pair total;
-    Pair base = block_scan(Pair{fresh, demand}, warp_sum, &total);
+    Pair base = block_scan<kThreads>(Pair{fresh, demand}, warp_sum, &total);
     base.tokens += carry.tokens;
     base.pages += carry.pages;
     const bool served = fits && (demand == 0 || base.pages + demand <= n_free);
@@ -203,7 +198,10 @@ cudaError_t launch_kv_plan(const PlanArgs &a, cudaStream_t stream) {
   uint32_t ctas = (a.p.n_slots + kTokensPerCta - 1) / kTokensPerCta;
   if (ctas < 1) ctas = 1;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  return launch_in_order(gdn_kv_plan_kernel, dim3(ctas), kThreads, 0, stream, a, FastDiv(a.p.page_size));
+  // a CTA of the requests' number: the fewer warps, the sooner its barriers are passed
+  const FastDiv page(a.p.page_size);
+  if (a.p.n_seqs <= 256) return launch_in_order(gdn_kv_plan_kernel<256>, dim3(ctas), 256, 0, stream, a, page);
+  return launch_in_order(gdn_kv_plan_kernel<1024>, dim3(ctas), 1024, 0, stream, a, page);
 }
 
 cudaError_t kv_plan_status(unsigned int *bits, bool reset, cudaStream_t stream) {
