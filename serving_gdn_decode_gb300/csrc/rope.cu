@@ -72,6 +72,18 @@ struct Vec<__nv_bfloat16, 1> {
   __device__ __forceinline__ void put(const float (&f)[1]) { x = __float2bfloat16_rn(f[0]); }
 };
 
+template <typename V>
+__device__ __forceinline__ V from_lane_xor(const V &v, int mask) {
+  static_assert(sizeof(V) == 16, "a 16-byte vector");
+  const uint4 x = *reinterpret_cast<const uint4 *>(&v);
+  uint4 y;
+  y.x = __shfl_xor_sync(0xffffffffu, x.x, mask);
+  y.y = __shfl_xor_sync(0xffffffffu, x.y, mask);
+  y.z = __shfl_xor_sync(0xffffffffu, x.z, mask);
+  y.w = __shfl_xor_sync(0xffffffffu, x.w, mask);
+  return *reinterpret_cast<const V *>(&y);
+}
+
 // Rotates the E pairs of two vectors: (lo[e], hi[e]), or neighbours within lo, then hi.
 template <typename T, int E>
 __device__ __forceinline__ void rotate(Vec<T, E> &lo, Vec<T, E> &hi, const float (&c)[E], const float (&s)[E], bool inter) {
@@ -108,14 +120,19 @@ struct RopeDivs {
   uint8_t place_axis[GDN_ROPE_MAX_DIM / 2];  // the axis of a place's E pairs; kMixed: several, or cos_sin only by the element
 };
 
-template <typename T, int E>
+// SHORT: rows of 128 bytes or less, rotated in full as halves.  A place's two
+// vectors would be 64-byte pieces of two accesses, and the cache's tags, not
+// its bytes, would bound the kernel (8209 tokens of 16 + 16 heads of 64, bf16:
+// 20.2 us); so there a lane takes one vector of a row that the warp reads
+// whole, and gets the other half from the lane that has it.
+template <typename T, int E, bool SHORT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __grid_constant__ RopeArgs a,
                                                                         const RopeDivs dv) {
   using V = Vec<T, E>;
   const gdn_rope_params &p = a.p;
   const uint32_t half = p.rot_dim / 2, lane = threadIdx.x & 31;
   const bool store = a.v != nullptr, inter = (p.flags & GDN_ROPE_INTERLEAVED) != 0;
-  const uint32_t places = p.head_dim / (2 * E), rot_places = p.rot_dim / (2 * E);
+  const uint32_t pairs = p.head_dim / (2 * E), places = SHORT ? 2 * pairs : pairs, rot_places = p.rot_dim / (2 * E);
   // rows of a token: q heads, k heads, v heads
   const uint32_t k_row = p.n_q_heads, v_row = k_row + p.n_kv_heads;
   const uint32_t n_rows = store ? v_row + p.n_kv_heads : v_row;
@@ -125,10 +142,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
   begin_in_order();
   const uint32_t n_units = p.n_tokens * dv.n_parts;  // below 2^31: parts > 1 only with few tokens
 
-  for (uint32_t j = places < 32 ? lane - my_row * places : lane; j < places; j += 32) {
+  for (uint32_t jj = places < 32 ? lane - my_row * places : lane; jj < places; jj += 32) {
+    const bool second = SHORT && jj >= pairs;  // of the row's halves
+    const uint32_t j = second ? jj - pairs : jj;
     const bool turns = j < rot_places;
     // where q and k rows have this place's two vectors, and v rows
-    const uint32_t col = turns && !inter ? j * E : j * 2 * E, gap = turns && !inter ? half : E, v_col = j * 2 * E;
+    // (halves of the rotated part, of the rest and of a v row, so that neighbouring lanes read neighbouring vectors)
+    const uint32_t col = SHORT ? jj * E : !turns ? p.rot_dim + (j - rot_places) * E : inter ? j * 2 * E : j * E;
+    const uint32_t gap = !turns ? (p.head_dim - p.rot_dim) / 2 : inter ? E : half;
+    const uint32_t v_col = SHORT ? jj * E : j * E, v_gap = p.head_dim / 2;
     const uint32_t axis = turns ? dv.place_axis[j] : 0;
 
     const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -142,16 +164,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
       auto load = [&](uint32_t r0) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const uint32_t r = r0 + u * at_once;
+          const uint32_t r = r0 + my_row + u * at_once;
           if (r >= row1 || !active) continue;
           const T *src = r < k_row   ? q + r * p.head_dim + col
                          : r < v_row ? k + (r - k_row) * p.head_dim + col
                                      : v + (r - v_row) * p.head_dim + v_col;
           lo[u] = *reinterpret_cast<const V *>(src);
-          hi[u] = *reinterpret_cast<const V *>(src + (r < v_row ? gap : E));
+          if (!SHORT) hi[u] = *reinterpret_cast<const V *>(src + (r < v_row ? gap : v_gap));
         }
       };
-      uint32_t r0 = part * dv.part_rows + my_row;
+      uint32_t r0 = part * dv.part_rows;
       load(r0);  // on its way while the cosines are looked up
       float c[E], s[E];
       if (turns) {
@@ -184,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
             }
           }
         }
-        if (p.flags & GDN_ROPE_INVERSE) {
+        // a pair's first element takes -s times the other, its second s
+        if (((p.flags & GDN_ROPE_INVERSE) != 0) != (SHORT && !second)) {
 #pragma unroll
           for (int e = 0; e < E; ++e) s[e] = -s[e];
         }
@@ -197,12 +220,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
         else
           report(GDN_DEVICE_BAD_PAGE);
       }
-      while (r0 < row1 && active) {
+      while (r0 < row1) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const uint32_t r = r0 + u * at_once;
-          if (r >= row1) continue;
-          if (turns && r < v_row) rotate<T, E>(lo[u], hi[u], c, s, inter);
+          const uint32_t r = r0 + my_row + u * at_once;
+          if constexpr (SHORT) hi[u] = from_lane_xor(lo[u], pairs);  // every lane takes part
+          if (r >= row1 || !active) continue;
+          if (r < v_row) {
+            if constexpr (SHORT) {
+              float mine[E], other[E];
+              lo[u].get(mine);
+              hi[u].get(other);
+#pragma unroll
+              for (int e = 0; e < E; ++e) mine[e] = mine[e] * c[e] + other[e] * s[e];
+              lo[u].put(mine);
+            } else if (turns) {
+              rotate<T, E>(lo[u], hi[u], c, s, inter);
+            }
+          }
           T *dst;
           if (r < k_row) {
             dst = static_cast<T *>(a.q_out) + token * p.q_out_stride + r * p.head_dim + col;
@@ -214,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
                             : static_cast<T *>(a.v_cache) + slot_at + (r - v_row) * p.cache_head_stride + v_col;
           }
           *reinterpret_cast<V *>(dst) = lo[u];
-          *reinterpret_cast<V *>(dst + (r < v_row ? gap : E)) = hi[u];
+          if (!SHORT) *reinterpret_cast<V *>(dst + (r < v_row ? gap : v_gap)) = hi[u];
         }
         r0 += kUnroll * at_once;
         load(r0);
@@ -223,10 +258,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_rope_kernel(const __
   }
 }
 
-template <typename T, int E>
+template <typename T, int E, bool SHORT = false>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   const gdn_rope_params &p = a.p;
-  const uint32_t places = p.head_dim / (2 * E), at_once = places < 32 ? 32 / places : 1;
+  const uint32_t places = p.head_dim / (SHORT ? E : 2 * E), at_once = places < 32 ? 32 / places : 1;
   const uint32_t rows = p.n_q_heads + p.n_kv_heads * (a.v ? 2 : 1);
   RopeDivs dv;
   dv.page = FastDiv(p.page_size ? p.page_size : 1);
@@ -246,7 +281,7 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
     dv.place_axis[j] = one ? x[0] : kMixed;
   }
   const uint64_t ctas = (static_cast<uint64_t>(p.n_tokens) * dv.n_parts + kWarps - 1) / kWarps;
-  return launch_in_order(gdn_rope_kernel<T, E>, dim3(static_cast<uint32_t>(ctas)), kThreads, 0, stream, a, dv);
+  return launch_in_order(gdn_rope_kernel<T, E, SHORT>, dim3(static_cast<uint32_t>(ctas)), kThreads, 0, stream, a, dv);
 }
 
 // Whether every access of E elements is aligned and none crosses the rotated
@@ -270,6 +305,11 @@ bool vectors_fit(const RopeArgs &a, uint32_t e, uint32_t elem) {
 template <typename T>
 cudaError_t launch_type(const RopeArgs &a, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(T);
+  const gdn_rope_params &p = a.p;
+  const uint32_t pairs = p.head_dim / (2 * E);  // a power of two: the other half is with lane ^ pairs
+  const bool whole = p.rot_dim == p.head_dim && !(p.flags & GDN_ROPE_INTERLEAVED);
+  if (vectors_fit(a, E, sizeof(T)) && whole && p.head_dim * sizeof(T) <= 128 && (pairs & (pairs - 1)) == 0)
+    return launch<T, E, true>(a, stream);
   return vectors_fit(a, E, sizeof(T))       ? launch<T, E>(a, stream)
          : vectors_fit(a, E / 2, sizeof(T)) ? launch<T, E / 2>(a, stream)
                                             : launch<T, 1>(a, stream);

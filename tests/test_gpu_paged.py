@@ -372,7 +372,7 @@ ROPE_TOL = {"f32": 2e-7, "bf16": 2.0 ** -9}
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("dim,rot,n_q,n_kv,n_axes", [
     (128, 128, 4, 2, 3), (256, 64, 16, 1, 2), (64, 64, 3, 3, 1), (64, 20, 5, 1, 4), (6, 2, 1, 1, 1), (80, 80, 2, 2, 2),
-    (256, 256, 40, 8, 4), (34, 34, 2, 1, 3)])
+    (256, 256, 40, 8, 4), (34, 34, 2, 1, 3), (32, 32, 7, 2, 2), (16, 16, 1, 1, 1), (72, 72, 5, 5, 2)])
 def test_rope_and_inverse(torch, dtype, inter, dim, rot, n_q, n_kv, n_axes):
     import serving_gdn_decode_gb300 as gdn
     dt, n = dtype_of(torch, dtype), 37
