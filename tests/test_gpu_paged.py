@@ -670,3 +670,12 @@ def test_steps_together(torch):
         assert kv.tolist() == [len(x) for x in keys]
         state = [kv, owned, left]
     assert int(state[2]) == n_pages - sum(state[1].tolist())
+
+
+def test_hybrid_example(torch, capsys):
+    """The example's decode steps (captured and replayed) end where one pass over all tokens does.  Both
+    paths are f32; eight layers of sums of 512 to 1024 terms, each step's rounding amplified by the
+    normalisations: 1e-3 of the logits is a hundred times what f32 leaves and far below any slip."""
+    from serving_gdn_decode_gb300 import hybrid_step
+    assert hybrid_step.main(["--requests", "5", "--prompt", "37", "--steps", "20", "--check"]) <= 1e-3
+    assert "device status 0" in capsys.readouterr().out
