@@ -204,9 +204,6 @@ struct Shape {
                                                      : 12;
   static constexpr int kSlots = kSlots16 / KT;
   static constexpr int kSteps = kChunks / 2;       // matrix steps over D (32 bytes each)
-  // the join of a CTA's warps goes through shared memory in pieces of 8 rows x kJoinCols
-  static constexpr int kJoinCols = D < 128 ? D : 128;
-  static constexpr int kJoinRow = kJoinCols + 4;  // padded: a fragment's rows fall on different banks
 };
 
 // A half tile in shared memory: row r's chunk c lies at r * kRowBytes +
@@ -318,6 +315,12 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
         a[h * 2 + 1] &= m;
       }
     }
+    // m: the largest magnitudes so far, as bits
+    __device__ __forceinline__ void largest(unsigned &m) const {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, a[i] & 0x7fff7fffu);
+    }
+    static __device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
     // c += V^T P^T
     __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
       mma_bf16(c, a, p.hi[nt][0], p.hi[nt][1]);
@@ -350,11 +353,24 @@ struct Warp<float, D, NT, RW> {
 
   template <typename F>
   __device__ __forceinline__ void load_q(F row, void *q_smem, int, int) {
-    uint2 *qs = static_cast<uint2 *>(q_smem);
-    for (int i = threadIdx.x; i < RW * NT * 8 * D; i += blockDim.x) {
-      const float *p = row(i / D);
-      const Tf32Pair x(p ? p[i % D] : 0.0f);
-      qs[i / D * (kQRow / 2) + i % D] = make_uint2(x.hi, x.lo);
+    // four elements a time, all of a thread's on their way before the first is split
+    constexpr int kFours = RW * NT * 8 * D / 4, kMine = kFours / 128;
+    float x[kMine][4];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int at = threadIdx.x + i * 128, col = at % (D / 4) * 4;
+      const float *p = row(at / (D / 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i][e] = p ? p[col + e] : 0.0f;
+    }
+    uint4 *qs = static_cast<uint4 *>(q_smem);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int at = threadIdx.x + i * 128, col = at % (D / 4) * 4;
+      const Tf32Pair a(x[i][0]), b(x[i][1]), c(x[i][2]), d(x[i][3]);
+      uint4 *to = qs + (at / (D / 4) * kQRow + col * 2) / 4;
+      to[0] = make_uint4(a.hi, a.lo, b.hi, b.lo);
+      to[1] = make_uint4(c.hi, c.lo, d.hi, d.lo);
     }
   }
 
@@ -440,6 +456,13 @@ struct Warp<float, D, NT, RW> {
           if (key < k0 || key >= k1) hi[h][i] = lo[h][i] = 0u;
         }
     }
+    __device__ __forceinline__ void largest(unsigned &m) const {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(hi[h][i] & 0x7fffffffu, lo[h][i] & 0x7fffffffu));
+    }
+    static __device__ __forceinline__ bool finite(unsigned m) { return m < 0x7f800000u; }
     __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
       float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -455,9 +478,15 @@ struct Warp<float, D, NT, RW> {
   };
 };
 
+// The join of a CTA's warps goes through shared memory in pieces of 8 rows x join_cols, rows padded so that a
+// fragment's fall on different banks.
+template <typename T, int D, int WARPS>
+constexpr int join_cols() {
+  return D < 256 || (sizeof(T) == 2 && WARPS == 4) ? D : 128;
+}
 template <typename T, int D, int WARPS>
 constexpr int join_bytes() {
-  return WARPS * 8 * Shape<T, D, 1>::kJoinRow * 4;
+  return WARPS * 8 * (join_cols<T, D, WARPS>() + 4) * 4;
 }
 template <typename T, int D, int NT, int RW, int WARPS, int KT>
 constexpr int smem_bytes() {
@@ -467,7 +496,8 @@ constexpr int smem_bytes() {
 template <typename T, int D, int NT, int RW, int WARPS, int KT>
 constexpr int ctas_per_sm() {
   const int by_smem = 227 * 1024 / (smem_bytes<T, D, NT, RW, WARPS, KT>() + 1024);  // + the static part
-  return by_smem > 3 ? 3 : by_smem;
+  const int by_regs = sizeof(T) == 4 && NT == 2 ? 2 : 3;
+  return by_smem > by_regs ? by_regs : by_smem;
 }
 
 // Four neighbouring results, rounded once; in one store where rows are aligned to it.
@@ -549,6 +579,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
   using S = Shape<T, D, KT>;
   using W = Warp<T, D, NT, RW>;
   constexpr int kTile = S::kTile;
+  constexpr int kJoinCols = join_cols<T, D, WARPS>(), kJoinRow = kJoinCols + 4;
   constexpr int kRows = RW * NT * 8;   // rows of a block
   constexpr int KW = WARPS / RW;       // key groups
   constexpr int kThreads = 32 * WARPS;
@@ -556,6 +587,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
   constexpr int kRing = S::kSlots / KW;
   static_assert(ctas_per_sm<T, D, NT, RW, WARPS, KT>() >= 1, "a CTA fits an SM's shared memory");
   static_assert(kRing <= 32, "a bit per slot");
+  static_assert(sizeof(T) == 2 || WARPS == 4, "the f32 form loads q with 128 threads");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[WARPS], s_offset;
   __shared__ uint32_t s_seq;
@@ -861,9 +893,39 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
             for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
           }
         }
+        continue;
+      }
+      // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite or NaN).
+      // Keys that no token of the warp sees are cut out of V; if tokens see different keys of the tile and a
+      // value of those is not finite, each token's columns take a product of their own.
+      const int seen0 = c.window ? r.len - r.tokens + t_first + 1 - static_cast<int>(min(c.window, 0x3fffffffu)) - key0 : 0;
+      const int seen1 = min(r.len - r.tokens + t_last + 1, it.k1) - key0;
+      bool apart = false;
+      if (t_first != t_last) {
+        unsigned most = 0;
+#pragma unroll 4
+        for (int md = 0; md < D / 16; ++md) {
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+            v.keep(seen0 - kt * kSub, seen1 - kt * kSub, lane);
+            v.largest(most);
+          }
+        }
+        apart = __any_sync(kFull, !W::V::finite(most));
+      }
+      if (!apart) {
+#pragma unroll
+        for (int md = 0; md < D / 16; ++md) {
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+            v.keep(seen0 - kt * kSub, seen1 - kt * kSub, lane);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
+          }
+        }
       } else {
-        // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite
-        // or NaN), so each token's columns take the product with V's unseen keys cut out.
 #pragma unroll 1
         for (int t = t_first; t <= t_last; ++t) {
           const int hi = r.len - r.tokens + t + 1 - key0;
@@ -909,20 +971,20 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int d0 = 0; d0 < D; d0 += S::kJoinCols) {
+      for (int d0 = 0; d0 < D; d0 += kJoinCols) {
 #pragma unroll
-        for (int md = 0; md < S::kJoinCols / 16; ++md)
+        for (int md = 0; md < kJoinCols / 16; ++md)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * S::kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
+            join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
         __syncthreads();
         bool poison = false;  // rows over a page that does not exist are NaN
 #pragma unroll
         for (int i = 0; i < WARPS; ++i) poison |= s_bad[i] != 0;
         if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
 #pragma unroll 1
-        for (int x = tid; x < RW * 8 * S::kJoinCols / 4; x += kThreads) {
-          const int row = x / (S::kJoinCols / 4), d = x % (S::kJoinCols / 4) * 4;
+        for (int x = tid; x < RW * 8 * kJoinCols / 4; x += kThreads) {
+          const int row = x / (kJoinCols / 4), d = x % (kJoinCols / 4) * 4;
           const int of = row / 8, in = row % 8, m_row = nt * 8 + in;  // rows of warps of, of + RW, ...
           const int n = of * NT * 8 + m_row, item_row = block * kRows + n;
           if (item_row >= rows) break;
@@ -933,7 +995,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
 #pragma unroll
           for (int i = 0; i < KW; ++i) {
             const float g = exp2_fast(s_m[i * RW + of][m_row] - top);
-            const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + of) * 8 + in) * S::kJoinRow + d);
+            const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + of) * 8 + in) * kJoinRow + d);
             sum[0] += g * y.x;
             sum[1] += g * y.y;
             sum[2] += g * y.z;
