@@ -1213,10 +1213,11 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_in_order(main, dim3(P::ctas), 32 * P::WARPS, smem, stream, c);
     if (e != cudaSuccess) return e;
-    // Few items have many parts each: four warps per row; many have few: a warp per row.
+    // Few items have many parts each: several warps per row; many have few: a warp per row.
+    constexpr int kFewPer = P::rows / 4 < kJoinWarps ? P::rows / 4 : kJoinWarps;
     const bool few = static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas;
-    return launch_in_order(few ? gdn_attn_join_kernel<T, P::D, P::rows, 2> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
-                           dim3(P::ctas, P::rows / (few ? 2 : kJoinWarps)), 32 * kJoinWarps, 0, stream, c);
+    return launch_in_order(few ? gdn_attn_join_kernel<T, P::D, P::rows, kFewPer> : gdn_attn_join_kernel<T, P::D, P::rows, kJoinWarps>,
+                           dim3(P::ctas, P::rows / (few ? kFewPer : kJoinWarps)), 32 * kJoinWarps, 0, stream, c);
   });
 }
 
