@@ -131,6 +131,7 @@ struct Call {
   int64_t q_stride, out_stride, page_stride, head_stride, slot_stride;
   FastDiv page_div, group_div;
   bool whole_tiles;  // pages hold whole tiles
+  bool whole_items;  // no item is split
   bool out_wide;     // output rows are aligned to four elements
 };
 
@@ -552,6 +553,13 @@ struct Item {
       item = static_cast<int>(divide(in_seq, all));
       const int at = static_cast<int>(in_seq - static_cast<long long>(item) * all);
       units = static_cast<int>(min(static_cast<long long>(all - at), u1 - u));
+      if (c.whole_items) {  // to the share that has its first unit
+        if (at > 0) {
+          pass(u);
+          continue;
+        }
+        units = all;
+      }
       tile0 = max(0, at - kItemUnits);
       tile1 = at + units - kItemUnits;
       if (tile1 > tile0) {
@@ -1205,6 +1213,12 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     using T = typename P::type;
     constexpr int smem = smem_bytes<T, P::D, P::NT, P::RW, P::WARPS, P::KT>();
     c.whole_tiles = p.page_size % (kSub * P::KT) == 0;
+    // An item of a few units is not split: the join of its parts would take longer than its keys (16 requests,
+    // 16/4 heads of 128, bf16, up to 256 keys: 8.7 split, 7.9 us whole; up to 512: 8.9, 10.8; f32 up to 128 keys: 10.3,
+    // 9.0; up to 256: equal).
+    const uint64_t seen = static_cast<uint64_t>(p.window) + p.n_tokens;  // keys a window of tokens sees at most
+    const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size;
+    c.whole_items = (p.window && seen < keys ? seen : keys) <= (sizeof(T) == 4 ? 128 : 256);
     c.splits = static_cast<Split *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.splits + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
@@ -1212,7 +1226,7 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_in_order(main, dim3(P::ctas), 32 * P::WARPS, smem, stream, c);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || c.whole_items) return e;
     // Few items have many parts each: several warps per row; many have few: a warp per row.
     constexpr int kFewPer = P::rows / 4 < kJoinWarps ? P::rows / 4 : kJoinWarps;
     const bool few = static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas;

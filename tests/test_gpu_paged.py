@@ -239,6 +239,18 @@ def test_attn_many_requests(torch):
     Case(torch, "bf16", lens, wins=[1 if n else 0 for n in lens], dim=64, group=2, n_kv=1).check(torch, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("max_pages", [8, 16, 17, 100])
+def test_attn_table_width(torch, dtype, max_pages):
+    """A table that bounds the lengths keeps an item in one CTA, a wider one lets it be split: either is right,
+    with more items than CTAs and with fewer."""
+    lens = [(13 * i) % 129 for i in range(90)]
+    for n, n_kv in ((90, 7), (3, 1)):
+        Case(torch, dtype, lens[:n], wins=[min(3, k) for k in lens[:n]], n_kv=n_kv, group=2, dim=64, page=16,
+             max_pages=max_pages).check(torch, dtype)
+    Case(torch, dtype, [128, 5, 0, 64], dim=256, group=9, n_kv=2, max_pages=max_pages).check(torch, dtype, window=40)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_attn_scales(torch, scale):
     Case(torch, "f32", [100, 17], dim=64).check(torch, "f32", scale=scale)
