@@ -184,6 +184,11 @@ __device__ __forceinline__ Request request(const Call &c, uint32_t s) {
 __device__ __forceinline__ long long divide(long long a, uint32_t b) {
   return a >> 32 ? a / b : static_cast<uint32_t>(a) / b;
 }
+// x - window, no lower than any key index needs.
+__device__ __forceinline__ int less_window(int x, uint32_t window) {
+  const long long y = static_cast<long long>(x) - window;
+  return y < -(1 << 30) ? -(1 << 30) : static_cast<int>(y);
+}
 // CTA x of `ctas` takes units [start(x), start(x + 1)).
 __device__ __forceinline__ long long share_start(long long total, int ctas, int x) {
   return divide(total * x, ctas);
@@ -795,7 +800,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
     const int t_last = c.group_div.div(min(block * kRows + row0 + NT * 8, rows) - 1);
     // keys in [all0, all1) are seen by every row of this warp
     const int all1 = min(r.len - r.tokens + t_first + 1, it.k1);
-    const int all0 = c.window ? r.len - r.tokens + t_last + 1 - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
+    const int all0 = c.window ? less_window(r.len - r.tokens + t_last + 1, c.window) : 0;
     if (W::kQSmem) __syncthreads();
 
     // Sums are kept relative to 2^m; m follows the running maximum only when that has grown by more than
@@ -906,7 +911,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite or NaN).
       // Keys that no token of the warp sees are cut out of V; if tokens see different keys of the tile and a
       // value of those is not finite, each token's columns take a product of their own.
-      const int seen0 = c.window ? r.len - r.tokens + t_first + 1 - static_cast<int>(min(c.window, 0x3fffffffu)) - key0 : 0;
+      const int seen0 = c.window ? less_window(r.len - r.tokens + t_first + 1 - key0, c.window) : 0;
       const int seen1 = min(r.len - r.tokens + t_last + 1, it.k1) - key0;
       bool apart = false;
       if (t_first != t_last) {
@@ -937,7 +942,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
 #pragma unroll 1
         for (int t = t_first; t <= t_last; ++t) {
           const int hi = r.len - r.tokens + t + 1 - key0;
-          const int lo = c.window ? hi - static_cast<int>(min(c.window, 0x3fffffffu)) : 0;
+          const int lo = c.window ? less_window(hi, c.window) : 0;
 #pragma unroll
           for (int md = 0; md < D / 16; ++md) {
 #pragma unroll

@@ -303,6 +303,15 @@ def test_attn_writes_its_rows_only(torch):
     assert bool((wide[0] == 5).all()) and bool((wide[4] == 5).all()) and bool((wide[:, 256:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attn_output_aligned_to_an_element_only(torch, dtype):
+    c = Case(torch, dtype, [90, 500, 3000], dim=64, group=3)
+    raw = torch.full((c.out.numel() + 2,), 5.0, dtype=c.out.dtype, device="cuda")
+    c.out = raw[1:-1].view(c.out.shape)
+    c.check(torch, dtype)
+    assert float(raw[0]) == 5 and float(raw[-1]) == 5
+
+
 def test_attn_offsets_past_32_bits(torch):
     """A cache of more than 2^32 elements: pages at its very end."""
     import serving_gdn_decode_gb300 as gdn
