@@ -7,34 +7,46 @@
 // from the tensor cores' rate, so the kernel is built around keeping loads in
 // flight.  A token's rows sit on the N side of the matrix instruction (S^T = K
 // Q^T, O^T = V^T P^T): N is 8 there, so a group of 1 to 8 query heads wastes
-// the least, and accumulators stay small enough for registers.  The warp-level
-// mma.sync serves this (about a tenth of its rate is needed); a tcgen05 tile
+// the least, and accumulators stay in registers.  The warp-level mma.sync
+// serves this (14 % of the tensor cycles at 4 rows per key head); a tcgen05 tile
 // would put 128 keys on the M side for the same 8 columns and pay tensor-memory
-// round trips between two tiny products.
+// round trips between two tiny products.  Past 32 rows per key head that turns:
+// there the warp-level instructions and their operand reads bound the kernel.
 //
-// Split over the length.  The work of a call is a list of units of 64 keys,
-// ordered by (request, key head, row block, keys); the lengths are on the
-// device, so every CTA takes the prefix sum of the requests' units and then the
-// same share of the whole list, whatever the lengths are.  A CTA's share may
-// begin and end inside an (request, head, row block) item: such ends leave
-// unnormalised sums with their running maximum in the workspace (at most two
-// per CTA), and a second launch joins them; an item that lies in one CTA goes
+// Measured on a GB300, back to back over three sets of buffers, as shares of the
+// measured copy bandwidth (6783 GB/s): 64 requests of up to 4096 keys, 32/8 heads
+// of 128, bf16: 81 us, 0.90; 256 requests, 48/8 heads: 308 us, 0.98; one request
+// of 200003 keys, 32/4 heads: 68 us, 0.89; 16 rows per key head: 0.92; 32 rows:
+// 0.58 to 0.82; 56 rows: 0.4 to 0.6; f32, heads of 128 and 256: 0.87 to 0.93.  Below
+// about 100 MB of cache the fixed part shows: 2.5 us of launch, 3 us until the
+// first products (lengths, page numbers and keys are three dependent reads), and
+// 3 us for the join.
+//
+// Split over the length.  The work of a call is a list of units: 64 keys, and
+// two units for an item's begin and end (an item is a request's key head and
+// block of rows; without the two, CTAs with many short items finished 25 %
+// late).  The lengths are on the device, so every CTA takes the prefix sum of
+// the requests' units and then the same share of the whole list, whatever the
+// lengths are.  A share may begin and end inside an item: such ends leave
+// unnormalised sums with their running maximum in the workspace (at most two per
+// CTA), and a second launch joins them; an item that lies in one CTA goes
 // straight to the output.  No atomics: the order of every sum is fixed by the
 // sizes.
 //
-// Inside a CTA each of the 4 warps takes every fourth 16-key tile of the item
-// with a softmax state of its own, and the four are joined at the item's end;
-// so the main loop has no barrier between warps.  Each warp feeds itself
-// through a ring of half tiles (16 rows of K, then the same rows of V) with
-// 16-byte asynchronous copies, which follow any page size, stride and tile
-// edge; rows past the end arrive as zeros, so stale values of a page never meet
-// the products.
+// Inside a CTA each key group (a warp, or with more rows several warps that share
+// a ring) takes every KW-th tile of the item with a softmax state of its own, and
+// the groups are joined at the item's end; so the main loop has no barrier between
+// groups.  A group feeds itself through a ring of half tiles (16 or 32 rows of K,
+// then the same rows of V) with 16-byte asynchronous copies, which follow any page
+// size, stride and tile edge; 80 to 190 KB per SM are on their way.  The feed runs
+// on into the next items, so that the ring does not drain between them.
 //
 // Precision.  f32: each operand is split in two TF32 halves and three products
-// are taken, so products and sums are good to f32.  bf16: K, V and q are exact
-// in the products; the probabilities are split in two bf16 halves (two products
-// instead of one), which keeps the result at f32 quality until its one rounding
-// at the end.  The maximum, the sum and all accumulators are f32.
+// are taken, so products are good to f32.  bf16: K, V and q are exact in the
+// products; the probabilities are split in two bf16 halves (two products instead
+// of one: bytes, not products, bound the kernel), which keeps the result at f32
+// quality until its one rounding at the end.  The maximum, the sum and all
+// accumulators are f32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

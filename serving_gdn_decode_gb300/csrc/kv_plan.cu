@@ -17,7 +17,9 @@
 // free stack), so the inputs stay as they are and the outputs are new arrays.
 //
 // The data is a few KB to a few MB, so latency bounds it: one dependent load,
-// a two-value scan over the CTA, and the stores.
+// a two-value scan over the CTA with one barrier, and the stores.  Measured on a
+// GB300, back to back: 64 requests 3.3 us, 1024 requests with 58 prompts among
+// them (32 thousand tokens) 5.6 us; a launch alone is about 2.
 #include <cuda_runtime.h>
 
 #include <climits>

@@ -13,6 +13,13 @@
 // rows of a token, a warp covering 32 / (places per head) rows at a time: the
 // token's cosines stay in the lane's registers for all of them, several rows
 // are on their way at once, and no warp waits for another.
+//
+// Measured on a GB300, back to back over three sets of buffers, as shares of the
+// measured copy bandwidth (6783 GB/s): store of 16384 tokens, 32 + 2 x 8 heads of
+// 128, bf16, three axes: 66 us, 0.91; gradient of 8209 tokens, 16 + 16 heads of 64:
+// 16.1 us, 0.64 (short: a launch and the first loads are a third of it); 64 tokens:
+// 3.1 us.  Cosines staged in shared memory for a CTA, one or several tokens a step,
+// took 73 to 127 us for the first: a barrier per token, and fewer loads in flight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 2;  // rows a lane has on their way
+constexpr int kUnroll = 2;  // rows a lane has on their way (1: 71, 3 with 5 CTAs: 71, 2: 70 us for 16384 tokens)
 constexpr int kCtasPerSm = 6;
 constexpr uint32_t kEnoughWarps = 152 * kCtasPerSm * kWarps;  // what the GPU holds
 
