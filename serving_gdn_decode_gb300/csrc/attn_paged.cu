@@ -1165,7 +1165,9 @@ auto dispatch(const gdn_attn_params &p, F f) {
     if constexpr (sizeof(T) * D >= 1024) {  // 1 KB per key: no room for more than 8 rows of q beside the rings
       return f(Pick<T, D, 1, 1>{});
     } else if constexpr (D == 256) {  // 16 columns' accumulators and q would not fit a thread's registers
-      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8, 2>{});
+      // up to 24 rows two blocks of 16, the second read from L2 in part, are ahead of one of 32 (windows of 1 to 4
+      // tokens, 8 heads each: 60.3 against 65.3 us); at 32 rows they are not (334 against 281 us)
+      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 24 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8, 2>{});
     } else if constexpr (sizeof(T) == 4) {
       return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
     } else {

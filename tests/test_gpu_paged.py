@@ -8,10 +8,12 @@ Tolerances, from the arithmetic:
   probability, like the output, by at most twice that: 4e-5 at the very worst,
   were all errors of one sign.  Their signs are random over 64 to 256 products,
   so 2e-5 is ample.
-* bf16 attention: the same sums, then one rounding to nearest of each element,
-  2^-9 of it at most: rel-L2 2^-9 + 2e-5.
+* bf16 attention: the same sums, then one rounding to nearest of each element: off
+  by 2^-8 of it at most, uniformly, so 2^-8 / sqrt(3) = 2.3e-3 root-mean-square for
+  elements just above a power of two and half of that just below the next; 1.7e-3
+  over all: rel-L2 2^-9 + 2e-5, which these tests' thousands of elements stay below.
 * rope: two f32 products and a sum, 3 * 2^-24 of sqrt(a^2 + b^2): rel-L2 2e-7;
-  bf16 adds its one rounding, 2^-9.
+  bf16 adds its one rounding, 2^-9 as above.
 * whole numbers (the plan; copies of v): equal.
 """
 import math
