@@ -702,3 +702,46 @@ def test_hybrid_example(torch, capsys):
     from serving_gdn_decode_gb300 import hybrid_step
     assert hybrid_step.main(["--requests", "5", "--prompt", "37", "--steps", "20", "--check"]) <= 1e-3
     assert "device status 0" in capsys.readouterr().out
+
+
+def test_calls_on_two_streams(torch):
+    """Calls that overlap on two streams, each with its own workspace, and calls back to back on one stream
+    that share one, give what they give alone."""
+    import serving_gdn_decode_gb300 as gdn
+    cases = [Case(torch, "bf16", [3000 + 500 * i, 700, 64], dim=128, group=4, seed=i) for i in range(4)]
+    alone = [c.run(torch).clone() for c in cases]
+    for c in cases:
+        c.out.fill_(9.0)
+    size = max(gdn.gdn_attn_workspace_size(c.q_dev, c.k_dev, 3) for c in cases)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, c in enumerate(cases):
+            gdn.gdn_attn_paged(c.q_dev, c.k_dev, c.v_dev, c.table, c.kv_lens, c.start, c.out, work[i % 2],
+                               stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for c, want in zip(cases, alone):
+        assert torch.equal(c.out, want)
+
+
+def test_a_step_follows_what_is_before_it(torch):
+    """Short kernels launched back to back read what the ones before them wrote: a chain of in-place
+    rotations by one position each, mixed with torch's kernels, ends at the sum of them."""
+    import serving_gdn_decode_gb300 as gdn
+    n, steps = 8, 200
+    table = table_of(torch, 2, 64).cuda()
+    pos = torch.ones(n, dtype=torch.int32, device="cuda")
+    q = torch.randn(n, 2, 64, generator=torch.Generator().manual_seed(0)).cuda()
+    k = q.clone()
+    start = q.double().cpu()
+    for i in range(steps):
+        gdn.gdn_rope(q, k, pos, table, q, k)
+        if i % 3 == 0:
+            q.mul_(2.0)
+            q.mul_(0.5)
+    angle = steps * 10000.0 ** (-torch.arange(32, dtype=torch.float64) * 2 / 64)
+    a, b = start[..., :32], start[..., 32:]
+    want = torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()], -1)
+    # each step is off by 2^-24 in its cosines and 2^-23 in its sums: 200 steps of either sign
+    assert rel(q, want) <= 200 * 3 * 2.0 ** -24 and torch.equal(q, k)
