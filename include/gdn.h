@@ -521,7 +521,8 @@ typedef struct gdn_attn_params {
  * NaN and infinities included; infinities that it does see give NaN or
  * infinities.  One token per request (decode) or a window of a few
  * (verification of drafted tokens) is what it is built for; longer windows are
- * right but read the keys once per 16 rows.
+ * right but read the keys once per block of 8 to 64 rows (tokens times query
+ * heads per key head).
  *
  * Everything is accumulated in f32, with operands split so that products are
  * good to f32 (bf16 inputs are exact), and rounded once.  Results do not vary

@@ -128,7 +128,6 @@ struct alignas(16) Split {
   int t0;        // the request's first row of q
   int head0;     // its key head's first query head
   int before;    // keys that are before the request's window of tokens; below 0, its first tokens see none
-  int unused;
 };
 
 struct Call {
@@ -686,8 +685,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
   const int32_t *f_table = nullptr;
   bool f_value = false, f_any = false;
   unsigned bad_slots = 0;  // bit i: the K tile in slot i of the ring is not there (its page is none of the cache's)
-  int page = 0;           // the page of the next tile (of this lane's row of it), looked up a tile ahead
-  long long row_at = 0;   // byte offset of the tile's first row (of this lane's row; -1: zeros) in the caches
+  int page = 0;          // the page of the next tile (of this lane's row of it), looked up a tile ahead
+  long long row_at = 0;  // byte offset of the tile's first row (of this lane's row; -1: zeros) in the caches
   constexpr int kPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;  // rows one access of the warp covers
   constexpr int kAccesses = kTile * S::kChunks / 32 / RW;  // of this warp for a half tile
   const int my_row = (S::kChunks >= 32 ? 0 : lane / S::kChunks) + rg * (kTile / RW), my_chunk = lane % S::kChunks;
@@ -1050,7 +1049,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
     if (!whole && it.tile0 == 0 && tid == 0) {
       const long long end = u + it.units + (r.tiles - it.tile1) - 1;  // the item's last unit
       c.splits[cta] = Split{part_slot, static_cast<int>(((end + 1) * ctas - 1) / total), block * kRows, rows, r.t0,
-                            head * static_cast<int>(c.group), r.len - r.tokens, 0};
+                            head * static_cast<int>(c.group), r.len - r.tokens};
     }
     it.pass(u);
     more = it.find(c, u, u1);

@@ -155,8 +155,7 @@ bool get_stream(PyObject *o, c10::DeviceIndex device, gdn_stream_t *out) {
   return true;
 }
 
-bool count(PyObject *const *args, Py_ssize_t n, Py_ssize_t want) {
-  (void)args;
+bool count(Py_ssize_t n, Py_ssize_t want) {
   if (n == want) return true;
   PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
   return false;
@@ -176,7 +175,7 @@ bool get_u32(PyObject *o, const char *name, uint32_t *out) {
 PyObject *py_kv_plan(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   static const char *const names[12] = {"ctx_lens", "new_lens", "owned", "free_pages", "n_free", "block_table", "kv_lens",
                                         "owned_out", "n_free_out", "token_start", "slot_map", "positions"};
-  if (!count(args, n_args, 15)) return nullptr;
+  if (!count(n_args, 15)) return nullptr;
   Arg a[12];
   for (int i = 0; i < 12; ++i)
     if (!get(args[i], names[i], &a[i]) || !small(a[i])) return nullptr;
@@ -244,7 +243,7 @@ bool rope_params(const Arg &q, const Arg &k, const Arg &positions, const Arg &co
 // rope(q, k, positions, cos_sin, q_out, k_out, axes, flags, stream)
 PyObject *py_rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   static const char *const names[6] = {"q", "k", "positions", "cos_sin", "q_out", "k_out"};
-  if (!count(args, n_args, 9)) return nullptr;
+  if (!count(n_args, 9)) return nullptr;
   Arg a[6];
   for (int i = 0; i < 6; ++i)
     if (!get(args[i], names[i], &a[i]) || !small(a[i])) return nullptr;
@@ -262,7 +261,7 @@ PyObject *py_rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
 // rope_store(q, k, v, positions, cos_sin, slot_map, q_out, k_cache, v_cache, axes, flags, stream)
 PyObject *py_rope_store(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   static const char *const names[9] = {"q", "k", "v", "positions", "cos_sin", "slot_map", "q_out", "k_cache", "v_cache"};
-  if (!count(args, n_args, 12)) return nullptr;
+  if (!count(n_args, 12)) return nullptr;
   Arg a[9];
   for (int i = 0; i < 9; ++i)
     if (!get(args[i], names[i], &a[i]) || !small(a[i])) return nullptr;
@@ -296,7 +295,7 @@ bool attn_params(const Arg &q, const Arg &k, const Arg &v, gdn_attn_params *p) {
 
 // attn_workspace_size(q, k_cache, n_seqs)
 PyObject *py_attn_workspace_size(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
-  if (!count(args, n_args, 3)) return nullptr;
+  if (!count(n_args, 3)) return nullptr;
   Arg q, k;
   gdn_attn_params p{};
   if (!get(args[0], "q", &q) || !get(args[1], "k_cache", &k) || !small(q) || !small(k) || !get_u32(args[2], "n_seqs", &p.n_seqs) ||
@@ -314,7 +313,7 @@ PyObject *py_attn_workspace_size(PyObject *, PyObject *const *args, Py_ssize_t n
 // attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start | None, output, workspace, scale | None, window, stream)
 PyObject *py_attn_paged(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   static const char *const names[8] = {"q", "k_cache", "v_cache", "block_table", "kv_lens", "token_start", "output", "workspace"};
-  if (!count(args, n_args, 11)) return nullptr;
+  if (!count(n_args, 11)) return nullptr;
   const bool ragged = args[5] != Py_None;
   Arg a[8];
   for (int i = 0; i < 8; ++i) {
