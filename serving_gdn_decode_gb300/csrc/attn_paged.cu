@@ -102,9 +102,9 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const unsigned (&a)[4], 
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x = hi + lo up to 2^-21 |x|, both with TF32's 10 mantissa bits: hi is x rounded to nearest (a carry into the
-// exponent is the next binade), lo the exact rest with its low bits cut, which leans to neither side since the
-// rest has either sign.  A NaN that the carry turns into a zero in hi stays in lo.
+// x = hi + lo up to 2^-23 |x|, both with TF32's 10 mantissa bits: hi is x rounded to nearest (a carry into the
+// exponent is the next binade), lo the exact rest, at most 12 bits, of which it keeps 11; the cut leans to neither
+// side since the rest has either sign.  A NaN that the carry turns into a zero in hi stays in lo.
 struct Tf32Pair {
   unsigned hi, lo;
   __device__ __forceinline__ explicit Tf32Pair(float x) {
