@@ -42,11 +42,13 @@
 // on into the next items, so that the ring does not drain between them.
 //
 // Precision.  f32: each operand is split in two TF32 halves and three products
-// are taken, so products are good to f32.  bf16: K, V and q are exact in the
+// are taken, so a product is good to 3 * 2^-22.  bf16: K, V and q are exact in the
 // products; the probabilities are split in two bf16 halves (two products instead
-// of one: bytes, not products, bound the kernel), which keeps the result at f32
-// quality until its one rounding at the end.  The maximum, the sum and all
-// accumulators are f32.
+// of one: bytes, not products, bound the kernel), each off by 2^-16 of itself at
+// most, to either side: a 256th of what the result's one rounding, at the end,
+// may take.  The maximum, the sums and all accumulators are
+// f32; a tile's sum is added to the running one outside the tensor cores, but for
+// the short sums of kShortKeys.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -143,6 +145,7 @@ struct Call {
   FastDiv page_div, group_div;
   bool whole_tiles;  // pages hold whole tiles
   bool whole_items;  // no item is split
+  bool short_sums;   // no item has more than kShortKeys keys
   bool out_wide;     // output rows are aligned to four elements
 };
 
@@ -338,18 +341,17 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
       for (int i = 0; i < 4; ++i) m = __vmaxu2(m, a[i] & 0x7fff7fffu);
     }
     static __device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
-    // c += V^T P^T
-    __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
-      mma_bf16(c, a, p.hi[nt][0], p.hi[nt][1]);
-      mma_bf16(c, a, p.lo[nt][0], p.lo[nt][1]);
+    // y += V^T P^T, the sum of one tile
+    __device__ __forceinline__ void mma(float (&y)[4], const P &p, int nt) const {
+      mma_bf16(y, a, p.lo[nt][0], p.lo[nt][1]);
+      mma_bf16(y, a, p.hi[nt][0], p.hi[nt][1]);
     }
   };
 };
 
 // f32: three TF32 products of split operands; q's halves in shared memory.
-// The tensor cores cut the low bits of a running sum at every product, so the
-// long sums are taken outside them: a product's sum starts at zero, over 32
-// elements of D (scores) or the tile's 16 keys (output), and is added in f32.
+// As the output's sums, those of a score are taken outside the tensor cores: a
+// product's sum starts at zero, over 32 elements of D, and is added in f32.
 template <int D, int NT, int RW>
 struct Warp<float, D, NT, RW> {
   using S = Shape<float, D, 1>;
@@ -480,8 +482,7 @@ struct Warp<float, D, NT, RW> {
         for (int i = 0; i < 4; ++i) m = max(m, max(hi[h][i] & 0x7fffffffu, lo[h][i] & 0x7fffffffu));
     }
     static __device__ __forceinline__ bool finite(unsigned m) { return m < 0x7f800000u; }
-    __device__ __forceinline__ void mma(float (&c)[4], const P &p, int nt) const {
-      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ void mma(float (&y)[4], const P &p, int nt) const {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         mma_tf32(y, lo[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
@@ -489,8 +490,6 @@ struct Warp<float, D, NT, RW> {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) mma_tf32(y, hi[h], p.hi[nt][2 * h], p.hi[nt][2 * h + 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] += y[j];
     }
   };
 };
@@ -516,6 +515,17 @@ constexpr int ctas_per_sm() {
   const int by_regs = sizeof(T) == 4 && NT == 2 ? 2 : 3;
   return by_smem > by_regs ? by_regs : by_smem;
 }
+
+// The tensor cores cut the low bits of a running sum at every product, always towards zero: over n products a sum
+// kept there leans by up to n 2^-24 of itself (6.9e-3 over 2^20 keys, measured).  So a tile's sum starts at zero and
+// is added in f32, rounded to nearest.  The additions cost nothing where registers are left for a tile's sums; where
+// the accumulators take 64 registers or a warp has two row tiles they spill (32 requests up to 8191 keys, windows of
+// 1 to 4, 16/2 heads of 256: 65.0 against 61.3 us), and there a call whose table's width or window holds an item to
+// kShortKeys keys keeps its sums in the tensor cores: 1024 products at most, 2^-14 of the sum, a 32nd of the result's
+// rounding to bf16.
+constexpr uint64_t kShortKeys = 8192;
+template <typename T, int D, int NT>
+constexpr bool kTightRegisters = sizeof(T) == 2 && (D == 256 || NT > 1);
 
 // Four neighbouring results, rounded once; in one store where rows are aligned to it.
 __device__ __forceinline__ void put4(float *o, const float (&x)[4], bool wide) {
@@ -826,6 +836,13 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
+    auto add = [&](int md, const float (&y)[NT][4]) {  // a tile's sums to the running ones
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[md][nt][j] += y[nt][j];
+    };
+
     const int n_tiles = it.tiles_of(kg);
     int key0 = it.k0 + kTile * kg;
     bool bad_page = false;
@@ -908,14 +925,30 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       const unsigned v_tile = ring + slot * S::kHalf;
       slot = slot + 1 == kRing ? 0 : slot + 1;
       if (!edge) {
+        if constexpr (kTightRegisters<T, D, NT>) {
+          if (c.short_sums) {
+#pragma unroll
+            for (int md = 0; md < D / 16; ++md) {
+#pragma unroll
+              for (int kt = 0; kt < KT; ++kt) {
+                const typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
+              }
+            }
+            continue;
+          }
+        }
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
+          float y[NT][4] = {};
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
             const typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
+            for (int nt = 0; nt < NT; ++nt) v.mma(y[nt], p[kt], nt);
           }
+          add(md, y);
         }
         continue;
       }
@@ -941,13 +974,15 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       if (!apart) {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
+          float y[NT][4] = {};
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
             typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
             v.keep(seen0 - kt * kSub, seen1 - kt * kSub, lane);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
+            for (int nt = 0; nt < NT; ++nt) v.mma(y[nt], p[kt], nt);
           }
+          add(md, y);
         }
       } else {
 #pragma unroll 1
@@ -1235,8 +1270,9 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     // 16/4 heads of 128, bf16, up to 256 keys: 8.7 split, 7.9 us whole; up to 512: 8.9, 10.8; f32 up to 128 keys: 10.3,
     // 9.0; up to 256: equal).
     const uint64_t seen = static_cast<uint64_t>(p.window) + p.n_tokens;  // keys a window of tokens sees at most
-    const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size;
-    c.whole_items = (p.window && seen < keys ? seen : keys) <= (sizeof(T) == 4 ? 128 : 256);
+    const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size, most = p.window && seen < keys ? seen : keys;
+    c.whole_items = most <= (sizeof(T) == 4 ? 128 : 256);
+    c.short_sums = most <= kShortKeys;
     c.splits = static_cast<Split *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.splits + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
