@@ -533,8 +533,9 @@ typedef struct gdn_attn_params {
  * each.  The size depends on dtype, head_dim, heads, n_seqs and n_tokens only,
  * and not on the lengths.
  *
- * A table entry outside [0, n_pages) for a key that is read makes the rows of
- * that request's key head NaN and sets GDN_DEVICE_BAD_PAGE; a length outside
+ * A table entry outside [0, n_pages) for a key that one of the request's rows sees makes
+ * the rows of that request's key head NaN and sets GDN_DEVICE_BAD_PAGE (entries of pages
+ * that the window has left may hold anything); a length outside
  * [0, max_pages * page_size] or a token_start that does not ascend within
  * [0, n_tokens] is clipped and sets GDN_DEVICE_BAD_REQUEST.
  *

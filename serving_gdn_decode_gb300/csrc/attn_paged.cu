@@ -152,10 +152,12 @@ struct Call {
 // A request's share of the work.
 struct Request {
   int t0, tokens;   // its rows of q
-  int len, lo;      // its keys: those that at least one token sees lie in [lo, len)
+  int len, first;   // its keys: those that at least one token sees lie in [first, len)
   int blocks;       // row blocks per key head
   int tiles;        // units of keys per (key head, row block); 1 when there is no key
   bool bad;
+  // where its units begin; tiles begin at multiples of their size
+  __device__ __forceinline__ int lo() const { return first & ~(kMostTile - 1); }
   __device__ __forceinline__ long long units(const Call &c) const {
     return tokens > 0 ? static_cast<long long>(c.n_kv) * blocks * (tiles + kItemUnits) : 0;
   }
@@ -186,10 +188,10 @@ __device__ __forceinline__ Request request(const Call &c, uint32_t s) {
   }
   r.len = len;
   const long long lo = c.window ? static_cast<long long>(len) - r.tokens + 1 - c.window : 0;
-  r.lo = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0) / kMostTile * kMostTile;  // tiles begin at multiples of their size
+  r.first = static_cast<int>(lo > 0 ? (lo < len ? lo : len) : 0);
   const long long rows = static_cast<long long>(r.tokens) * c.group;
   r.blocks = static_cast<int>((rows + ROWS - 1) / ROWS);
-  const int tiles = (len - r.lo + kUnit - 1) / kUnit;
+  const int tiles = (len - r.lo() + kUnit - 1) / kUnit;
   r.tiles = tiles > 0 ? tiles : 1;
   return r;
 }
@@ -589,8 +591,8 @@ struct Item {
       tile0 = max(0, at - kItemUnits);
       tile1 = at + units - kItemUnits;
       if (tile1 > tile0) {
-        k0 = r.lo + tile0 * kUnit;
-        k1 = min(r.len, r.lo + tile1 * kUnit);
+        k0 = r.lo() + tile0 * kUnit;
+        k1 = min(r.len, r.lo() + tile1 * kUnit);
         return true;
       }
       pass(u);
@@ -694,7 +696,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
   unsigned f_slot = 0;
   const int32_t *f_table = nullptr;
   bool f_value = false, f_any = false;
-  unsigned bad_slots = 0;  // bit i: the K tile in slot i of the ring is not there (its page is none of the cache's)
+  unsigned bad_slots = 0;  // bit i: the K tile in slot i of the ring is not there (its page is none of the cache's), and
+                           // is not wholly before the window: pages that the window has left may be given back
   int page = 0;          // the page of the next tile (of this lane's row of it), looked up a tile ahead
   long long row_at = 0;  // byte offset of the tile's first row (of this lane's row; -1: zeros) in the caches
   constexpr int kPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;  // rows one access of the warp covers
@@ -751,8 +754,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
         if (!f_value) {
           const int key = f.k0 + kTile * kg + f_i * kStep;
           const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
-          const bool none = static_cast<uint32_t>(page) >= c.n_pages;
-          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
+          const bool none = static_cast<uint32_t>(page) >= c.n_pages, seen = key + kTile > f.r.first;
+          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none && seen) << f_slot;
           if (none) page = 0;
           row_at = (page * c.page_stride + f_head * c.head_stride) * static_cast<int>(sizeof(T)) + o * slot_bytes;
         }
@@ -768,8 +771,8 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
         if (!f_value) {
           const int key = f.k0 + kTile * kg + f_i * kStep + (lane & (kTile - 1));
           const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
-          const bool none = key < f.k1 && static_cast<uint32_t>(page) >= c.n_pages;
-          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none) << f_slot;
+          const bool none = static_cast<uint32_t>(page) >= c.n_pages, seen = key >= f.r.first && key < f.k1;
+          bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(none && seen) << f_slot;
           row_at = key < f.k1 && !none
                        ? (page * c.page_stride + f_head * c.head_stride) * static_cast<int>(sizeof(T)) + o * slot_bytes
                        : -1;

@@ -10,6 +10,10 @@ from test_gpu_paged import TOL, Case, clean_status, dtype_of, rel, torch  # noqa
 
 pytestmark = pytest.mark.gpu
 
+# Of a single row (64 elements or more): f32 as a whole tensor; bf16 by the largest rounding that all its elements
+# could have at once, half a unit of the last of 8 bits.
+ROW_TOL = {"f32": TOL["f32"], "bf16": 2.0 ** -8}
+
 
 # ------------------------------------------------------------------ attention: long sums
 
@@ -40,3 +44,36 @@ def test_attn_sums_of_long_items_do_not_drift(torch, dim, group):
         assert rel(out[r], ref) <= TOL["bf16"]
         signed = float(((out[r].double() - ref) / ref).mean())
         assert abs(signed) <= 4 * 2.0 ** -9 / math.sqrt(dim)
+
+
+# ------------------------------------------------------------------ attention: pages behind a sliding window
+
+
+@pytest.mark.parametrize("dtype,dim,group,wins", [("bf16", 64, 2, (1, 1, 1)), ("bf16", 128, 8, (1, 4, 7)), ("bf16", 256, 8, (1, 2, 3)),
+                                                  ("f32", 64, 2, (1, 3, 1)), ("f32", 256, 4, (1, 1, 2))])
+@pytest.mark.parametrize("page", [1, 8, 16, 24, 32, 48])
+@pytest.mark.parametrize("window", [1, 20, 64, 300])
+def test_attn_pages_behind_the_window_may_be_gone(torch, dtype, dim, group, wins, page, window):
+    """A server gives back the pages that a sliding window has left: their table entries are no pages any more,
+    at any place of the window's begin in a tile, and the rows and the status word are as with them."""
+    for first_len in (49, 64, 337, 1000):
+        lens = [first_len, first_len + 15, first_len + 22]
+        c = Case(torch, dtype, lens, wins=list(wins), dim=dim, group=group, n_kv=1, page=page, seed=first_len)
+        ref = c.reference(torch, window=window)
+        for s, (n, w) in enumerate(zip(lens, wins)):
+            gone = max(0, n - w + 1 - window) // page  # pages of which no row sees a key
+            c.table[s, :gone] = -1 if s % 2 else 1 << 20
+        got = c.run(torch, window=window)
+        for row in range(sum(wins)):
+            assert rel(got[row], ref[row]) <= ROW_TOL[dtype]
+
+
+def test_attn_a_page_that_one_row_sees_must_be_there(torch):
+    """Of the window's keys the first one's page is missing: only the first of three tokens sees it."""
+    from serving_gdn_decode_gb300 import _native as nat
+    c = Case(torch, "bf16", [100, 50], wins=[3, 1], dim=64, group=2, page=1)
+    ref = c.reference(torch, window=20)
+    c.table[0, 100 - 3 + 1 - 20] = -1
+    got = c.run(torch, window=20)
+    assert bool(got[:3].isnan().all()) and rel(got[3], ref[3]) <= TOL["bf16"]
+    assert nat.gdn_device_status(reset=True) == nat.GDN_DEVICE_BAD_PAGE
