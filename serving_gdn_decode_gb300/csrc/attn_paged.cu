@@ -105,12 +105,15 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const unsigned (&a)[4], 
 }
 
 // x = hi + lo up to 2^-23 |x|, both with TF32's 10 mantissa bits: hi is x rounded to nearest (a carry into the
-// exponent is the next binade), lo the exact rest, at most 12 bits, of which it keeps 11; the cut leans to neither
-// side since the rest has either sign.  A NaN that the carry turns into a zero in hi stays in lo.
+// exponent is the next binade, but for the last, whose largest TF32 value takes what would become an infinity), lo
+// the exact rest, at most 12 bits, of which it keeps 11; the cut leans to neither side since the rest has either sign.
+// An infinity or a NaN is in lo.
 struct Tf32Pair {
   unsigned hi, lo;
   __device__ __forceinline__ explicit Tf32Pair(float x) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    float h;  // the smaller magnitude, with x's sign
+    asm("min.xorsign.abs.f32 %0, %1, %2;\n" : "=f"(h) : "f"(__uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u)), "f"(3.40116213421e38f));
+    hi = __float_as_uint(h);
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
   }
 };

@@ -77,3 +77,27 @@ def test_attn_a_page_that_one_row_sees_must_be_there(torch):
     got = c.run(torch, window=20)
     assert bool(got[:3].isnan().all()) and rel(got[3], ref[3]) <= TOL["bf16"]
     assert nat.gdn_device_status(reset=True) == nat.GDN_DEVICE_BAD_PAGE
+
+
+# ------------------------------------------------------------------ attention: f32's largest values
+
+
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 12), (128, 3), (256, 2)])
+def test_attn_f32_largest_values(torch, dim, group):
+    """Values and keys up to f32's largest are finite in their TF32 halves too: one key's value comes back (to
+    2^-22), a key with the lowest value is as good as masked where the score says so."""
+    c = Case(torch, "f32", [1, 3, 40], dim=dim, group=group, n_kv=1, page=4)
+    top = torch.finfo(torch.float32).max
+    p = int(c.table[0, 0])
+    c.v[p, 0, 0, ::2], c.v[p, 0, 0, 1::2] = top, -top
+    # request 1: q is positive in its first element only, keys 0 and 2 have f32's lowest there: scores of -1e35 and less
+    row = c.q[1].zero_()
+    row[:, 0] = 1e-3
+    p = int(c.table[1, 0])
+    c.k[p, 0, 0, 0], c.k[p, 0, 2, 0] = -top, -top
+    c.k[p, 0, 1, 0] = 1.0
+    c.v[p, 0, 0] = top / 2
+    c.q_dev.copy_(c.q), c.k_dev.copy_(c.k), c.v_dev.copy_(c.v)
+    got, ref = c.run(torch), c.reference(torch)
+    for r in range(3):
+        assert rel(got[r], ref[r]) <= TOL["f32"]
