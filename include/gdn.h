@@ -487,7 +487,10 @@ typedef struct gdn_rope_params {
  * outside (0, head_dim], an axis_of_pair entry >= n_axes, unknown flags or
  * dtype, pointers not aligned to an element, token strides below a row's
  * length, an output that overlaps another buffer (other than exactly its own
- * input); UNSUPPORTED for GDN_ROPE_INVERSE with gdn_rope_store.  Any alignment
+ * input; k_cache and v_cache may lie among one another, as views of one array,
+ * while no row of one shares a byte with one of the other), cache strides of which one
+ * is below what the smaller ones and a row cover (gdn_rope_store; strides over an
+ * extent of 1 do not count); UNSUPPORTED for GDN_ROPE_INVERSE with gdn_rope_store.  Any alignment
  * and strides are taken; 16-byte aligned rows go 16 bytes at a time.
  */
 gdn_status gdn_rope(const void *q, const void *k, const int32_t *positions, const float *cos_sin,

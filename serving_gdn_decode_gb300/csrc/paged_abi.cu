@@ -77,7 +77,7 @@ struct Cache {
   unsigned long long es;
 };
 
-// The cache's extent, and that no two rows of it share an element.
+// The sizes and strides alone, and the cache's extent.  What is only read may share rows.
 gdn_status check_cache(const Cache &c, unsigned long long *bytes) {
   if (c.n_pages == 0 || c.page_size == 0)
     return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: n_pages and page_size must be > 0");
@@ -95,6 +95,46 @@ gdn_status check_cache(const Cache &c, unsigned long long *bytes) {
   *bytes = static_cast<unsigned long long>(elems) * c.es;
   return GDN_OK;
 }
+
+// What is stored into: each stride over an extent above 1 passes what the smaller ones cover, so that no two rows
+// share an element.
+class StoredCache {
+ public:
+  explicit StoredCache(const Cache &c) : row_(static_cast<int64_t>(c.dim * c.es)) {
+    const struct { uint32_t extent; int64_t stride; } all[] = {
+        {c.n_pages, c.page_stride}, {c.n_kv, c.head_stride}, {c.page_size, c.slot_stride}};
+    for (const auto &x : all) {
+      if (x.extent <= 1) continue;
+      int i = n_++;
+      for (; i > 0 && dims_[i - 1].stride < x.stride * static_cast<int64_t>(c.es); --i) dims_[i] = dims_[i - 1];
+      dims_[i] = Dim{x.extent, x.stride * static_cast<int64_t>(c.es)};
+    }
+  }
+  bool rows_apart() const {
+    int64_t covered = row_;
+    for (int i = n_ - 1; i >= 0; --i) {
+      if (dims_[i].stride < covered) return false;
+      covered += (dims_[i].extent - 1) * dims_[i].stride;
+    }
+    return true;
+  }
+  // Whether a cache of the same layout, `d` bytes on, shares a byte with this one (rows_apart() holds): whether d is
+  // a difference of two places.  The smaller strides reach less far than the one at hand, so only the two multiples
+  // of it on either side of d can be part of it.
+  bool meets(int64_t d, int i = 0) const {
+    if (i == n_) return -row_ < d && d < row_;
+    const int64_t s = dims_[i].stride, below = d / s - (d % s < 0), most = dims_[i].extent - 1;
+    for (int64_t x = below; x <= below + 1; ++x)
+      if (-most <= x && x <= most && meets(d - x * s, i + 1)) return true;
+    return false;
+  }
+
+ private:
+  struct Dim { int64_t extent, stride; };  // in bytes, the largest first
+  Dim dims_[3];
+  int n_ = 0;
+  int64_t row_;
+};
 
 gdn_status run_rope(const gdn::RopeArgs &x, bool store, const gdn_rope_params *params, gdn_stream_t stream) {
   gdn::g_last_error[0] = '\0';
@@ -131,11 +171,15 @@ gdn_status run_rope(const gdn::RopeArgs &x, bool store, const gdn_rope_params *p
   if (p.positions_stride < 0 || p.positions_stride > (int64_t{1} << 40))
     return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: positions_stride must lie in [0, 2^40]");
   unsigned long long cache_bytes = 0;
+  Cache cache{};
   if (store) {
-    const gdn_status r = check_cache(Cache{p.n_pages, p.page_size, p.n_kv_heads, p.head_dim, p.cache_page_stride,
-                                           p.cache_head_stride, p.cache_slot_stride, es}, &cache_bytes);
+    cache = Cache{p.n_pages, p.page_size, p.n_kv_heads, p.head_dim, p.cache_page_stride, p.cache_head_stride, p.cache_slot_stride, es};
+    const gdn_status r = check_cache(cache, &cache_bytes);
     if (r != GDN_OK) return r;
   }
+  const StoredCache stored(cache);
+  if (store && !stored.rows_apart())
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: the cache strides let rows overlap");
   if (t == 0) return GDN_OK;
   const Rows in[] = {{a.q, t, qb, es * p.q_stride, "q"},
                      {a.k, t, kb, es * p.k_stride, "k"},
@@ -169,7 +213,8 @@ gdn_status run_rope(const gdn::RopeArgs &x, bool store, const gdn_rope_params *p
     for (int i = 0; i < o; ++i) {
       // k_cache and v_cache may be two views of one array: pages of K and V in turn, or heads, or slots
       if (o == 2 && i == 1) {
-        if (out[o].p == out[i].p) return overlap_error(out[o], out[i]);
+        if (store && stored.meets(static_cast<int64_t>(reinterpret_cast<uintptr_t>(out[o].p) - reinterpret_cast<uintptr_t>(out[i].p))))
+          return overlap_error(out[o], out[i]);
         continue;
       }
       if (rows_overlap(out[o], out[i])) return overlap_error(out[o], out[i]);
