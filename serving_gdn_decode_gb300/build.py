@@ -4,7 +4,9 @@ and the compiled torch binding of the full-attention operators beside it.
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
 shared library next to this file.  ptxas register/spill reports go to
 ``_build/ptxas.log``.  ``csrc/paged_binding.cpp`` compiles with g++ against the
-installed torch's headers.  Run as ``python -m serving_gdn_decode_gb300.build``.
+installed torch's headers; the library itself needs neither, and where torch is
+not installed it is all that is built.  Run as
+``python -m serving_gdn_decode_gb300.build``.
 """
 from __future__ import annotations
 
@@ -45,14 +47,30 @@ def _sources() -> list[str]:
 def _deps() -> list[str]:
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "gdn.h"),
-                                                         os.path.abspath(__file__), BINDING_SRC]
+                                                         os.path.abspath(__file__)]
+
+
+def _newer(out: str, deps: list[str]) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    """Whether the binding is there, for this library's header, this Python and this torch."""
+    try:
+        with open(_stamp_path()) as f:
+            stamp = f.read()
+    except OSError:
+        return False
+    return stamp == _binding_stamp() and _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "gdn.h"),
+                                                         os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _lib_up_to_date() and (_torch_root() is None or _binding_up_to_date())
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -64,16 +82,29 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _torch_root() -> str:
+def _torch_root() -> str | None:
     import importlib.util
     spec = importlib.util.find_spec("torch")  # its place only: importing it takes seconds
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the binding of the full-attention operators needs its headers")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
-def _compile_binding() -> str:
-    root = _torch_root()
+def _stamp_path() -> str:
+    return os.path.join(BUILD, "paged_binding.for")
+
+
+def _binding_stamp() -> str:
+    """What a binding is compiled for: one of another Python or torch would not load, or worse, would."""
+    import importlib.metadata
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"python {sys.version}\ntorch {version} in {_torch_root()}\n"
+
+
+def _compile_binding(root: str) -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "paged_binding.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"],
@@ -85,8 +116,8 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str) -> None:
-    libs = os.path.join(_torch_root(), "lib")
+def _link_binding(root: str, obj: str) -> None:
+    libs = os.path.join(root, "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-L", libs, "-ltorch_python",
            "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
@@ -94,17 +125,14 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(_stamp_path(), "w") as f:
+        f.write(_binding_stamp())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_lib() -> None:
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
         results = list(ex.map(_compile, srcs))
-        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"==== {os.path.basename(src)}\n{log}\n")
@@ -114,9 +142,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    root = _torch_root()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding, root) if root and (force or not _binding_up_to_date()) else None
+        if force or not _lib_up_to_date():
+            _build_lib()
+    if binding is not None:  # whatever became of it, the library is there
+        _link_binding(root, binding.result())
     if verbose:
         print(f"built {LIB}")
+        if root is None:
+            print("torch is not installed: the full-attention operators are in the library, their torch binding was not built")
     return LIB
 
 
