@@ -4,8 +4,8 @@ and ``gdn_attn_paged`` of ``include/gdn.h``.
 
 Argument marshalling only, as in ``_native``, here by the compiled module
 ``_paged_binding``: shapes, strides and dtypes become the params struct of the C
-call, which checks the rest.  There is no fallback: if the module is missing,
-importing this one raises.
+call, which checks the rest.  There is no fallback: if the module is missing or
+cannot load, every call raises.
 
 The paged cache: ``k_cache`` and ``v_cache`` of shape [n_pages, n_kv_heads,
 page_size, head_dim], f32 or bf16, with any strides over contiguous rows of
@@ -21,8 +21,15 @@ from __future__ import annotations
 try:
     from . import _paged_binding as _binding
 except ImportError as e:
-    raise RuntimeError("_paged_binding.so is missing or cannot load: build it with "
-                       "`python -m serving_gdn_decode_gb300.build` (there is no fallback)") from e
+    class _Missing:
+        def __init__(self, cause):
+            self._cause = cause
+
+        def __getattr__(self, name):
+            raise RuntimeError("_paged_binding.so is missing or cannot load: build it with "
+                               "`python -m serving_gdn_decode_gb300.build` (there is no fallback)") from self._cause
+
+    _binding = _Missing(e)
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2

@@ -3,6 +3,8 @@ CUDA toolkit alone gets the library, and a binding compiled for another torch is
 taken for this one's."""
 import os
 import shutil
+import subprocess
+import sys
 
 import pytest
 
@@ -59,3 +61,21 @@ def test_a_binding_of_another_torch_is_stale(small, monkeypatch):
     before = os.stat(b.BINDING).st_ino
     b.build()
     assert b.up_to_date() and os.stat(b.BINDING).st_ino != before and os.path.getmtime(b.LIB) == lib_time
+
+
+def test_a_missing_binding_is_an_error_of_its_calls_only():
+    """Without it everything else imports as ever, by name and by star, and the calls that need it say what is missing."""
+    code = ("import sys\n"
+            "sys.modules['serving_gdn_decode_gb300._paged_binding'] = None\n"
+            "from serving_gdn_decode_gb300 import *\n"
+            "assert pack_params(64, 64, 1, 1, 1, 1) is not None and gdn_forward and GdnError\n"
+            "for call in (lambda: gdn_rope(*[None] * 6), lambda: gdn_rope_store(*[None] * 9), lambda: gdn_kv_plan(*[None] * 14),\n"
+            "             lambda: gdn_attn_paged(*[None] * 8), lambda: gdn_attn_workspace_size(None, None, 1)):\n"
+            "    try:\n"
+            "        call()\n"
+            "    except RuntimeError as e:\n"
+            "        assert 'serving_gdn_decode_gb300.build' in str(e), e\n"
+            "    else:\n"
+            "        raise AssertionError('no error')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=b.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
