@@ -1295,8 +1295,6 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
   });
 }
 
-cudaError_t attn_paged_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  return read_paged_status(bits, reset, stream);
-}
+cudaError_t attn_paged_status_word(unsigned int **word) { return paged_status_word(word); }
 
 }  // namespace gdn

@@ -973,8 +973,6 @@ cudaError_t launch_chunked(const Problem &p, cudaStream_t stream) {
   return p.decay_after ? launch<true, true, false>(p, stream) : launch<false, true, false>(p, stream);
 }
 
-cudaError_t chunked_wait_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  return chunked::read_wait_status(bits, reset, stream);
-}
+cudaError_t chunked_status_word(unsigned int **word) { return chunked::wait_status_word(word); }
 
 }  // namespace gdn

@@ -1339,8 +1339,6 @@ cudaError_t launch_chunked_split_noalloc(const Problem &p, cudaStream_t stream) 
   return launch_chunked_split(p, ws, stream);
 }
 
-cudaError_t chunked_split_wait_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  return chunked::read_wait_status(bits, reset, stream);
-}
+cudaError_t chunked_split_status_word(unsigned int **word) { return chunked::wait_status_word(word); }
 
 }  // namespace gdn

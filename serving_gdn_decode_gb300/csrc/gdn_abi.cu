@@ -11,7 +11,6 @@
 #include "../../include/gdn.h"
 #include "abi_common.h"
 #include "gdn_internal.h"
-#include "paged_internal.h"
 
 namespace gdn {
 
@@ -553,15 +552,11 @@ gdn_status gdn_device_status(uint32_t *status, int reset, gdn_stream_t stream) {
   g_last_error[0] = '\0';
   if (status == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: status is NULL");
   *status = 0;
-  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  unsigned int one = 0, two = 0;
-  cudaError_t err = gdn::chunked_wait_status(&one, reset != 0, cs);
-  if (err == cudaSuccess) err = gdn::chunked_split_wait_status(&two, reset != 0, cs);
-  unsigned int paged = 0;
-  if (err == cudaSuccess) err = gdn::paged_status(&paged, reset != 0, cs);
+  unsigned int bits = 0;
+  const cudaError_t err = gdn::read_device_status(&bits, reset != 0, reinterpret_cast<cudaStream_t>(stream));
   if (err != cudaSuccess)
     return fail(GDN_ERR_CUDA, "gdn: reading the device status failed: %s", cudaGetErrorString(err));
-  *status = one | two | paged;
+  *status = bits;
   return GDN_OK;
 }
 

@@ -206,8 +206,6 @@ cudaError_t launch_kv_plan(const PlanArgs &a, cudaStream_t stream) {
   return launch_in_order(gdn_kv_plan_kernel<1024>, dim3(ctas), 1024, 0, stream, a, page);
 }
 
-cudaError_t kv_plan_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  return read_paged_status(bits, reset, stream);
-}
+cudaError_t kv_plan_status_word(unsigned int **word) { return paged_status_word(word); }
 
 }  // namespace gdn

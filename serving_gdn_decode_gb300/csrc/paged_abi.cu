@@ -9,19 +9,6 @@
 #include "abi_common.h"
 #include "paged_internal.h"
 
-namespace gdn {
-
-cudaError_t paged_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  unsigned int a = 0, b = 0, c = 0;
-  cudaError_t e = kv_plan_status(&a, reset, stream);
-  if (e == cudaSuccess) e = rope_status(&b, reset, stream);
-  if (e == cudaSuccess) e = attn_paged_status(&c, reset, stream);
-  *bits = a | b | c;
-  return e;
-}
-
-}  // namespace gdn
-
 namespace {
 
 using gdn::aligned;

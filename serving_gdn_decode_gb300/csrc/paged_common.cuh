@@ -40,18 +40,9 @@ cudaError_t launch_in_order(void (*kernel)(P...), dim3 grid, unsigned threads, s
 
 __device__ __forceinline__ void report(unsigned int bits) { atomicOr(&g_paged_status, bits); }
 
-// Host: *bits = this translation unit's word after all work on `stream` so
-// far; cleared afterwards when `reset`.  Symbol copies only; synchronises.
-inline cudaError_t read_paged_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  unsigned int h = 0u;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&h, g_paged_status, sizeof h, 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess && reset) {
-    static const unsigned int zero = 0u;
-    e = cudaMemcpyToSymbolAsync(g_paged_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
-  }
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  *bits = e == cudaSuccess ? h : 0u;
-  return e;
+// Host: the word's address on the current device.
+inline cudaError_t paged_status_word(unsigned int **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_paged_status);
 }
 
 }  // namespace

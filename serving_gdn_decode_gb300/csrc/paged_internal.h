@@ -54,11 +54,9 @@ struct AttnArgs {
 size_t attn_workspace_bytes(const gdn_attn_params &p);
 cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream);
 
-// Failure bits of the three files' kernels on the current device, as
-// chunked_wait_status.
-cudaError_t kv_plan_status(unsigned int *bits, bool reset, cudaStream_t stream);
-cudaError_t rope_status(unsigned int *bits, bool reset, cudaStream_t stream);
-cudaError_t attn_paged_status(unsigned int *bits, bool reset, cudaStream_t stream);
-cudaError_t paged_status(unsigned int *bits, bool reset, cudaStream_t stream);  // all three
+// The status words of the three files' kernels on the current device (read_device_status).
+cudaError_t kv_plan_status_word(unsigned int **word);
+cudaError_t rope_status_word(unsigned int **word);
+cudaError_t attn_paged_status_word(unsigned int **word);
 
 }  // namespace gdn

@@ -457,8 +457,6 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
   return a.p.dtype == GDN_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, stream) : launch_type<float>(a, stream);
 }
 
-cudaError_t rope_status(unsigned int *bits, bool reset, cudaStream_t stream) {
-  return read_paged_status(bits, reset, stream);
-}
+cudaError_t rope_status_word(unsigned int **word) { return paged_status_word(word); }
 
 }  // namespace gdn
