@@ -99,7 +99,9 @@ bool want_rows(const Arg &a, at::ScalarType t, int64_t n, int64_t heads, int64_t
 template <typename P>
 bool want_cache(const Arg &k, const Arg &v, at::ScalarType t, int64_t dim, P *p, uint32_t *n_kv) {
   if (!want_type(k, t) || !want_type(v, t)) return false;
-  if (k->dim() != 4 || k->sizes() != v->sizes() || k->strides() != v->strides())
+  bool one_layout = k->dim() == 4 && k->sizes() == v->sizes();
+  for (int i = 0; one_layout && i < 4; ++i) one_layout = k->size(i) <= 1 || k->stride(i) == v->stride(i);
+  if (!one_layout)
     return fail(GDN_ERR_INVALID_ARGUMENT,
                 "k_cache and v_cache must be [n_pages, n_kv_heads, page_size, head_dim] of one layout");
   if (k->size(3) != dim || (*n_kv && k->size(1) != *n_kv))

@@ -78,3 +78,18 @@ def test_cache_overlap_against_enumeration(L):  # noqa: F811
             assert refused(st, "overlap") == nat.GDN_ERR_INVALID_ARGUMENT
         seen[clean] += 1
     assert min(seen.values()) > 400
+
+
+def test_strides_over_one_element_make_no_layout(L):  # noqa: F811
+    """A cache of one key head as it is and one whose heads and slots are swapped lie alike in memory (refused here
+    for being on the host, after every other check)."""
+    import torch
+
+    from test_paged_host import call
+    f = torch.zeros
+    for k, v in ((f(5, 1, 8, 64), f(5, 8, 1, 64).transpose(1, 2)), (f(1, 2, 8, 64), f(3, 2, 8, 64)[:1].as_strided((1, 2, 8, 64), (7, 512, 64, 1)))):
+        for op, more in (("attn_paged", {}), ("rope_store", dict(k=f(2, k.size(1), 64), v=f(2, k.size(1), 64)))):
+            with pytest.raises(nat.GdnError, match="must be a CUDA tensor"):
+                call(op, k_cache=k, v_cache=v, **more)
+    with pytest.raises(nat.GdnError, match="one layout"):
+        call("attn_paged", k_cache=f(5, 2, 8, 64), v_cache=f(5, 8, 2, 64).transpose(1, 2))
