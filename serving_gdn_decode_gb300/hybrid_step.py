@@ -64,10 +64,12 @@ class Model:
 
 
 class Server:
-    """The state of `requests` requests: recurrent states, the paged cache and its plan."""
+    """The state of `requests` requests of up to `tokens` tokens: recurrent states, the paged cache and its plan."""
 
     def __init__(self, model: Model, requests: int, prompt: int, tokens: int):
         cfg, dev, s = model.cfg, model.device, requests
+        if tokens > cfg.max_tokens:  # past the table of cosines the rotated q and k would be NaN
+            raise ValueError(f"{tokens} tokens per request, but the model has {cfg.max_tokens} positions")
         self.model, self.requests = model, s
         self.max_pages = -(-tokens // cfg.page)
         self.n_pages = s * self.max_pages
@@ -134,10 +136,10 @@ def generate(model: Model, prompts: torch.Tensor, steps: int):
     """Greedy tokens after `prompts` [requests, prompt] and the last step's logits: one step for the
     prompts, then `steps` decode steps as replays of one captured step."""
     s, prompt = prompts.shape
-    server = Server(model, s, prompt, prompt + steps + 1)
-    ids = server.step(prompts.reshape(-1), prompt).argmax(-1)
+    server = Server(model, s, prompt, prompt + steps)
+    logits = server.step(prompts.reshape(-1), prompt).clone()
+    ids = logits.argmax(-1)
     out = [ids.clone()]
-    logits = torch.empty(s, model.cfg.vocab, device=prompts.device)
 
     def decode():
         logits.copy_(server.step(ids, 1))

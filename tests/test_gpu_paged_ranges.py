@@ -101,3 +101,16 @@ def test_attn_f32_largest_values(torch, dim, group):
     got, ref = c.run(torch), c.reference(torch)
     for r in range(3):
         assert rel(got[r], ref[r]) <= TOL["f32"]
+
+
+# ------------------------------------------------------------------ the example
+
+
+@pytest.mark.parametrize("steps", [0, 1, 2])
+def test_hybrid_example_of_few_steps(torch, capsys, steps):
+    """Without a decode step the logits are the prompts'; with one, nothing is captured yet.  The bound is
+    test_hybrid_example's."""
+    from serving_gdn_decode_gb300 import hybrid_step
+    args = ["--requests", "3", "--prompt", "17", "--steps", str(steps), "--check"]
+    assert hybrid_step.main(args) <= 1e-3
+    assert "device status 0" in capsys.readouterr().out
