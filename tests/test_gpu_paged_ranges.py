@@ -6,7 +6,7 @@ import math
 
 import pytest
 
-from test_gpu_paged import TOL, Case, clean_status, dtype_of, rel, torch  # noqa: F401 (fixtures among them)
+from test_gpu_paged import ROPE_TOL, TOL, Case, clean_status, dtype_of, rel, table_of, torch  # noqa: F401 (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -101,6 +101,97 @@ def test_attn_f32_largest_values(torch, dim, group):
     got, ref = c.run(torch), c.reference(torch)
     for r in range(3):
         assert rel(got[r], ref[r]) <= TOL["f32"]
+
+
+# ------------------------------------------------------------------ attention: wide rows, long and split; prompts among decodes
+
+
+def check_rows(torch, c, dtype, **kw):
+    ref, got = c.reference(torch, **kw), c.run(torch, **kw)
+    for row in range(len(ref)):
+        assert rel(got[row], ref[row]) <= ROW_TOL[dtype], row
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("page", [24, 32])
+@pytest.mark.parametrize("group,wins", [(16, (1, 1, 1)), (32, (1, 1, 1)), (40, (1, 1, 1)), (64, (1, 1, 1)), (8, (7, 1, 4))])
+def test_attn_wide_rows_over_long_keys(torch, dtype, dim, page, group, wins):
+    """Blocks of 16, 32 and 64 rows per key head whose items are split over many CTAs and joined, on pages that hold
+    whole tiles and on pages that do not; every row by itself."""
+    check_rows(torch, Case(torch, dtype, [5003, 64, 1711], wins=list(wins), dim=dim, group=group, n_kv=1, page=page), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group", [(64, 4), (128, 8), (256, 2)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_attn_prompts_among_decodes(torch, dtype, dim, group, window):
+    """A step with whole prompts, the rest of one, and single tokens: many row blocks per request."""
+    c = Case(torch, dtype, [150, 900, 333, 1, 70], wins=[150, 1, 41, 1, 70], dim=dim, group=group, n_kv=2, page=16)
+    check_rows(torch, c, dtype, window=window)
+
+
+# ------------------------------------------------------------------ rope: prompts
+
+
+def rope_all(torch, x, pos, table, axes, inter, sign=1.0):
+    """rope_reference of many tokens: all pairs at once, in 64 bits on the GPU."""
+    half = table.shape[1] // 2
+    at = pos.long()[torch.tensor(list(axes), device="cuda")].T  # [tokens, pairs]
+    j = torch.arange(half, device="cuda")
+    c, s = table[at, j].double()[:, None], sign * table[at, half + j].double()[:, None]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if inter else (slice(0, half), slice(half, 2 * half))
+    y = x.double().clone()
+    y[..., a] = x[..., a].double() * c - x[..., b].double() * s
+    y[..., b] = x[..., b].double() * c + x[..., a].double() * s
+    return y
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [4001, 20011])  # one to a few parts per token, several steps of rows each
+@pytest.mark.parametrize("n_q,n_kv,dim,rot,axes,inter", [(32, 8, 128, 128, 3, False), (7, 1, 64, 64, 2, False), (16, 2, 256, 64, 1, True),
+                                                       (5, 3, 128, 128, 2, True), (3, 1, 256, 256, 1, False), (6, 2, 72, 72, 2, False),
+                                                       (9, 3, 34, 20, 2, False)])
+def test_rope_and_store_of_prompts(torch, dtype, n, n_q, n_kv, dim, rot, axes, inter):
+    """Every form of both kernels over prompts: the store into a paged cache with q in place in the fused rows, and
+    the rotation there and back."""
+    import serving_gdn_decode_gb300 as gdn
+    dt, page = dtype_of(torch, dtype), 16
+    g = torch.Generator(device="cuda").manual_seed(n + dim)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).to(dt)  # noqa: E731
+    fused = rand(n, (n_q + 2 * n_kv) * dim)
+    q, k, v = (x.unflatten(1, (-1, dim)) for x in fused.split([n_q * dim, n_kv * dim, n_kv * dim], 1))
+    table = table_of(torch, 500, rot).cuda()
+    pos = torch.randint(0, 500, (axes, n), device="cuda", generator=g).to(torch.int32)
+    of_pair = bytes(j * axes // (rot // 2) for j in range(rot // 2))
+    pages = n // page + 2
+    kc, vc = rand(pages, n_kv, page, dim), rand(pages, n_kv, page, dim)
+    slots = torch.randperm(pages * page, device="cuda", generator=g)[:n].to(torch.int32)
+    slots[::61] = -1
+    before = [x.clone() for x in (q, k, v, kc, vc)]
+    tol = ROPE_TOL[dtype]
+
+    qo, ko = torch.empty_like(before[0]), torch.empty_like(before[1])
+    gdn.gdn_rope(q, k, pos, table, qo, ko, axes=of_pair, interleaved=inter)
+    for got, x in ((qo, before[0]), (ko, before[1])):
+        want = rope_all(torch, x, pos, table, of_pair, inter)
+        assert rel(got, want) <= tol and torch.equal(got[..., rot:], x[..., rot:])
+        per_token = (got.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+        assert float(per_token.max()) <= 2.5 * tol  # of a token's elements alone: bf16's largest roundings are twice its usual ones
+    gdn.gdn_rope(qo, ko, pos, table, qo, ko, axes=of_pair, interleaved=inter, inverse=True)
+    assert rel(qo, before[0]) <= 2 * tol and rel(ko, before[1]) <= 2 * tol
+
+    gdn.gdn_rope_store(q, k, v, pos, table, slots, kc, vc, q, axes=of_pair, interleaved=inter)
+    assert rel(q, rope_all(torch, before[0], pos, table, of_pair, inter)) <= tol
+    assert torch.equal(k, before[1]) and torch.equal(v, before[2])
+    flat = lambda x: x.transpose(1, 2).reshape(-1, n_kv, dim)  # noqa: E731
+    has = slots >= 0
+    at = slots[has].long()
+    assert torch.equal(flat(vc)[at], before[2][has])
+    assert rel(flat(kc)[at], rope_all(torch, before[1], pos, table, of_pair, inter)[has]) <= tol
+    rest = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(flat(kc)[rest], flat(before[3])[rest]) and torch.equal(flat(vc)[rest], flat(before[4])[rest])
 
 
 # ------------------------------------------------------------------ the example
