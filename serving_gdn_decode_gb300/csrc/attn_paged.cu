@@ -42,7 +42,7 @@
 // on into the next items, so that the ring does not drain between them.
 //
 // Precision.  f32: each operand is split in two TF32 halves and three products
-// are taken, so a product is good to 3 * 2^-22.  bf16: K, V and q are exact in the
+// are taken, so a product is good to 2^-20.  bf16: K, V and q are exact in the
 // products; the probabilities are split in two bf16 halves (two products instead
 // of one: bytes, not products, bound the kernel), each off by 2^-16 of itself at
 // most, to either side: a 256th of what the result's one rounding, at the end,
@@ -105,16 +105,33 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const unsigned (&a)[4], 
 }
 
 // x = hi + lo up to 2^-23 |x|, both with TF32's 10 mantissa bits: hi is x rounded to nearest (a carry into the
-// exponent is the next binade, but for the last, whose largest TF32 value takes what would become an infinity), lo
-// the exact rest, at most 12 bits, of which it keeps 11; the cut leans to neither side since the rest has either sign.
-// An infinity or a NaN is in lo.
+// exponent is the next binade), lo the exact rest, at most 12 bits, of which the matrix instruction reads 11; the cut
+// leans to neither side since the rest has either sign.  From 3.4026e38 on the carry would make hi an infinity and lo
+// the other one; with TOP hi stops at TF32's largest value and the rest, an infinity or a NaN too, is in lo.
+template <bool TOP>
 struct Tf32Pair {
   unsigned hi, lo;
   __device__ __forceinline__ explicit Tf32Pair(float x) {
-    float h;  // the smaller magnitude, with x's sign
-    asm("min.xorsign.abs.f32 %0, %1, %2;\n" : "=f"(h) : "f"(__uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u)), "f"(3.40116213421e38f));
-    hi = __float_as_uint(h);
-    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    if constexpr (TOP) {
+      float h;  // the smaller magnitude, with x's sign
+      asm("min.xorsign.abs.f32 %0, %1, %2;\n" : "=f"(h) : "f"(__uint_as_float(hi)), "f"(3.40116213421e38f));
+      hi = __float_as_uint(h);
+    }
+    lo = __float_as_uint(x - __uint_as_float(hi));
+  }
+};
+// x = hi + lo, hi being x cut to TF32, which is finite where x is, lo the exact rest, at most 13 bits: rounded to
+// nearest by the addition and the instruction's cut (ROUND: up to 2^-22 |x|), or cut (up to 2^-21 |x|, 2^-23 on
+// average, towards zero; f32's largest value would round up to an infinity).  An infinity or a NaN is in hi, a NaN whose
+// payload is in its 13 low bits alone as an infinity.  Beside the other split's lo, which has either sign, the product
+// lo * lo that is left out is below 2^-21 and leans to neither side.
+template <bool ROUND>
+struct Tf32Cut {
+  unsigned hi, lo;
+  __device__ __forceinline__ explicit Tf32Cut(float x) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + (ROUND ? 0x1000u : 0u);
   }
 };
 
@@ -148,7 +165,6 @@ struct Call {
   FastDiv page_div, group_div;
   bool whole_tiles;  // pages hold whole tiles
   bool whole_items;  // no item is split
-  bool short_sums;   // no item has more than kShortKeys keys
   bool out_wide;     // output rows are aligned to four elements
 };
 
@@ -360,6 +376,10 @@ struct Warp<__nv_bfloat16, D, NT, RW> {
 template <int D, int NT, int RW>
 struct Warp<float, D, NT, RW> {
   using S = Shape<float, D, 1>;
+  // Heads of 64, 16/16, 24 requests, window 1000: 33.5 us with Tf32Pair, 36.4 with Tf32Cut (whose form spills);
+  // 64 requests up to 4096 keys, 32/8 heads of 128: 186 and 175; 8/4 heads of 256: 174 and 156.
+  using KeyHalves = std::conditional_t<D == 64, Tf32Pair<true>, Tf32Cut<true>>;
+  using ValueHalves = std::conditional_t<D == 64, Tf32Pair<true>, Tf32Cut<false>>;
   static constexpr int kQRow = 2 * D + 8;  // (hi, lo) pairs, padded
   static constexpr int kQSmem = RW * NT * 8 * kQRow * 4;
   unsigned k_at[4], v_at[8], q_at;
@@ -391,7 +411,7 @@ struct Warp<float, D, NT, RW> {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int at = threadIdx.x + i * 128, col = at % (D / 4) * 4;
-      const Tf32Pair a(x[i][0]), b(x[i][1]), c(x[i][2]), d(x[i][3]);
+      const Tf32Pair<true> a(x[i][0]), b(x[i][1]), c(x[i][2]), d(x[i][3]);
       uint4 *to = qs + (at / (D / 4) * kQRow + col * 2) / 4;
       to[0] = make_uint4(a.hi, a.lo, b.hi, b.lo);
       to[1] = make_uint4(c.hi, c.lo, d.hi, d.lo);
@@ -415,7 +435,7 @@ struct Warp<float, D, NT, RW> {
         ldmatrix_x4(a, k_tile + k_at[i] + k4 * 128);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const Tf32Pair x(__uint_as_float(a[j]));
+          const KeyHalves x(__uint_as_float(a[j]));
           a[j] = x.hi;
           lo[j] = x.lo;
         }
@@ -447,7 +467,7 @@ struct Warp<float, D, NT, RW> {
         for (int b = 0; b < 4; ++b) {
           const float x = __shfl_sync(kFull, p[nt][(b >> 1) * 2], src + (b & 1) * 16);
           const float y = __shfl_sync(kFull, p[nt][(b >> 1) * 2 + 1], src + (b & 1) * 16);
-          const Tf32Pair t(odd ? y : x);
+          const Tf32Pair<false> t(odd ? y : x);  // at most 2^8
           hi[nt][b] = t.hi;
           lo[nt][b] = t.lo;
         }
@@ -466,7 +486,7 @@ struct Warp<float, D, NT, RW> {
           asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x)
                        : "r"(v_tile + w.v_at[(md & 1) * 4 + (i & 1) * 2 + (i >> 1)] + (md >> 1) * 128 + h * 8 * S::kRowBytes)
                        : "memory");
-          const Tf32Pair t(x);
+          const ValueHalves t(x);
           hi[h][i] = t.hi;
           lo[h][i] = t.lo;
         }
@@ -523,14 +543,15 @@ constexpr int ctas_per_sm() {
 
 // The tensor cores cut the low bits of a running sum at every product, always towards zero: over n products a sum
 // kept there leans by up to n 2^-24 of itself (6.9e-3 over 2^20 keys, measured).  So a tile's sum starts at zero and
-// is added in f32, rounded to nearest.  The additions cost nothing where registers are left for a tile's sums; where
-// the accumulators take 64 registers or a warp has two row tiles they spill (32 requests up to 8191 keys, windows of
-// 1 to 4, 16/2 heads of 256: 65.0 against 61.3 us), and there a call whose table's width or window holds an item to
-// kShortKeys keys keeps its sums in the tensor cores: 1024 products at most, 2^-14 of the sum, a 32nd of the result's
-// rounding to bf16.
-constexpr uint64_t kShortKeys = 8192;
+// is added in f32, rounded to nearest.  That costs bf16 a few registers and the latency of a product, where there are
+// few of either (64 requests up to 8192 keys, windows of 1 to 7, 8 heads of 128 per key head: 274 us, and 248 with the
+// sums in the tensor cores; of 256: 288 and 276; 32 requests, windows of 1 to 4, 8 of 256: 65 and 61; heads of 64 and
+// 32 rows: 237 and 229; heads of 128 with one row tile: equal).  There the part of an item that lies in a CTA keeps its
+// sums in the tensor cores if it has at most kShortKeys keys per key group: 1024 products, 2^-14 of the sum, a 32nd of
+// the result's rounding to bf16.  At 128 elements its edge tiles do not, for the registers.
+constexpr int kShortKeys = 8192;
 template <typename T, int D, int NT>
-constexpr bool kTightRegisters = sizeof(T) == 2 && (D == 256 || NT > 1);
+constexpr bool kKeepsShortSums = sizeof(T) == 2 && (D != 128 || NT > 1);
 
 // Four neighbouring results, rounded once; in one store where rows are aligned to it.
 __device__ __forceinline__ void put4(float *o, const float (&x)[4], bool wide) {
@@ -842,13 +863,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    auto add = [&](int md, const float (&y)[NT][4]) {  // a tile's sums to the running ones
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[md][nt][j] += y[nt][j];
-    };
-
+    const bool short_sums = it.k1 - it.k0 <= kShortKeys * KW;
     const int n_tiles = it.tiles_of(kg);
     int key0 = it.k0 + kTile * kg;
     bool bad_page = false;
@@ -857,12 +872,9 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       // scores
       arrived();
       float s[KT][NT][4];
+      const bool edge = key0 + kTile > all1 || key0 < all0;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) w.scores(s[kt], ring + slot * S::kHalf + kt * kSub * S::kRowBytes, q_smem);
-      bad_page |= bad_slots >> slot & 1;
-      slot = slot + 1 == kRing ? 0 : slot + 1;
-      const bool edge = key0 + kTile > all1 || key0 < all0;
-      bool grown = false;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -881,6 +893,9 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
               if (key > hi || key <= lo) s[kt][nt][j] = -INFINITY;
             }
       }
+      bad_page |= bad_slots >> slot & 1;
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      bool grown = false;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -930,32 +945,29 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
       arrived();
       const unsigned v_tile = ring + slot * S::kHalf;
       slot = slot + 1 == kRing ? 0 : slot + 1;
-      if (!edge) {
-        if constexpr (kTightRegisters<T, D, NT>) {
-          if (c.short_sums) {
-#pragma unroll
-            for (int md = 0; md < D / 16; ++md) {
-#pragma unroll
-              for (int kt = 0; kt < KT; ++kt) {
-                const typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) v.mma(acc[md][nt], p[kt], nt);
-              }
-            }
-            continue;
-          }
-        }
+      // the tile's values, those of keys outside [from, to) as zeros; into the running sums or beside them
+      auto weigh = [&](auto direct, auto cut, int from, int to) {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
           float y[NT][4] = {};
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
-            const typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+            typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
+            if constexpr (cut()) v.keep(from - kt * kSub, to - kt * kSub, lane);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) v.mma(y[nt], p[kt], nt);
+            for (int nt = 0; nt < NT; ++nt) v.mma(direct() ? acc[md][nt] : y[nt], p[kt], nt);
           }
-          add(md, y);
+          if constexpr (!direct()) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[md][nt][j] += y[nt][j];
+          }
         }
+      };
+      if (!edge) {
+        if (kKeepsShortSums<T, D, NT> && short_sums) weigh(std::bool_constant<kKeepsShortSums<T, D, NT>>{}, std::false_type{}, 0, 0);
+        else weigh(std::false_type{}, std::false_type{}, 0, 0);
         continue;
       }
       // A key that a token does not see must not reach its row even as 0 * v (v may be stale, infinite or NaN).
@@ -978,18 +990,9 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
         apart = __any_sync(kFull, !W::V::finite(most));
       }
       if (!apart) {
-#pragma unroll
-        for (int md = 0; md < D / 16; ++md) {
-          float y[NT][4] = {};
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            typename W::V v(w, v_tile + kt * kSub * S::kRowBytes, md);
-            v.keep(seen0 - kt * kSub, seen1 - kt * kSub, lane);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) v.mma(y[nt], p[kt], nt);
-          }
-          add(md, y);
-        }
+        constexpr bool kDirect = kKeepsShortSums<T, D, NT> && D != 128;
+        if (kDirect && short_sums) weigh(std::bool_constant<kDirect>{}, std::true_type{}, seen0, seen1);
+        else weigh(std::false_type{}, std::true_type{}, seen0, seen1);
       } else {
 #pragma unroll 1
         for (int t = t_first; t <= t_last; ++t) {
@@ -1276,9 +1279,8 @@ cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream) {
     // 16/4 heads of 128, bf16, up to 256 keys: 8.7 split, 7.9 us whole; up to 512: 8.9, 10.8; f32 up to 128 keys: 10.3,
     // 9.0; up to 256: equal).
     const uint64_t seen = static_cast<uint64_t>(p.window) + p.n_tokens;  // keys a window of tokens sees at most
-    const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size, most = p.window && seen < keys ? seen : keys;
-    c.whole_items = most <= (sizeof(T) == 4 ? 128 : 256);
-    c.short_sums = most <= kShortKeys;
+    const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size;
+    c.whole_items = (p.window && seen < keys ? seen : keys) <= (sizeof(T) == 4 ? 128 : 256);
     c.splits = static_cast<Split *>(a.workspace);
     c.part = reinterpret_cast<float *>(c.splits + P::ctas);
     c.part_ml = reinterpret_cast<float2 *>(c.part + part_floats(P::ctas, P::rows, P::D));
