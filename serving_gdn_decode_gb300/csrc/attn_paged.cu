@@ -1208,9 +1208,14 @@ auto dispatch(const gdn_attn_params &p, F f) {
     if constexpr (sizeof(T) * D >= 1024) {  // 1 KB per key: no room for more than 8 rows of q beside the rings
       return f(Pick<T, D, 1, 1>{});
     } else if constexpr (D == 256) {  // 16 columns' accumulators and q would not fit a thread's registers
-      // up to 24 rows two blocks of 16, the second read from L2 in part, are ahead of one of 32 (windows of 1 to 4
-      // tokens, 8 heads each: 60.3 against 65.3 us); at 32 rows they are not (334 against 281 us)
-      return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 24 ? f(Pick<T, D, 1, 2, 8>{}) : f(Pick<T, D, 1, 4, 8, 2>{});
+      // 17 to 24 rows take one block of 32 rather than two of 16, which read every key twice (64 requests up to 8192
+      // keys, 17 to 24 heads on each of 4: 205 against 302 us; 32 requests, 2 key heads: 65 against 86) -- but where
+      // that is an average of windows of different lengths, many requests have 16 rows or less (32 requests, windows
+      // of 1 to 4 tokens, 8 heads on each of 2: 67 against 61).
+      const bool some_narrow = p.n_tokens % p.n_seqs != 0 && p.n_q_heads / p.n_kv_heads <= 16;
+      return rows <= 8                           ? f(Pick<T, D, 1, 1>{})
+             : rows <= (some_narrow ? 24u : 16u) ? f(Pick<T, D, 1, 2, 8>{})
+                                                 : f(Pick<T, D, 1, 4, 8, 2>{});
     } else if constexpr (sizeof(T) == 4) {
       return rows <= 8 ? f(Pick<T, D, 1, 1>{}) : rows <= 16 ? f(Pick<T, D, 2, 1>{}) : f(Pick<T, D, 2, 2>{});
     } else {
