@@ -131,6 +131,28 @@ def test_attn_prompts_among_decodes(torch, dtype, dim, group, window):
     check_rows(torch, c, dtype, window=window)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group", [(64, 3), (64, 6), (64, 14), (128, 4), (128, 7), (128, 14), (256, 2), (256, 4), (256, 14)])
+@pytest.mark.parametrize("page", [16, 24, 32])
+def test_attn_unseen_values_of_wide_rows(torch, dtype, dim, group, page):
+    """Windows of four tokens whose blocks of rows go over one, two and four warps: the newest key and value are NaN
+    and infinite, and reach the newest token only; before the sliding window everything is."""
+    window = 37
+    c = Case(torch, dtype, [500, 93, 64], wins=[4, 4, 4], dim=dim, group=group, n_kv=1, page=page)
+    ref = c.reference(torch, window=window)
+    for s, n in enumerate(c.lens):
+        for j in [*range(n - 4 + 1 - window), n - 1]:
+            p = int(c.table[s, j // page])
+            c.k[p, 0, j % page], c.v[p, 0, j % page] = math.inf if j % 2 else math.nan, math.nan if j % 2 else -math.inf
+    c.k_dev.copy_(c.k), c.v_dev.copy_(c.v)
+    got = c.run(torch, window=window)
+    for row in range(12):
+        if row % 4 == 3:
+            assert not bool(got[row].isfinite().any())
+        else:
+            assert rel(got[row], ref[row]) <= ROW_TOL[dtype], row
+
+
 # ------------------------------------------------------------------ rope: prompts
 
 
