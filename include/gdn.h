@@ -525,11 +525,17 @@ typedef struct gdn_attn_params {
  * infinities.  One token per request (decode) or a window of a few
  * (verification of drafted tokens) is what it is built for; longer windows are
  * right but read the keys once per block of 8 to 64 rows (tokens times query
- * heads per key head).
+ * heads per key head), and every block reads all keys that any of the request's
+ * rows sees: a prompt of T tokens costs T times its length, and a sliding window
+ * far shorter than the prompt does not change that.  Rows of q that no request has
+ * are not written.
  *
- * Everything is accumulated in f32, with operands split so that products are
- * good to f32 (bf16 inputs are exact), and rounded once.  Results do not vary
- * from run to run.
+ * The running maximum, the sums and the result are f32, rounded once at the end.
+ * f32 operands are split so that a product is good to 2^-20 of its factors'
+ * magnitudes; bf16 q, k and v are exact, and each probability is good to 2^-16
+ * where the result's rounding takes 2^-8.  Sums are kept relative to a maximum that
+ * may lag by a factor of 2^8: values above 2^119 may give infinities.  Results do
+ * not vary from run to run.
  *
  * workspace: DEVICE, at least gdn_attn_workspace_size bytes, 16-byte aligned,
  * contents irrelevant before and unspecified after; concurrent calls need one

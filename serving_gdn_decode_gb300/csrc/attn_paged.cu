@@ -16,8 +16,9 @@
 // Measured on a GB300, back to back over three sets of buffers, as shares of the
 // measured copy bandwidth (6783 GB/s): 64 requests of up to 4096 keys, 32/8 heads
 // of 128, bf16: 81 us, 0.90; 256 requests, 48/8 heads: 308 us, 0.98; one request
-// of 200003 keys, 32/4 heads: 68 us, 0.89; 16 rows per key head: 0.92; 32 rows:
-// 0.58 to 0.82; 56 rows: 0.4 to 0.6; f32, heads of 128 and 256: 0.87 to 0.93.  Below
+// of 200003 keys, 32/4 heads: 68 us, 0.89; 16 rows per key head: 0.91; 17 to 24 rows
+// at head_dim 256: 0.60 to 0.71; 32 rows: 0.58 to 0.82; 56 rows: 0.43 to 0.58; f32 with
+// 2 to 8 rows per key head: 0.87 to 0.97, with one, heads of 64: 0.71.  Below
 // about 100 MB of cache the fixed part shows: 2.5 us of launch, 3 us until the
 // first products (lengths, page numbers and keys are three dependent reads), and
 // 3 us for the join.

@@ -14,7 +14,8 @@ page_size, n_kv_heads, head_dim]).  Slot number: page * page_size + place in the
 
 Every call runs on ``stream`` (default: the current stream of the tensors'
 device) and does not block; tensors must stay alive and unchanged until the
-stream reaches it.
+stream reaches it.  No call is recorded by autograd, and a tensor written in place
+keeps its version: the gradients of ``gdn_rope`` are a call of their own.
 """
 from __future__ import annotations
 
