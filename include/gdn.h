@@ -564,6 +564,90 @@ gdn_status gdn_attn_paged(const void *q, const void *k_cache, const void *v_cach
                           const int32_t *token_start, void *output, const gdn_attn_params *params,
                           void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * ----------------------------------------------------------------------
+ * The 8-bit cache: half the bytes of bf16 per cached token.
+ *
+ * k_cache and v_cache hold e4m3 codes (one byte an element: sign, 4 bits of
+ * exponent, 3 of mantissa; largest value 448) in the layout above, strides in
+ * elements.  k_scale and v_scale, DEVICE f32 [n_kv_heads, n_pages], innermost
+ * first and contiguous, have one scale for each page and key head: an element
+ * stands for code * scale.  gdn_kv_store_fp8 makes the scales, powers of two;
+ * the other two calls take any f32.
+ */
+typedef struct gdn_kv_fp8_params {
+  uint32_t dtype; /* of k and v */
+  uint32_t head_dim; /* a multiple of 16, at most 256 */
+  uint32_t n_kv_heads, n_tokens;
+  uint32_t page_size, n_pages;
+  int64_t k_stride, v_stride; /* token strides */
+  int64_t cache_page_stride, cache_head_stride, cache_slot_stride;
+} gdn_kv_fp8_params;
+
+/*
+ * gdn_kv_store_fp8 -- quantises k and v as they are written to the cache:
+ * token i's rows go to slot_map[i] (DEVICE int32, as gdn_kv_plan gives it; a
+ * negative slot: nowhere).  A run is a sequence of neighbouring tokens whose
+ * slots follow one another in one page.  For each run, at places a .. b - 1 of
+ * its page, and each key head, for k and v apart:
+ *     need  = the smallest power of two s in [2^-110, 2^119] with |x| <= 448 s
+ *             for all finite x of the run's rows
+ *     scale = need if a = 0, else max(need, the page's scale)
+ *     the page's codes at places 0 .. a - 1, where its scale grows, become
+ *             code * (old scale / scale), rounded to the nearest e4m3
+ *     the run's codes become x / scale, rounded to the nearest e4m3 (ties to
+ *             even; at most 448); NaN and infinities become NaN
+ * So a page's first token starts a new scale, whatever the page held, and later
+ * ones can only raise it; after a rollback into a page its scale stays.  Places
+ * from b on keep their codes: they mean nothing until they are stored.  An old
+ * scale of 0 makes the codes before zero, one that is negative, infinite or
+ * NaN makes them NaN.
+ *
+ * Tokens of one page must be neighbours, slot after slot: a page that two runs
+ * of a call share has unspecified contents where they are not neighbours, and
+ * where they are the second is left out and GDN_DEVICE_BAD_REQUEST is set.  A
+ * slot past the cache stores nothing and sets GDN_DEVICE_BAD_PAGE.
+ *
+ * gdn_kv_load_fp8 -- the reverse: row i of k and v becomes code * scale of slot
+ * slot_map[i], rounded to dtype (bf16 and f32 hold what gdn_kv_store_fp8 makes
+ * exactly); rows of negative slots are left as they were.  A slot past the
+ * cache makes the rows NaN and sets GDN_DEVICE_BAD_PAGE.
+ *
+ * Checks: INVALID_ARGUMENT for NULL pointers, zero sizes (n_tokens may be 0:
+ * nothing is done), unknown dtype, more than 16384 heads, slot_map, k, v or the
+ * scales not aligned to an element, caches not 16-byte aligned or their strides
+ * not multiples of 16, token strides below a row's length, page counts times
+ * page_size at 2^31 - 2^16 or above, an output that overlaps another buffer
+ * (k_cache and v_cache, and k and v as outputs, may lie among one another as in
+ * gdn_rope_store), cache strides that let rows overlap (gdn_kv_store_fp8);
+ * UNSUPPORTED for a head_dim that is not a multiple of 16, or above 256.  k and
+ * v may have any alignment; 16-byte aligned rows go 16 bytes at a time.
+ */
+gdn_status gdn_kv_store_fp8(const void *k, const void *v, const int32_t *slot_map, void *k_cache,
+                            void *v_cache, float *k_scale, float *v_scale,
+                            const gdn_kv_fp8_params *params, gdn_stream_t stream);
+
+gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, void *k, void *v,
+                           const gdn_kv_fp8_params *params, gdn_stream_t stream);
+
+/*
+ * gdn_attn_paged_fp8 -- gdn_attn_paged over an 8-bit cache: the same params
+ * (dtype is that of q and the output; the cache strides are in elements of one
+ * byte and multiples of 16), the same rows, windows, table rules, checks,
+ * workspace rules (gdn_attn_fp8_workspace_size) and reports.  Codes are exact
+ * in the products; a page's scale multiplies the scores (k) and the sums (v) in
+ * f32.  A scale that is NaN reaches the rows that see a key of its page.
+ */
+gdn_status gdn_attn_fp8_workspace_size(const gdn_attn_params *params, size_t *bytes);
+
+gdn_status gdn_attn_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
+                              const float *k_scale, const float *v_scale,
+                              const int32_t *block_table, const int32_t *kv_lens,
+                              const int32_t *token_start, void *output,
+                              const gdn_attn_params *params, void *workspace,
+                              size_t workspace_bytes, gdn_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the thread's next call. */
 const char *gdn_last_error(void);
@@ -571,7 +655,8 @@ const char *gdn_last_error(void);
 /* Bits of the device status word. */
 #define GDN_DEVICE_WAIT_TIMEOUT 0x1u /* a chunked kernel's bounded wait ran out */
 #define GDN_DEVICE_OUT_OF_PAGES 0x2u /* gdn_kv_plan: the free stack could not serve a request */
-#define GDN_DEVICE_BAD_REQUEST 0x4u  /* gdn_kv_plan, gdn_attn_paged: impossible lengths or offsets */
+#define GDN_DEVICE_BAD_REQUEST 0x4u  /* gdn_kv_plan, gdn_attn_paged*: impossible lengths or offsets; gdn_kv_store_fp8: a page's
+                                        tokens out of order */
 #define GDN_DEVICE_BAD_PAGE 0x8u     /* a page number or slot outside the cache */
 #define GDN_DEVICE_BAD_POSITION 0x10u /* gdn_rope*: a position outside the cos/sin table */
 

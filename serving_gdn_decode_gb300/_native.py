@@ -63,6 +63,12 @@ class AttnParams(ctypes.Structure):
                              "cache_slot_stride")]
 
 
+class KvFp8Params(ctypes.Structure):
+    """Mirror of gdn_kv_fp8_params (include/gdn.h)."""
+    _fields_ = [(n, _U32) for n in ("dtype", "head_dim", "n_kv_heads", "n_tokens", "page_size", "n_pages")] + \
+        [(n, _I64) for n in ("k_stride", "v_stride", "cache_page_stride", "cache_head_stride", "cache_slot_stride")]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -120,6 +126,12 @@ def lib() -> ctypes.CDLL:
             L.gdn_attn_workspace_size.restype = ctypes.c_int
             L.gdn_attn_paged.argtypes = [vp] * 7 + [ctypes.POINTER(AttnParams), vp, sz, vp]
             L.gdn_attn_paged.restype = ctypes.c_int
+            L.gdn_kv_store_fp8.argtypes = L.gdn_kv_load_fp8.argtypes = [vp] * 7 + [ctypes.POINTER(KvFp8Params), vp]
+            L.gdn_kv_store_fp8.restype = L.gdn_kv_load_fp8.restype = ctypes.c_int
+            L.gdn_attn_fp8_workspace_size.argtypes = [ctypes.POINTER(AttnParams), ctypes.POINTER(sz)]
+            L.gdn_attn_fp8_workspace_size.restype = ctypes.c_int
+            L.gdn_attn_paged_fp8.argtypes = [vp] * 9 + [ctypes.POINTER(AttnParams), vp, sz, vp]
+            L.gdn_attn_paged_fp8.restype = ctypes.c_int
             _lib = L
     return _lib
 

@@ -14,7 +14,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWords = 5;
+constexpr int kWords = 7;
 struct Words {
   unsigned int *at[kWords];
 };
@@ -38,7 +38,7 @@ cudaError_t read_device_status(unsigned int *bits, bool reset, cudaStream_t stre
   std::lock_guard<std::mutex> lock(one_at_a_time);
   Words w;
   cudaError_t (*const words[kWords])(unsigned int **) = {chunked_status_word, chunked_split_status_word, kv_plan_status_word,
-                                                         rope_status_word, attn_paged_status_word};
+                                                         rope_status_word, attn_paged_status_word, kv_fp8_status_word, attn_fp8_status_word};
   for (int i = 0; i < kWords; ++i)
     if ((e = words[i](&w.at[i])) != cudaSuccess) return e;
   gdn_status_kernel<<<1, 1, 0, stream>>>(w, reset);

@@ -1,5 +1,6 @@
 // C-ABI entry points of the full-attention operators: argument checks and
-// dispatch (gdn_kv_plan, gdn_rope, gdn_rope_store, gdn_attn_paged).
+// dispatch (gdn_kv_plan, gdn_rope, gdn_rope_store, gdn_attn_paged, and the 8-bit
+// cache's gdn_kv_store_fp8, gdn_kv_load_fp8, gdn_attn_paged_fp8).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -210,8 +211,8 @@ gdn_status run_rope(const gdn::RopeArgs &x, bool store, const gdn_rope_params *p
   return cuda_status(gdn::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// The checks of a gdn_attn_params block alone.
-gdn_status check_attn_params(const gdn_attn_params *params, unsigned long long *cache_bytes) {
+// The checks of a gdn_attn_params block alone; the cache's elements have cache_es bytes, or dtype's.
+gdn_status check_attn_params(const gdn_attn_params *params, unsigned long long *cache_bytes, unsigned long long cache_es = 0) {
   if (params == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: params is NULL");
   const gdn_attn_params &p = *params;
   if (p.dtype > GDN_DTYPE_BF16) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: unknown dtype %u", p.dtype);
@@ -225,7 +226,7 @@ gdn_status check_attn_params(const gdn_attn_params *params, unsigned long long *
   if (static_cast<unsigned long long>(p.n_tokens) * p.n_q_heads > 0x7fff0000ull || p.n_seqs > 0x7fff0000u)
     return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: n_seqs and n_tokens x n_q_heads must stay below 2^31 - 2^16");
   if (!std::isfinite(p.scale)) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: scale must be finite");
-  const unsigned long long es = elem_bytes(p.dtype);
+  const unsigned long long es = cache_es ? cache_es : elem_bytes(p.dtype);
   const gdn_status r = check_cache(Cache{p.n_pages, p.page_size, p.n_kv_heads, p.head_dim, p.cache_page_stride,
                                          p.cache_head_stride, p.cache_slot_stride, es}, cache_bytes);
   if (r != GDN_OK) return r;
@@ -240,6 +241,111 @@ gdn_status check_attn_params(const gdn_attn_params *params, unsigned long long *
   if (p.dtype == GDN_DTYPE_BF16 && p.q_stride % 2)
     return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: q_stride must be even in bf16");
   return GDN_OK;
+}
+
+struct AttnBuffers {
+  const void *q, *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *kv_lens, *token_start;
+  void *output, *workspace;
+  size_t workspace_bytes;
+};
+
+// The checks of an attention call's pointers; nothing to check with n_tokens 0.
+gdn_status check_attn_buffers(const AttnBuffers &x, const gdn_attn_params &p, unsigned long long cache_bytes, size_t need,
+                              bool scaled = false) {
+  if (x.token_start == nullptr && p.n_tokens < p.n_seqs)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: without token_start q needs a row per request (%u rows, %u requests)",
+                p.n_tokens, p.n_seqs);
+  if (p.n_tokens == 0) return GDN_OK;
+  const unsigned long long es = elem_bytes(p.dtype), row = es * p.head_dim * p.n_q_heads;
+  const unsigned long long scale_bytes = 4ull * p.n_pages * p.n_kv_heads;
+  const Rows in[] = {{x.q, p.n_tokens, row, es * p.q_stride, "q"},
+                     {x.k_cache, 1, cache_bytes, 0, "k_cache"},
+                     {x.v_cache, 1, cache_bytes, 0, "v_cache"},
+                     {x.k_scale, scaled ? 1ull : 0ull, scale_bytes, 0, "k_scale"},
+                     {x.v_scale, scaled ? 1ull : 0ull, scale_bytes, 0, "v_scale"},
+                     {x.block_table, 1, 4ull * p.n_seqs * p.max_pages, 0, "block_table"},
+                     {x.kv_lens, 1, 4ull * p.n_seqs, 0, "kv_lens"},
+                     {x.token_start, x.token_start ? 1ull : 0ull, 4ull * (p.n_seqs + 1ull), 0, "token_start"}};
+  const Rows out{x.output, p.n_tokens, row, es * p.out_stride, "output"};
+  const Rows ws{x.workspace, 1, need, 0, "workspace"};
+  for (const Rows &b : in)
+    if (b.rows && b.p == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s is NULL", b.name);
+  if (x.output == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: output is NULL");
+  if (x.workspace == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: workspace is NULL");
+  if (x.workspace_bytes < need)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: workspace has %zu bytes, %zu needed", x.workspace_bytes, need);
+  const struct { const void *p; uintptr_t a; const char *name; } al[] = {
+      {x.q, 4, "q"},           {x.k_cache, 16, "k_cache"}, {x.v_cache, 16, "v_cache"}, {x.k_scale, 4, "k_scale"},
+      {x.v_scale, 4, "v_scale"}, {x.block_table, 4, "block_table"}, {x.kv_lens, 4, "kv_lens"},
+      {x.token_start, 4, "token_start"}, {x.output, es, "output"}, {x.workspace, 16, "workspace"}};
+  for (const auto &y : al)
+    if (!aligned(y.p, y.a))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s must be %u-byte aligned", y.name, static_cast<unsigned>(y.a));
+  for (const Rows &b : in) {
+    if (rows_overlap(out, b)) return overlap_error(out, b);
+    if (rows_overlap(ws, b)) return overlap_error(ws, b);
+  }
+  if (rows_overlap(ws, out)) return overlap_error(ws, out);
+  return GDN_OK;
+}
+
+gdn_status run_kv_fp8(const gdn::KvFp8Args &x, bool store, const gdn_kv_fp8_params *params, gdn_stream_t stream) {
+  gdn::g_last_error[0] = '\0';
+  if (params == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: params is NULL");
+  gdn::KvFp8Args a = x;
+  a.p = *params;
+  const gdn_kv_fp8_params &p = a.p;
+  if (p.dtype > GDN_DTYPE_BF16) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: unknown dtype %u", p.dtype);
+  if (p.n_kv_heads == 0 || p.head_dim == 0) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: n_kv_heads and head_dim must be > 0");
+  if (p.head_dim % 16 || p.head_dim > 256)
+    return fail(GDN_ERR_UNSUPPORTED, "gdn: head_dim (%u) must be a multiple of 16, at most 256, in an 8-bit cache", p.head_dim);
+  if (p.n_kv_heads > (1u << 14)) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: too many heads");
+  if (p.n_tokens > kMaxSlots) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: n_tokens must stay below 2^31 - 2^16");
+  const unsigned long long es = elem_bytes(p.dtype), t = p.n_tokens, row = es * p.head_dim * p.n_kv_heads;
+  const struct { int64_t stride; const char *name; } st[] = {{p.k_stride, "k_stride"}, {p.v_stride, "v_stride"}};
+  for (const auto &s : st)
+    if (s.stride < static_cast<int64_t>(row / es) || s.stride > (int64_t{1} << 40))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s is shorter than a row, or above 2^40", s.name);
+  const Cache cache{p.n_pages, p.page_size, p.n_kv_heads, p.head_dim, p.cache_page_stride, p.cache_head_stride, p.cache_slot_stride, 1};
+  unsigned long long cache_bytes = 0;
+  const gdn_status r = check_cache(cache, &cache_bytes);
+  if (r != GDN_OK) return r;
+  if (p.cache_page_stride % 16 || p.cache_head_stride % 16 || p.cache_slot_stride % 16)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: the cache strides must be multiples of 16 bytes");
+  const StoredCache stored(cache);
+  if (store && !stored.rows_apart())
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: the cache strides let rows overlap");
+  if (t == 0) return GDN_OK;
+  const unsigned long long scale_bytes = 4ull * p.n_pages * p.n_kv_heads;
+  const Rows rows[] = {{store ? a.k : a.k_out, t, row, es * p.k_stride, "k"},
+                       {store ? a.v : a.v_out, t, row, es * p.v_stride, "v"},
+                       {a.slot_map, 1, 4 * t, 0, "slot_map"},
+                       {a.k_cache, 1, cache_bytes, 0, "k_cache"},
+                       {a.v_cache, 1, cache_bytes, 0, "v_cache"},
+                       {a.k_scale, 1, scale_bytes, 0, "k_scale"},
+                       {a.v_scale, 1, scale_bytes, 0, "v_scale"}};
+  const uintptr_t align[] = {es, es, 4, 16, 16, 4, 4};
+  for (int i = 0; i < 7; ++i) {
+    if (rows[i].p == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s is NULL", rows[i].name);
+    if (!aligned(rows[i].p, align[i]))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s must be %u-byte aligned", rows[i].name, static_cast<unsigned>(align[i]));
+  }
+  // outputs: the caches and scales, or k and v
+  const int out0 = store ? 3 : 0, out1 = store ? 7 : 2;
+  for (int o = out0; o < out1; ++o)
+    for (int i = 0; i < 7; ++i) {
+      if (i == o || (i >= out0 && i < o)) continue;  // an output, seen before
+      if (store && o == 3 && i == 4) {  // k_cache and v_cache may be two views of one array
+        if (stored.meets(static_cast<int64_t>(reinterpret_cast<uintptr_t>(rows[4].p) - reinterpret_cast<uintptr_t>(rows[3].p))))
+          return overlap_error(rows[4], rows[3]);
+        continue;
+      }
+      if (rows_overlap(rows[o], rows[i])) return overlap_error(rows[o], rows[i]);
+    }
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(store ? gdn::launch_kv_store_fp8(a, on) : gdn::launch_kv_load_fp8(a, on));
 }
 
 }  // namespace
@@ -330,42 +436,65 @@ gdn_status gdn_attn_paged(const void *q, const void *k_cache, const void *v_cach
                           void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
   gdn::g_last_error[0] = '\0';
   unsigned long long cache_bytes = 0;
-  const gdn_status r = check_attn_params(params, &cache_bytes);
+  gdn_status r = check_attn_params(params, &cache_bytes);
   if (r != GDN_OK) return r;
-  const gdn_attn_params &p = *params;
-  if (token_start == nullptr && p.n_tokens < p.n_seqs)
-    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: without token_start q needs a row per request (%u rows, %u requests)",
-                p.n_tokens, p.n_seqs);
-  if (p.n_tokens == 0) return GDN_OK;
-  const unsigned long long es = elem_bytes(p.dtype), row = es * p.head_dim * p.n_q_heads;
-  const size_t need = gdn::attn_workspace_bytes(p);
-  const Rows in[] = {{q, p.n_tokens, row, es * p.q_stride, "q"},
-                     {k_cache, 1, cache_bytes, 0, "k_cache"},
-                     {v_cache, 1, cache_bytes, 0, "v_cache"},
-                     {block_table, 1, 4ull * p.n_seqs * p.max_pages, 0, "block_table"},
-                     {kv_lens, 1, 4ull * p.n_seqs, 0, "kv_lens"},
-                     {token_start, token_start ? 1ull : 0ull, 4ull * (p.n_seqs + 1ull), 0, "token_start"}};
-  const Rows out{output, p.n_tokens, row, es * p.out_stride, "output"};
-  const Rows ws{workspace, 1, need, 0, "workspace"};
-  for (const Rows &b : in)
-    if (b.rows && b.p == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s is NULL", b.name);
-  if (output == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: output is NULL");
-  if (workspace == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: workspace is NULL");
-  if (workspace_bytes < need)
-    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: workspace has %zu bytes, %zu needed", workspace_bytes, need);
-  const struct { const void *p; uintptr_t a; const char *name; } al[] = {
-      {q, 4, "q"},           {k_cache, 16, "k_cache"}, {v_cache, 16, "v_cache"}, {block_table, 4, "block_table"},
-      {kv_lens, 4, "kv_lens"}, {token_start, 4, "token_start"}, {output, es, "output"}, {workspace, 16, "workspace"}};
-  for (const auto &x : al)
-    if (!aligned(x.p, x.a))
-      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: %s must be %u-byte aligned", x.name, static_cast<unsigned>(x.a));
-  for (const Rows &b : in) {
-    if (rows_overlap(out, b)) return overlap_error(out, b);
-    if (rows_overlap(ws, b)) return overlap_error(ws, b);
-  }
-  if (rows_overlap(ws, out)) return overlap_error(ws, out);
-  gdn::AttnArgs a{q, k_cache, v_cache, block_table, kv_lens, token_start, output, p, workspace};
+  const AttnBuffers x{q, k_cache, v_cache, nullptr, nullptr, block_table, kv_lens, token_start, output, workspace, workspace_bytes};
+  r = check_attn_buffers(x, *params, cache_bytes, gdn::attn_workspace_bytes(*params));
+  if (r != GDN_OK || params->n_tokens == 0) return r;
+  const gdn::AttnArgs a{q, k_cache, v_cache, block_table, kv_lens, token_start, output, *params, workspace};
   return cuda_status(gdn::launch_attn_paged(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_store_fp8(const void *k, const void *v, const int32_t *slot_map, void *k_cache, void *v_cache,
+                            float *k_scale, float *v_scale, const gdn_kv_fp8_params *params, gdn_stream_t stream) {
+  gdn::KvFp8Args a{};
+  a.k = k;
+  a.v = v;
+  a.slot_map = slot_map;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return run_kv_fp8(a, true, params, stream);
+}
+
+gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, void *k, void *v, const gdn_kv_fp8_params *params, gdn_stream_t stream) {
+  gdn::KvFp8Args a{};
+  a.k_out = k;
+  a.v_out = v;
+  a.slot_map = slot_map;
+  a.k_cache = const_cast<void *>(k_cache);
+  a.v_cache = const_cast<void *>(v_cache);
+  a.k_scale = const_cast<float *>(k_scale);
+  a.v_scale = const_cast<float *>(v_scale);
+  return run_kv_fp8(a, false, params, stream);
+}
+
+gdn_status gdn_attn_fp8_workspace_size(const gdn_attn_params *params, size_t *bytes) {
+  gdn::g_last_error[0] = '\0';
+  if (bytes == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: bytes is NULL");
+  *bytes = 0;
+  unsigned long long cache_bytes;
+  const gdn_status r = check_attn_params(params, &cache_bytes, 1);
+  if (r != GDN_OK) return r;
+  *bytes = gdn::attn_fp8_workspace_bytes(*params);
+  return GDN_OK;
+}
+
+gdn_status gdn_attn_paged_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                              const float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
+                              const int32_t *token_start, void *output, const gdn_attn_params *params, void *workspace,
+                              size_t workspace_bytes, gdn_stream_t stream) {
+  gdn::g_last_error[0] = '\0';
+  unsigned long long cache_bytes = 0;
+  gdn_status r = check_attn_params(params, &cache_bytes, 1);
+  if (r != GDN_OK) return r;
+  const AttnBuffers x{q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, token_start, output, workspace, workspace_bytes};
+  r = check_attn_buffers(x, *params, cache_bytes, gdn::attn_fp8_workspace_bytes(*params), true);
+  if (r != GDN_OK || params->n_tokens == 0) return r;
+  const gdn::AttnFp8Args a{q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, token_start, output, *params, workspace};
+  return cuda_status(gdn::launch_attn_paged_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -58,7 +58,7 @@ bool get(PyObject *o, const char *name, Arg *out) {
   return true;
 }
 
-const char *name_of(at::ScalarType t) { return t == at::kBFloat16 ? "bf16" : t == at::kFloat ? "f32" : t == at::kInt ? "int32" : "another type"; }
+const char *name_of(at::ScalarType t) { return t == at::kBFloat16 ? "bf16" : t == at::kFloat ? "f32" : t == at::kInt ? "int32" : t == at::kFloat8_e4m3fn ? "e4m3" : "another type"; }
 
 bool want_type(const Arg &a, at::ScalarType t) {
   if (a->scalar_type() == t) return true;
@@ -284,7 +284,7 @@ PyObject *py_rope_store(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
 
 // ------------------------------------------------------------------ attention
 
-bool attn_params(const Arg &q, const Arg &k, const Arg &v, gdn_attn_params *p) {
+bool attn_params(const Arg &q, const Arg &k, const Arg &v, bool fp8, gdn_attn_params *p) {
   if (!data_type(q, &p->dtype)) return false;
   if (q->dim() != 3) return bad("q", "must be [n_tokens, n_q_heads, head_dim]");
   p->n_tokens = static_cast<uint32_t>(q->size(0));
@@ -292,38 +292,54 @@ bool attn_params(const Arg &q, const Arg &k, const Arg &v, gdn_attn_params *p) {
   p->head_dim = static_cast<uint32_t>(q->size(2));
   p->n_kv_heads = 0;
   return want_rows(q, q->scalar_type(), q->size(0), q->size(1), q->size(2), &p->q_stride) &&
-         want_cache(k, v, q->scalar_type(), q->size(2), p, &p->n_kv_heads);
+         want_cache(k, v, fp8 ? at::kFloat8_e4m3fn : q->scalar_type(), q->size(2), p, &p->n_kv_heads);
 }
 
-// attn_workspace_size(q, k_cache, n_seqs)
+// f32 [n_pages, n_kv_heads], contiguous
+bool want_scales(const Arg &a, int64_t n_pages, int64_t n_kv) {
+  if (!want_type(a, at::kFloat)) return false;
+  if (a->dim() == 2 && a->size(0) == n_pages && a->size(1) == n_kv && a->is_contiguous()) return true;
+  return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be contiguous, of %lld x %lld elements", a.name, static_cast<long long>(n_pages),
+              static_cast<long long>(n_kv));
+}
+
+// attn_workspace_size(q, k_cache, n_seqs), attn_fp8_workspace_size(q, k_cache, n_seqs)
+template <bool FP8>
 PyObject *py_attn_workspace_size(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   if (!count(n_args, 3)) return nullptr;
   Arg q, k;
   gdn_attn_params p{};
   if (!get(args[0], "q", &q) || !get(args[1], "k_cache", &k) || !small(q) || !small(k) || !get_u32(args[2], "n_seqs", &p.n_seqs) ||
-      !attn_params(q, k, k, &p))
+      !attn_params(q, k, k, FP8, &p))
     return nullptr;
   p.max_pages = 1;
   p.scale = 1.0f;
   p.out_stride = static_cast<int64_t>(p.n_q_heads) * p.head_dim;
   size_t bytes = 0;
-  const gdn_status st = gdn_attn_workspace_size(&p, &bytes);
+  const gdn_status st = FP8 ? gdn_attn_fp8_workspace_size(&p, &bytes) : gdn_attn_workspace_size(&p, &bytes);
   if (st != GDN_OK) return finish(st);
   return PyLong_FromSize_t(bytes);
 }
 
-// attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start | None, output, workspace, scale | None, window, stream)
+// attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start | None, output, workspace, scale | None, window, stream),
+// attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ...)
+template <bool FP8>
 PyObject *py_attn_paged(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
-  static const char *const names[8] = {"q", "k_cache", "v_cache", "block_table", "kv_lens", "token_start", "output", "workspace"};
-  if (!count(n_args, 11)) return nullptr;
-  const bool ragged = args[5] != Py_None;
-  Arg a[8];
-  for (int i = 0; i < 8; ++i) {
+  static const char *const names[10] = {"q", "k_cache", "v_cache", "block_table", "kv_lens", "token_start", "output", "workspace",
+                                        "k_scale", "v_scale"};
+  constexpr int kArgs = FP8 ? 10 : 8;
+  if (!count(n_args, kArgs + 3)) return nullptr;
+  // the scales, where there are any, stand behind the caches in the call and last here
+  auto place = [](int i) { return !FP8 || i < 3 ? i : i < 8 ? i + 2 : i - 5; };
+  PyObject *const *const more = args + kArgs;  // scale, window, stream
+  const bool ragged = args[place(5)] != Py_None;
+  Arg a[kArgs];
+  for (int i = 0; i < kArgs; ++i) {
     if (i == 5 && !ragged) a[i] = a[4];
-    else if (!get(args[i], names[i], &a[i]) || (i < 7 && !small(a[i]))) return nullptr;
+    else if (!get(args[place(i)], names[i], &a[i]) || (i != 7 && !small(a[i]))) return nullptr;
   }
   gdn_attn_params p{};
-  if (!attn_params(a[0], a[1], a[2], &p) || !get_u32(args[9], "window", &p.window)) return nullptr;
+  if (!attn_params(a[0], a[1], a[2], FP8, &p) || !get_u32(more[1], "window", &p.window)) return nullptr;
   const int64_t n = a[4]->numel();
   if (a[3]->dim() != 2) {
     bad("block_table", "must be [n_seqs, max_pages]");
@@ -332,26 +348,69 @@ PyObject *py_attn_paged(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   if (!want_ints(a[3], a[3]->size(1), n) || !want_ints(a[4], n) || (ragged && !want_ints(a[5], n + 1)) ||
       !want_rows(a[6], a[0]->scalar_type(), p.n_tokens, p.n_q_heads, p.head_dim, &p.out_stride))
     return nullptr;
+  if constexpr (FP8)
+    if (!want_scales(a[8], p.n_pages, p.n_kv_heads) || !want_scales(a[9], p.n_pages, p.n_kv_heads)) return nullptr;
   if (!a[7]->is_contiguous()) {
     bad("workspace", "must be contiguous");
     return nullptr;
   }
-  if (!on_one_device(a, 8)) return nullptr;
+  if (!on_one_device(a, kArgs)) return nullptr;
   p.n_seqs = static_cast<uint32_t>(n);
   p.max_pages = static_cast<uint32_t>(a[3]->size(1));
-  if (args[8] == Py_None) {
+  if (more[0] == Py_None) {
     p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(p.head_dim)));
   } else {
-    const double s = PyFloat_AsDouble(args[8]);
+    const double s = PyFloat_AsDouble(more[0]);
     if (s == -1.0 && PyErr_Occurred()) return nullptr;
     p.scale = static_cast<float>(s);
   }
   gdn_stream_t stream;
-  if (!get_stream(args[10], a[0]->get_device(), &stream)) return nullptr;
+  if (!get_stream(more[2], a[0]->get_device(), &stream)) return nullptr;
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(a[0]->get_device()));
-  return finish(gdn_attn_paged(a[0].ptr(), a[1].ptr(), a[2].ptr(), static_cast<const int32_t *>(a[3].ptr()),
-                               static_cast<const int32_t *>(a[4].ptr()), ragged ? static_cast<const int32_t *>(a[5].ptr()) : nullptr,
-                               a[6].ptr(), &p, a[7].ptr(), static_cast<size_t>(a[7]->nbytes()), stream));
+  const int32_t *table = static_cast<const int32_t *>(a[3].ptr()), *lens = static_cast<const int32_t *>(a[4].ptr()),
+                *start = ragged ? static_cast<const int32_t *>(a[5].ptr()) : nullptr;
+  const size_t bytes = static_cast<size_t>(a[7]->nbytes());
+  if constexpr (FP8)
+    return finish(gdn_attn_paged_fp8(a[0].ptr(), a[1].ptr(), a[2].ptr(), static_cast<const float *>(a[8].ptr()),
+                                     static_cast<const float *>(a[9].ptr()), table, lens, start, a[6].ptr(), &p, a[7].ptr(), bytes, stream));
+  else
+    return finish(gdn_attn_paged(a[0].ptr(), a[1].ptr(), a[2].ptr(), table, lens, start, a[6].ptr(), &p, a[7].ptr(), bytes, stream));
+}
+
+// ------------------------------------------------------------------ the 8-bit cache
+
+// kv_store_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream),
+// kv_load_fp8(slot_map, k_cache, v_cache, k_scale, v_scale, k, v, stream)
+template <bool STORE>
+PyObject *py_kv_fp8(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+  static const char *const names[7] = {"k", "v", "slot_map", "k_cache", "v_cache", "k_scale", "v_scale"};
+  if (!count(n_args, 8)) return nullptr;
+  Arg a[7];
+  for (int i = 0; i < 7; ++i)
+    if (!get(args[STORE ? i : (i + 5) % 7], names[i], &a[i]) || !small(a[i])) return nullptr;
+  gdn_kv_fp8_params p{};
+  if (!data_type(a[0], &p.dtype)) return nullptr;
+  if (a[0]->dim() != 3) {
+    bad("k", "must be [n_tokens, n_kv_heads, head_dim]");
+    return nullptr;
+  }
+  const at::ScalarType t = a[0]->scalar_type();
+  const int64_t n = a[0]->size(0), heads = a[0]->size(1), dim = a[0]->size(2);
+  uint32_t n_kv = static_cast<uint32_t>(heads);
+  if (!want_rows(a[0], t, n, heads, dim, &p.k_stride) || !want_rows(a[1], t, n, heads, dim, &p.v_stride) || !want_ints(a[2], n) ||
+      !want_cache(a[3], a[4], at::kFloat8_e4m3fn, dim, &p, &n_kv) || !want_scales(a[5], p.n_pages, n_kv) ||
+      !want_scales(a[6], p.n_pages, n_kv) || !on_one_device(a, 7))
+    return nullptr;
+  p.head_dim = static_cast<uint32_t>(dim);
+  p.n_kv_heads = n_kv;
+  p.n_tokens = static_cast<uint32_t>(n);
+  gdn_stream_t stream;
+  if (!get_stream(args[7], a[0]->get_device(), &stream)) return nullptr;
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(a[0]->get_device()));
+  const int32_t *slots = static_cast<const int32_t *>(a[2].ptr());
+  float *ks = static_cast<float *>(a[5].ptr()), *vs = static_cast<float *>(a[6].ptr());
+  return finish(STORE ? gdn_kv_store_fp8(a[0].ptr(), a[1].ptr(), slots, a[3].ptr(), a[4].ptr(), ks, vs, &p, stream)
+                      : gdn_kv_load_fp8(slots, a[3].ptr(), a[4].ptr(), ks, vs, a[0].ptr(), a[1].ptr(), &p, stream));
 }
 
 // Every entry: a C++ exception of torch (a tensor without storage, say) becomes a Python one.
@@ -372,8 +431,12 @@ PyMethodDef method(const char *name) {
 PyMethodDef g_methods[] = {method<py_kv_plan>("kv_plan"),
                            method<py_rope>("rope"),
                            method<py_rope_store>("rope_store"),
-                           method<py_attn_workspace_size>("attn_workspace_size"),
-                           method<py_attn_paged>("attn_paged"),
+                           method<py_attn_workspace_size<false>>("attn_workspace_size"),
+                           method<py_attn_paged<false>>("attn_paged"),
+                           method<py_kv_fp8<true>>("kv_store_fp8"),
+                           method<py_kv_fp8<false>>("kv_load_fp8"),
+                           method<py_attn_workspace_size<true>>("attn_fp8_workspace_size"),
+                           method<py_attn_paged<true>>("attn_paged_fp8"),
                            PyMethodDef{nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

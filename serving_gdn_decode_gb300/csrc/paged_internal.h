@@ -1,5 +1,6 @@
 // Internal interface between the C-ABI host code (paged_abi.cu) and the
-// launchers of the full-attention operators: kv_plan.cu, rope.cu, attn_paged.cu.
+// launchers of the full-attention operators: kv_plan.cu, rope.cu, attn_paged.cu,
+// kv_fp8.cu, attn_fp8.cu.
 // Nothing here is exported from the shared library.
 #pragma once
 
@@ -54,9 +55,33 @@ struct AttnArgs {
 size_t attn_workspace_bytes(const gdn_attn_params &p);
 cudaError_t launch_attn_paged(const AttnArgs &a, cudaStream_t stream);
 
-// The status words of the three files' kernels on the current device (read_device_status).
+struct KvFp8Args {
+  const void *k, *v;  // store: the rows to store; load: nullptr
+  void *k_out, *v_out;  // load: the rows to write; store: nullptr
+  const int32_t *slot_map;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  gdn_kv_fp8_params p;
+};
+cudaError_t launch_kv_store_fp8(const KvFp8Args &a, cudaStream_t stream);
+cudaError_t launch_kv_load_fp8(const KvFp8Args &a, cudaStream_t stream);
+
+struct AttnFp8Args {
+  const void *q, *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *kv_lens, *token_start;
+  void *output;
+  gdn_attn_params p;
+  void *workspace;
+};
+size_t attn_fp8_workspace_bytes(const gdn_attn_params &p);
+cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream);
+
+// The status words of the files' kernels on the current device (read_device_status).
 cudaError_t kv_plan_status_word(unsigned int **word);
 cudaError_t rope_status_word(unsigned int **word);
 cudaError_t attn_paged_status_word(unsigned int **word);
+cudaError_t kv_fp8_status_word(unsigned int **word);
+cudaError_t attn_fp8_status_word(unsigned int **word);
 
 }  // namespace gdn

@@ -1,6 +1,8 @@
 """The full-attention layers of a hybrid model's serving step, on torch tensors:
 ``gdn_kv_plan``, ``gdn_rope``, ``gdn_rope_store``, ``gdn_attn_workspace_size``
-and ``gdn_attn_paged`` of ``include/gdn.h``.
+and ``gdn_attn_paged`` of ``include/gdn.h``, and with an 8-bit cache
+``gdn_kv_store_fp8``, ``gdn_kv_load_fp8``, ``gdn_attn_fp8_workspace_size`` and
+``gdn_attn_paged_fp8``.
 
 Argument marshalling only, as in ``_native``, here by the compiled module
 ``_paged_binding``: shapes, strides and dtypes become the params struct of the C
@@ -11,6 +13,9 @@ The paged cache: ``k_cache`` and ``v_cache`` of shape [n_pages, n_kv_heads,
 page_size, head_dim], f32 or bf16, with any strides over contiguous rows of
 head_dim (pass ``cache.transpose(1, 2)`` for a cache held as [n_pages,
 page_size, n_kv_heads, head_dim]).  Slot number: page * page_size + place in the page.
+An 8-bit cache has ``k_cache`` and ``v_cache`` of ``torch.float8_e4m3fn`` and, for
+each page and key head, an f32 scale in ``k_scale`` and ``v_scale`` ([n_pages,
+n_kv_heads], contiguous): an element stands for code * scale.
 
 Every call runs on ``stream`` (default: the current stream of the tensors'
 device) and does not block; tensors must stay alive and unchanged until the
@@ -90,3 +95,34 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start, outpu
     ``gdn_attn_workspace_size`` bytes."""
     _binding.attn_paged(q, k_cache, v_cache, block_table, kv_lens, token_start, output, workspace, scale, window,
                         stream)
+
+
+def gdn_kv_store_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantises k and v ([n_tokens, n_kv_heads, head_dim], f32 or bf16) as they are
+    written to the 8-bit paged cache at ``slot_map`` (int32 [n_tokens], as
+    ``gdn_kv_plan`` gives it; negative: nowhere).  A page's scale per key head is the
+    smallest power of two that keeps its tokens within e4m3's range; it starts anew
+    with the page's first token and grows with later ones, the codes before them
+    rounded again.  Tokens of one page must be neighbours, slot after slot."""
+    _binding.kv_store_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream)
+
+
+def gdn_kv_load_fp8(slot_map, k_cache, v_cache, k_scale, v_scale, k, v, stream=None) -> None:
+    """Rows of the 8-bit cache as values: row i of ``k`` and ``v`` ([n_tokens,
+    n_kv_heads, head_dim], f32 or bf16) from slot ``slot_map[i]``; rows of negative
+    slots are left as they were."""
+    _binding.kv_load_fp8(slot_map, k_cache, v_cache, k_scale, v_scale, k, v, stream)
+
+
+def gdn_attn_fp8_workspace_size(q, k_cache, n_seqs) -> int:
+    """Bytes of workspace ``gdn_attn_paged_fp8`` needs for ``n_seqs`` requests with
+    q's rows and heads; the lengths do not matter."""
+    return _binding.attn_fp8_workspace_size(q, k_cache, n_seqs)
+
+
+def gdn_attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, token_start, output,
+                       workspace, scale=None, window=0, stream=None) -> None:
+    """``gdn_attn_paged`` over an 8-bit cache; q and output are f32 or bf16, and
+    ``workspace`` has at least ``gdn_attn_fp8_workspace_size`` bytes."""
+    _binding.attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, token_start, output,
+                            workspace, scale, window, stream)
