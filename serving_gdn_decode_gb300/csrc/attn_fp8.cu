@@ -6,9 +6,11 @@
 // 200 flops a byte, so HBM bounds it up to some 16 rows per key head, as it bounds
 // the kernel over a bf16 cache, at half the bytes.  The same structure serves (its
 // file gives the reasons): a token's rows on the N side of the warp-level matrix
-// instruction (S^T = K Q^T, O^T = V^T P^T), shares of a list of units, a ring of
-// half tiles per key group that runs on across items.  What differs is how codes
-// become operands.
+// instruction (S^T = K Q^T, O^T = V^T P^T), and shares of a list of units.  What
+// differs is how codes become operands, and how they come: one warp of a CTA feeds
+// a ring of tiles with 16-byte asynchronous copies, across items, and the others
+// take its tiles in turn, so that these have neither the copies' instructions nor
+// their registers, and more of them fit an SM.
 //
 // Operands.  e4m3 is a part of f16, so a code is exact there, and the products are
 // those of f16 matrix instructions with f32 sums.  q goes in with each row scaled
@@ -25,10 +27,14 @@
 // codes, times their page's scale over the largest of the tile, and the sums are
 // added to the running ones, in f32, times that largest.  Where scales of a tile
 // are further apart than 2^8 its pages take products of their own.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cmath>
+#include <mutex>
+#include <numeric>
 #include <type_traits>
 
 #include "attn_work.cuh"
@@ -47,6 +53,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const unsigned (&a)[4], u
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c = a b
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ unsigned f16x2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -70,41 +82,73 @@ __device__ __forceinline__ float load_f32(unsigned addr) {
   return x;
 }
 
-// A half tile in shared memory: kTile rows of codes, then, beside K, the scales of its keys and of their values.
+
+__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// Arrives once this thread's copies so far are done.
+__device__ __forceinline__ void mbar_arrive_after_copies(unsigned bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// Whether the phase ended within about a second of clock.
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase) {
+  long long t0 = 0;
+  for (int i = 0;; ++i) {
+    unsigned done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+    if (done) return true;
+    if (i == 0) t0 = clock64();
+    else if (clock64() - t0 > 2000000000LL) return false;
+  }
+}
+
+// Arrives, and expects `bytes` of copies that report to the barrier themselves.
+__device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+// A box of a cache, at element e and place o of key head h and page p, by one thread.
+__device__ __forceinline__ void copy_box(unsigned dst, const CUtensorMap *map, int e, int o, int h, int p, unsigned bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
+               ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(e), "r"(o), "r"(h), "r"(p), "r"(bar) : "memory");
+}
+
+// A stage of the ring: a tile's rows of K, then of V, in parts of 128 elements (64, where a head has no more).
 template <int D, int KT>
 struct Shape8 {
   static constexpr int kTile = kSub * KT;
   static constexpr int kChunks = D / 16;  // 16-byte chunks per row
-  static constexpr int kCodes = kTile * D;
-  static constexpr int kHalf = kCodes + 2 * kTile * 4;
+  static constexpr int kRow = D < 128 ? D : 128;  // of a part
+  static constexpr int kParts = D / kRow;
+  static constexpr int kPart = kTile * kRow;
+  static constexpr int kCodes = kTile * D;  // of K, of V
+  static constexpr int kStage = 2 * kCodes;
   static constexpr int kSteps = D / 16;   // matrix steps of Q K^T
   static constexpr int kBytes = D >= 128 ? 16 : 8;  // neighbouring elements that a lane takes of a value at once
-  static constexpr int kPieces = D / (8 * kBytes);  // such pieces of a row
 };
 
-// Where chunk c of row r lies.  K: lanes read chunks 0-3 or 4-7 of rows r and r + 1 at once; rows of 128 bytes and
-// more exchange the two in odd rows.  V: lanes read two neighbouring chunks (64 elements: one) of rows r, r + 2,
-// r + 4 and r + 6 at once; rows of 64 bytes are put in such an order that these follow one another.  Either way eight
-// lanes' 16 bytes (16 lanes' 8) fall on different banks.  The chunk's place is linear over XOR in the row's low bits.
+// Where chunk c of row r lies: as the tensor copies' swizzle of 128 (64) bytes has it.  Linear over XOR in r's low bits.
 template <int D>
-__device__ __forceinline__ constexpr int k_order(int r) {
-  return D >= 128 ? (r & 1) << 2 : 0;
+__device__ __forceinline__ constexpr int order(int r) {
+  return D >= 128 ? r & 7 : r >> 1 & 3;
+}
+template <int D, int KT>
+__device__ __forceinline__ constexpr int place(int r, int c) {
+  using S = Shape8<D, KT>;
+  return c / 8 * S::kPart + r * S::kRow + (((c & 7) ^ order<D>(r)) << 4);
+}
+// The key of a score tile's row g of 8.  Lanes read chunks 0-3 or 4-7 of K of two neighbouring rows g at once, and one
+// or two neighbouring chunks of V of rows g, g + 2, g + 4 and g + 6: with these keys, all of either on different banks.
+template <int D>
+__device__ __forceinline__ constexpr int key_of(int g) {
+  return D >= 128 ? g ^ (g & 1) << 2 : ((g >> 1 & 1) | (g & 4)) ^ (g & 1) * 3;
 }
 template <int D>
-__device__ __forceinline__ constexpr int v_order(int r) {
-  return D >= 128 ? (r >> 1 & 3) << 1 : (r >> 2 & 1) << 1;
-}
-template <int D>
-__device__ __forceinline__ constexpr int v_row(int r) {
-  return D >= 128 ? r : (r & ~7) + (r >> 1 & 3) + (r & 1) * 4;
-}
-template <int D>
-__device__ __forceinline__ constexpr int k_place(int r, int c) {
-  return r * D + ((c ^ k_order<D>(r)) << 4);
-}
-template <int D>
-__device__ __forceinline__ constexpr int v_place(int r, int c) {
-  return v_row<D>(r) * D + ((c ^ v_order<D>(r)) << 4);
+__device__ __forceinline__ constexpr int row_of(int key) {  // the reverse
+  return D >= 128 ? key ^ (key & 1) << 2 : (key >> 1 & 1) | ((key ^ key >> 1) & 1) << 1 | (key & 4);
 }
 
 // What a warp has of q and does with a tile.  HALVES: f16 halves of q and of the probabilities (bf16 1, f32 2).
@@ -114,38 +158,33 @@ struct Warp8 {
   static constexpr int kHalves = sizeof(T) == 4 ? 2 : 1;
   unsigned q[S::kSteps][NT][kHalves][2];
   float by[NT][2];  // what takes the column's sums of codes to scores in the log2 domain
-  unsigned k_at, v_at[4];  // this lane's offsets: of row lane / 4; of values 2 t, 2 t + 1, 2 t + 8, 2 t + 9, t = lane % 4
+  unsigned k_at, v_at[2];  // this lane's offsets: of row g = lane / 4 of K; of rows g = 2 (lane % 4), and one more, of V
 
   __device__ __forceinline__ explicit Warp8(int lane) {
-    k_at = k_place<D>(lane / 4, lane & 3);
+    k_at = place<D, KT>(key_of<D>(lane / 4), lane & 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (lane & 3) * 2 + (i & 1) + (i >> 1) * 8;
-      v_at[i] = S::kBytes == 16 ? v_place<D>(r, lane / 4) : v_place<D>(r, lane / 8) + (lane / 4 & 1) * 8;
+    for (int i = 0; i < 2; ++i) {
+      const int r = key_of<D>((lane & 3) * 2 + i);
+      v_at[i] = S::kBytes == 16 ? place<D, KT>(r, lane / 4) : place<D, KT>(r, lane / 8) + (lane / 4 & 1) * 8;
     }
   }
 
-  // row(n): q's row of column n of the block, or nullptr; this warp's begin at row0
-  template <typename F>
-  __device__ __forceinline__ void load_q(F row, int lane, int row0, float scale_log2) {
+  // rows: q's rows of the block in shared memory, ROW bytes apart; this warp's begin at row0
+  template <int ROW>
+  __device__ __forceinline__ void load_q(unsigned rows, int lane, int row0, float scale_log2) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const T *p = row(row0 + nt * 8 + lane / 4);
+      const unsigned p = rows + (row0 + nt * 8 + lane / 4) * ROW;
       // step ks of 64-element group ks / 4: elements (lane % 4) * 16 + ks % 4 * 4 .. + 4 of the group
       float x[S::kSteps][4], top = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < S::kSteps; ++ks) {
-        const T *e = p + (ks >> 2) * 64 + (lane & 3) * 16 + (ks & 3) * 4;
-        if constexpr (sizeof(T) == 2) {
+        Words<sizeof(T)> e;  // four elements
+        load_words(e, p + ((ks >> 2) * 64 + (lane & 3) * 16 + (ks & 3) * 4) * static_cast<int>(sizeof(T)));
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const unsigned u = p ? reinterpret_cast<const unsigned *>(e)[b] : 0u;
-            x[ks][2 * b] = __uint_as_float(u << 16);
-            x[ks][2 * b + 1] = __uint_as_float(u & 0xffff0000u);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[ks][i] = p ? e[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 2) x[ks][i] = __uint_as_float(i & 1 ? e.w[i / 2] & 0xffff0000u : e.w[i / 2] << 16);
+          else x[ks][i] = __uint_as_float(e.w[i]);
         }
       }
 #pragma unroll
@@ -176,19 +215,12 @@ struct Warp8 {
   // s = K Q^T of 16 keys, as sums of codes
   __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile) const {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-#pragma unroll
     for (int g = 0; g < D / 64; ++g) {
       Words<4> lo, hi;
-      const unsigned at = k_tile + (k_at ^ ((g & 1) << 6)) + (g >> 1) * 128;
+      const unsigned at = k_tile + (k_at ^ ((g & 1) << 6)) + (g >> 1) * S::kPart;
       load_words(lo, at);
-      load_words(hi, at + 8 * D);
-      float t[NT][4];
-      if constexpr (kHalves == 2) {
-        // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements, and added outside
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.0f;
-      }
+      load_words(hi, at + 8 * S::kRow);
+      float t[NT][4];  // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements
       unsigned a[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -202,13 +234,18 @@ struct Warp8 {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(kHalves == 2 ? t[nt] : s[nt], a[i], q[g * 4 + i][nt][h][0], q[g * 4 + i][nt][h][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float (&to)[4] = kHalves == 2 && g > 0 ? t[nt] : s[nt];
+            const bool first = i == 0 && h == kHalves - 1 && (kHalves == 2 || g == 0);
+            if (first) mma_f16_first(to, a[i], q[g * 4 + i][nt][h][0], q[g * 4 + i][nt][h][1]);
+            else mma_f16(to, a[i], q[g * 4 + i][nt][h][0], q[g * 4 + i][nt][h][1]);
+          }
       if constexpr (kHalves == 2) {
+        if (g > 0)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j];
+            for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j];
       }
     }
   }
@@ -237,13 +274,13 @@ struct Warp8 {
     Words<S::kBytes / 4> r[4];
     __device__ __forceinline__ void load(const Warp8 &w, unsigned v_tile, int piece) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_words(r[i], v_tile + w.v_at[i] + piece * 128);
+      for (int i = 0; i < 4; ++i) load_words(r[i], v_tile + w.v_at[i & 1] + (i >> 1) * 8 * S::kRow + piece * S::kPart);
     }
     // keys outside [k0, k1) as zeros
     __device__ __forceinline__ void keep(int k0, int k1, int lane) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int key = (lane & 3) * 2 + (i & 1) + (i >> 1) * 8;
+        const int key = key_of<D>((lane & 3) * 2 + (i & 1)) + (i >> 1) * 8;
         if (key < k0 || key >= k1)
 #pragma unroll
           for (int x = 0; x < S::kBytes / 4; ++x) r[i].w[x] = 0u;
@@ -267,36 +304,344 @@ struct Warp8 {
       a[3] = codes_f16x2(y, 2);
     }
   };
-  // y += V^T P^T
-  static __device__ __forceinline__ void weigh(float (&y)[4], const unsigned (&a)[4], const P &p, int nt) {
+  // y = V^T P^T (first) or y += V^T P^T
+  static __device__ __forceinline__ void weigh(float (&y)[4], const unsigned (&a)[4], const P &p, int nt, bool first) {
 #pragma unroll
-    for (int h = kHalves - 1; h >= 0; --h) mma_f16(y, a, p.b[nt][h][0], p.b[nt][h][1]);
+    for (int h = kHalves - 1; h >= 0; --h)
+      if (first && h == kHalves - 1) mma_f16_first(y, a, p.b[nt][h][0], p.b[nt][h][1]);
+      else mma_f16(y, a, p.b[nt][h][0], p.b[nt][h][1]);
   }
 };
 
 // The join of a CTA's warps goes through shared memory in pieces of 8 rows x join_cols.
 template <int D>
 constexpr int join_cols() {
-  return D < 256 ? D : 128;
+  return D < 256 ? 64 : 128;
 }
 template <int D, int WARPS>
 constexpr int join_bytes() {
   return WARPS * 8 * (join_cols<D>() + 4) * 4;
 }
 
-// A variant: NT 8-row tiles of a warp, RW warps that share a ring, each with rows of its own, WARPS of a CTA, KT matrix
-// tiles of 16 keys in a step, CTAS on an SM, SLOTS half tiles in a CTA's rings together.
-template <typename T_, int D_, int NT_, int RW_, int WARPS_, int KT_, int CTAS_, int SLOTS_>
+// A variant: NT 8-row tiles of a warp, RW warps that share their tiles, each with rows of its own, WARPS of a CTA beside
+// the FEED that feed them, KT matrix tiles of 16 keys in a step, CTAS on an SM.  BOXED: pages hold whole groups of 8 keys.
+template <typename T_, int D_, int NT_, int RW_, int WARPS_, int FEED_, int KT_, int CTAS_, bool BOXED_>
 struct Pick8 {
   using T = T_;
-  static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, KT = KT_, CTAS = CTAS_, SLOTS = SLOTS_;
-  static constexpr int rows = NT * RW * 8, ctas = kSms * CTAS;
-  static constexpr int smem = SLOTS * Shape8<D, KT>::kHalf + join_bytes<D, WARPS>();
-  static_assert((smem + 1024 + 700) * CTAS <= 228 * 1024, "the CTAs fit an SM's shared memory");
+  using S = Shape8<D_, KT_>;
+  static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, FEED = FEED_, KT = KT_, CTAS = CTAS_;
+  static constexpr bool BOXED = BOXED_;
+  static constexpr int rows = NT * RW * 8, ctas = kSms * CTAS, threads = 32 * (WARPS + FEED);
+  // items that are known ahead, with their q
+  static constexpr int q_row = D * static_cast<int>(sizeof(T)) + 16, q_bytes = rows * q_row, slots = q_bytes <= 2400 ? 4 : q_bytes <= 4800 ? 3 : 2;
+  // beside a stage: the scales of its groups of 8 keys (of its keys), and of their values
+  static constexpr int groups = BOXED ? KT * 2 : S::kTile, scales = 2 * groups * 4;
+  static constexpr int fixed = join_bytes<D, WARPS>() + slots * q_bytes;
+  // the ring has what the SM's shared memory holds beside that and the static part
+  static constexpr int fit = (228 * 1024 / CTAS - 1024 - 1024 - 512 - 64 * WARPS * NT - 24 * 32 - fixed) / (S::kStage + scales);
+  // A stage is always filled by the same warp and emptied by the same group: waits tell two phases of a barrier apart, and
+  // who let one pass would take the next but one for it.
+  static constexpr int turn = std::lcm(WARPS / RW, FEED), STAGES = (fit < 32 ? fit : 32) / turn * turn;
+  static constexpr int smem = 1024 + STAGES * (S::kStage + scales) + fixed;  // stages begin at multiples of 1024
+  static_assert(STAGES > WARPS / RW && STAGES % (WARPS / RW) == 0 && STAGES % FEED == 0, "two stages per key group at least");
 };
 
+// An item, or the part of it that lies in a CTA's share, as the feeding warps tell the others.
+struct Job {
+  int k0, k1;           // its keys
+  int t0, tokens, len;  // its request's rows of q, and keys
+  int rows, head, block;
+  int slot;   // where its sums go in the workspace; -1: it lies in this CTA, and its results go to the output
+  int last;   // the last CTA that has a part of it, where it begins in this one; else -1
+  int none;   // there is none any more
+};
+
+// What the feeding warps and the others share beside the ring: shared-memory addresses.
+struct Ring {
+  unsigned stages, scales, q, missing;
+  unsigned full, empty, job_full, job_empty, met;  // of barriers: of a stage, of a job's slot, of the CTA's key groups
+  Job *jobs;
+};
+
+// A feeding warp: puts every FEED-th tile of the share's items into the ring, and the first one an item's rows of q before.
+// (One alone takes 600 to 1000 clocks for a tile, all latency: waits, exchanges of lanes, 140 to issue a tensor copy.)
 template <typename P>
-__global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(const __grid_constant__ Call c) {
+struct Feed {
+  using T = typename P::T;
+  using S = typename P::S;
+  static constexpr int D = P::D, kTile = S::kTile;
+  using Part = Item<P::rows, 1, kTile>;
+  const Call &c;
+  const Ring &ring;
+  int lane, id;
+  int stage, slot = 0;
+  int skip;  // tiles before this warp's next one, from the item's first
+  unsigned phase = 1, job_phase = 1;
+  bool filled = false;  // every stage has been
+
+  __device__ __forceinline__ Feed(const Call &c_, const Ring &r) : c(c_), ring(r), lane(threadIdx.x & 31), id((threadIdx.x >> 5) - P::WARPS), stage(id), skip(id) {}
+
+  // Copies have to land before the CTA ends: where every wait ended well, the other warps have seen to it.
+  __device__ __forceinline__ bool give_up() {
+    report(GDN_DEVICE_WAIT_TIMEOUT);
+    for (int x = id; x < P::STAGES; x += P::FEED)
+      if (x < stage || filled) mbar_wait(ring.full + x * 8, x < stage ? phase ^ 1 : phase);
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    return false;
+  }
+  // The item at unit u as a job, and its rows of q: row n is token n / group, query head n % group of the key head; zeros
+  // for those that are not.
+  __device__ __forceinline__ bool put_job(const Share &sh, const Part &f, int head, long long u) {
+    if (id != 0) return true;
+    if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) return give_up();
+    const int block = f.item - head * f.r.blocks, rows = f.r.tokens * static_cast<int>(c.group);
+    if (lane == 0) {
+      Job &j = ring.jobs[slot];
+      j.k0 = f.k0;
+      j.k1 = f.k1;
+      j.t0 = f.r.t0;
+      j.tokens = f.r.tokens;
+      j.len = f.r.len;
+      j.rows = rows;
+      j.head = head;
+      j.block = block;
+      j.none = 0;
+      const bool whole = f.tile0 == 0 && f.tile1 == f.r.tiles;
+      j.slot = whole ? -1 : 2 * sh.cta + (u == sh.u0 ? 0 : 1);  // an item that goes on from the CTA before is the share's first
+      j.last = -1;
+      if (!whole && f.tile0 == 0) {
+        const long long end = u + f.units + (f.r.tiles - f.tile1) - 1;  // the item's last unit
+        j.last = static_cast<int>(((end + 1) * sh.ctas - 1) / sh.total);
+      }
+      mbar_arrive(ring.job_full + slot * 8);
+    }
+    if (f.k0 < f.k1) {
+      const unsigned to = ring.q + slot * P::q_bytes;
+      auto copy = [&](auto bytes) {
+        constexpr int kBytes = bytes(), kOf = D * static_cast<int>(sizeof(T)) / kBytes;
+#pragma unroll 4
+        for (int x = lane; x < P::rows * kOf; x += 32) {
+          const int n = x / kOf, col = x % kOf * kBytes, row = block * P::rows + n, t = c.group_div.div(row);
+          const char *src = static_cast<const char *>(c.q);
+          if (row < rows)
+            src += (static_cast<int64_t>(f.r.t0 + t) * c.q_stride + (static_cast<int64_t>(head) * c.group + (row - t * static_cast<int>(c.group))) * D) *
+                       static_cast<int>(sizeof(T)) + col;
+          const int size = row < rows ? kBytes : 0;
+          const unsigned dst = to + n * P::q_row + col;
+          if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(size) : "memory");
+          else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(size) : "memory");
+        }
+      };
+      if (c.q_wide) copy(std::integral_constant<int, 16>{});
+      else copy(std::integral_constant<int, 4>{});
+    }
+    next_job();
+    return true;
+  }
+  // After the last item.
+  __device__ __forceinline__ void put_end() {
+    if (id == 0) {
+      if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) {
+        give_up();
+        return;
+      }
+      if (lane == 0) {
+        ring.jobs[slot].none = 1;
+        mbar_arrive(ring.job_full + slot * 8);
+      }
+      next_job();
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  }
+  __device__ __forceinline__ void next_job() {
+    mbar_arrive_after_copies(ring.job_full + slot * 8);
+    if (++slot == P::slots) {
+      slot = 0;
+      job_phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void next_stage() {
+    stage += P::FEED;
+    if (stage >= P::STAGES) {
+      stage -= P::STAGES;
+      phase ^= 1;
+      filled = true;
+    }
+  }
+  // Past an item of n tiles.
+  __device__ __forceinline__ void next_item(int n) { skip = (skip + P::FEED - n % P::FEED) % P::FEED; }
+};
+
+// Boxes of c.box rows of a page by tensor copies.  A lane has one box of 32: its page, the place in it and its scales,
+// the pages looked up two such batches ahead and the scales one.
+template <typename P>
+__device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_map, const CUtensorMap *v_map, const Share &sh, uint32_t seq,
+                                           long long in_seq, const Ring &ring) {
+  using S = typename P::S;
+  constexpr int kTile = S::kTile;
+  Feed<P> d(c, ring);
+  const int lane = d.lane, box = c.box, per_tile = kTile / box, batch = 32 * box;
+  typename Feed<P>::Part f;
+  f.seq = seq;
+  f.in_seq = in_seq;
+  f.r = request<P::rows>(c, seq);
+  long long u = sh.u0;
+  // of a batch: this lane's box's page, or -1 where there is none, and its scales; what an item begins with is found while the
+  // one before is fed
+  auto page_of = [&](const typename Feed<P>::Part &x, int key) {
+    return key < x.k1 ? c.table[static_cast<uint64_t>(x.seq) * c.max_pages + c.page_div.div(key)] : -1;
+  };
+  auto scale_of = [&](const float *scales, int page, int head) {
+    return static_cast<uint32_t>(page) < c.n_pages ? scales[static_cast<uint64_t>(page) * c.n_kv + head] : 0.0f;
+  };
+  bool more = f.find(c, u, sh.u1);
+  if (!more) {
+    d.put_end();
+    return;
+  }
+  int page = page_of(f, f.k0 + lane * box), page1 = page_of(f, f.k0 + batch + lane * box);
+  float ks = scale_of(c.k_scale, page, f.item / f.r.blocks), vs = scale_of(c.v_scale, page, f.item / f.r.blocks);
+  while (more) {
+    typename Feed<P>::Part g = f;
+    int g_page = -1, g_page1 = -1;
+    const int head = f.item / f.r.blocks;
+    if (!d.put_job(sh, f, head, u)) return;
+    bool looked = false;
+    auto look_ahead = [&] {
+      looked = true;
+      g.pass(u);
+      more = g.find(c, u, sh.u1);
+      if (more) {
+        g_page = page_of(g, g.k0 + lane * box);
+        g_page1 = page_of(g, g.k0 + batch + lane * box);
+      }
+    };
+    for (int b0 = f.k0; b0 < f.k1; b0 += batch) {
+      const int key = b0 + lane * box;
+      const int at = key - static_cast<int>(c.page_div.div(key) * c.page_size);
+      const bool there = static_cast<uint32_t>(page) < c.n_pages;
+      const unsigned valid = __ballot_sync(kFull, there);
+      const unsigned gone = __ballot_sync(kFull, !there && key < f.k1 && key + box > f.r.first);
+      const int page2 = page_of(f, key + 2 * batch);
+      const float ks1 = scale_of(c.k_scale, page1, head), vs1 = scale_of(c.v_scale, page1, head);
+#pragma unroll 1
+      for (int x = d.skip * per_tile; x < 32 && b0 + x * box < f.k1; x += P::FEED * per_tile) {
+        const unsigned of_tile = ((2u << (per_tile - 1)) - 1) << x;
+        const unsigned full = ring.full + d.stage * 8, to = ring.stages + d.stage * S::kStage;
+        if (!mbar_wait(ring.empty + d.stage * 8, d.phase)) {
+          d.give_up();
+          return;
+        }
+        {  // lane i has the scales of the tile's group i of 8 keys
+          const int i = x + (lane & (P::groups - 1)) * 8 / box;
+          const float of_k = __shfl_sync(kFull, ks, i), of_v = __shfl_sync(kFull, vs, i);
+          if (lane < P::groups) {
+            const unsigned dst = ring.scales + d.stage * P::scales + lane * 4;
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst), "f"(of_k) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst + P::groups * 4), "f"(of_v) : "memory");
+          }
+        }
+        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(ring.missing + d.stage * 4), "r"(gone & of_tile) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_expect(full, __popc(valid & of_tile) * box * 2 * P::D);
+        // boxes past the item's end, or of no page, are left as they are and cut out later
+#pragma unroll 1
+        for (unsigned left = valid & of_tile; left; left &= left - 1) {
+          const int i = __ffs(left) - 1, pg = __shfl_sync(kFull, page, i), row = __shfl_sync(kFull, at, i);
+          const unsigned dst = to + (i - x) * box * S::kRow;
+          if (lane == 0) {
+#pragma unroll
+            for (int e = 0; e < S::kParts; ++e) {
+              copy_box(dst + e * S::kPart, k_map, e * 128, row, head, pg, full);
+              copy_box(dst + S::kCodes + e * S::kPart, v_map, e * 128, row, head, pg, full);
+            }
+          }
+        }
+        d.next_stage();
+        if (!looked) look_ahead();
+      }
+      page = page1;
+      page1 = page2;
+      ks = ks1;
+      vs = vs1;
+    }
+    if (!looked) look_ahead();
+    d.next_item((f.k1 - f.k0 + kTile - 1) / kTile);
+    f = g;
+    page = g_page;
+    page1 = g_page1;
+    if (more) {
+      ks = scale_of(c.k_scale, page, f.item / f.r.blocks);
+      vs = scale_of(c.v_scale, page, f.item / f.r.blocks);
+    }
+  }
+  d.put_end();
+}
+
+// Row by row, for pages of any size: a lane has a key of the tile.
+template <typename P>
+__device__ __forceinline__ void feed_rows(const Call &c, const Share &sh, uint32_t seq, long long in_seq, const Ring &ring) {
+  using S = typename P::S;
+  constexpr int D = P::D, kTile = S::kTile;
+  constexpr int kPer = 32 / S::kChunks;               // rows one access of the warp covers
+  constexpr int kAccesses = kTile * S::kChunks / 32;  // of K or V
+  Feed<P> d(c, ring);
+  const int lane = d.lane, my_row = lane / S::kChunks, my_chunk = lane % S::kChunks;
+  const unsigned mine = place<D, P::KT>(my_row, my_chunk);
+  const char *const k = static_cast<const char *>(c.k) + my_chunk * 16, *const v = static_cast<const char *>(c.v) + my_chunk * 16;
+  typename Feed<P>::Part f;
+  f.seq = seq;
+  f.in_seq = in_seq;
+  f.r = request<P::rows>(c, seq);
+  for (long long u = sh.u0; f.find(c, u, sh.u1); f.pass(u)) {
+    const int head = f.item / f.r.blocks;
+    const int32_t *const table = c.table + static_cast<uint64_t>(f.seq) * c.max_pages;
+    if (!d.put_job(sh, f, head, u)) return;
+    int key = f.k0 + d.skip * kTile + (lane & (kTile - 1));
+    int page = key < f.k1 ? table[c.page_div.div(key)] : 0;
+    for (int tile = f.k0 + d.skip * kTile; tile < f.k1; tile += P::FEED * kTile) {
+      const int ahead = key + P::FEED * kTile, next = ahead < f.k1 ? table[c.page_div.div(ahead)] : 0;
+      const bool none = static_cast<uint32_t>(page) >= c.n_pages, valid = key < f.k1 && !none;
+      const bool gone = __any_sync(kFull, none && key < f.k1 && key >= f.r.first);
+      const int o = key - static_cast<int>(c.page_div.div(key) * c.page_size);
+      const long long row_at = valid ? page * c.page_stride + head * c.head_stride + o * c.slot_stride : -1;  // -1: zeros
+      const uint64_t scale_at = (valid ? static_cast<uint64_t>(page) * c.n_kv : 0) + head;
+      const unsigned full = ring.full + d.stage * 8, to = ring.stages + d.stage * S::kStage;
+      if (!mbar_wait(ring.empty + d.stage * 8, d.phase)) {
+        d.give_up();
+        return;
+      }
+      if (lane < kTile) {
+        const unsigned dst = ring.scales + d.stage * P::scales + lane * 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(c.k_scale + scale_at) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst + kTile * 4), "l"(c.v_scale + scale_at) : "memory");
+      }
+      if (lane == 0) {
+        asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(ring.missing + d.stage * 4), "r"(static_cast<unsigned>(gone)) : "memory");
+        mbar_arrive(full);
+      }
+#pragma unroll
+      for (int x = 0; x < kAccesses; ++x) {
+        const int row = x * kPer;  // behind my_row
+        const long long off = __shfl_sync(kFull, row_at, my_row + row);
+        const long long from = off < 0 ? 0 : off;
+        const unsigned dst = to + (mine ^ (order<D>(row) << 4)) + row * S::kRow;
+        cp_async_16_or_zero(dst, k + from, off >= 0);
+        cp_async_16_or_zero(dst + S::kCodes, v + from, off >= 0);
+      }
+      mbar_arrive_after_copies(full);
+      d.next_stage();
+      key = ahead;
+      page = next;
+    }
+    d.next_item((f.k1 - f.k0 + kTile - 1) / kTile);
+  }
+  d.put_end();
+}
+
+template <typename P>
+__global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const __grid_constant__ Call c, const __grid_constant__ CUtensorMap k_map,
+                                                                             const __grid_constant__ CUtensorMap v_map) {
   using T = typename P::T;
   constexpr int D = P::D, NT = P::NT, RW = P::RW, WARPS = P::WARPS, KT = P::KT;
   using S = Shape8<D, KT>;
@@ -304,190 +649,73 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
   constexpr int kTile = S::kTile;
   constexpr int kJoinCols = join_cols<D>(), kJoinRow = kJoinCols + 4;
   constexpr int kRows = P::rows;       // rows of a block
-  constexpr int KW = WARPS / RW;       // key groups
-  constexpr int kStep = kTile * KW;    // keys from a group's tile to its next
-  constexpr int kRing = P::SLOTS / KW;
-  static_assert(kRing >= 3 && kRing <= 32, "a bit per slot");
+  constexpr int KW = WARPS / RW;       // key groups: group g takes every KW-th tile of the share
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[WARPS], s_offset;
+  __shared__ long long s_scan[WARPS + P::FEED], s_offset;
   __shared__ uint32_t s_seq;
   __shared__ float s_m[WARPS][NT * 8], s_l[WARPS][NT * 8];
   __shared__ int s_bad[WARPS];
+  __shared__ unsigned s_missing[P::STAGES];
+  __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_met;
+  __shared__ Job s_jobs[P::slots];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kg = warp / RW, rg = warp % RW, row0 = rg * NT * 8;  // key group; rows of the block
-  const unsigned ring = smem_u32(smem) + kg * kRing * S::kHalf;
-  float *join = reinterpret_cast<float *>(smem + P::SLOTS * S::kHalf);
+  const unsigned start = (1024u - (smem_u32(smem) & 1023u)) & 1023u;
+  float *join = reinterpret_cast<float *>(smem + start + P::STAGES * (S::kStage + P::scales));
+  const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + join_bytes<D, WARPS>(),
+                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(&s_met), s_jobs};
+  if (tid < P::STAGES) {
+    mbar_init(ring.full + tid * 8, P::BOXED ? 1 : 33);  // what the feeding warp stores, and its lanes' copies
+    mbar_init(ring.empty + tid * 8, RW);
+  }
+  if (tid < P::slots) {
+    mbar_init(ring.job_full + tid * 8, 33);
+    mbar_init(ring.job_empty + tid * 8, WARPS);
+  }
+  if (tid == 0) mbar_init(ring.met, WARPS);
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   begin_in_order();
-  const Share sh = take_share<kRows, WARPS>(c, s_scan, s_seq, s_offset);
+  const Share sh = take_share<kRows, WARPS + P::FEED>(c, s_scan, s_seq, s_offset);  // (its barriers show the initialised ones)
   if (sh.cta >= sh.ctas) return;
-  const int cta = sh.cta, ctas = sh.ctas;
-  const long long total = sh.total, u0 = sh.u0, u1 = sh.u1;
-
-  // The ring's feed runs ahead of the products, across items: `f` is the item
-  // that the next half tile belongs to, `f_i` its tile.
-  Item<kRows, KW, kTile> f;
-  f.seq = s_seq;
-  f.in_seq = s_offset;
-  f.r = request<kRows>(c, f.seq);
-  Item<kRows, KW, kTile> it = f;
-  long long f_u = u0;
-  int f_i = 0, f_n = 0, f_head = 0;
-  unsigned f_slot = 0;
-  const int32_t *f_table = nullptr;
-  bool f_value = false, f_any = false;
-  unsigned bad_slots = 0;  // bit i: a page of the K tile in slot i of the ring is none of the cache's, and not wholly
-                           // before the window: pages that the window has left may be given back
-  // the next tile's pages, looked up a tile ahead: of its 16-key parts, or of this lane's row
-  constexpr int kPer = 32 / S::kChunks;                    // rows one access of the warp covers
-  constexpr int kAccesses = kTile * S::kChunks / 32 / RW;  // of this warp for a half tile
-  static_assert(kAccesses >= 1, "every warp of a key group has a part of a half tile");
-  int page[KT];
-  long long row_at[KT];  // byte offset of the part's first row (of this lane's row; -1: zeros) in the caches
-  const int my_row = lane / S::kChunks + rg * (kTile / RW), my_chunk = lane % S::kChunks;
-  const long long my_src = (my_row & (kSub - 1)) * c.slot_stride + my_chunk * 16;
-  const unsigned my_k = k_place<D>(my_row, my_chunk), my_v = v_place<D>(my_row, my_chunk);
-  auto look_up = [&] {
-    const int key = f.k0 + kTile * kg + f_i * kStep;
-    if (c.whole_tiles) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) page[kt] = key + kt * kSub < f.k1 ? f_table[c.page_div.div(key + kt * kSub)] : 0;
-    } else {
-      const int mine = key + (lane & (kTile - 1));
-      page[0] = mine < f.k1 ? f_table[c.page_div.div(mine)] : 0;
-    }
-  };
-  auto next_item = [&] {  // to the next item in which this key group has a tile
-    for (f_any = false; f.find(c, f_u, u1); ) {
-      f.pass(f_u);
-      f_n = f.tiles_of(kg);
-      if (f_n > 0) {
-        f_any = true;
-        f_i = 0;
-        f_head = f.item / f.r.blocks;
-        f_table = c.table + static_cast<uint64_t>(f.seq) * c.max_pages;
-        look_up();
-        break;
-      }
-    }
-  };
-  int head = 0, block = 0;
+  if (warp >= WARPS) {
+    if constexpr (P::BOXED) feed_boxes<P>(c, &k_map, &v_map, sh, s_seq, s_offset, ring);
+    else feed_rows<P>(c, sh, s_seq, s_offset, ring);
+    return;
+  }
+  const int kg = warp / RW, rg = warp % RW, row0 = rg * NT * 8;  // key group; rows of the block
   W w(lane);
-  auto begin_q = [&] {
-    head = it.item / it.r.blocks;
-    block = it.item - head * it.r.blocks;
-    // Column n of the score tile is row block * kRows + n of the item: token row / group, query head row % group.
-    const int rows = it.r.tokens * static_cast<int>(c.group);
-    auto q_row = [&](int n) -> const T * {
-      const int row = block * kRows + n;
-      if (row >= rows) return nullptr;
-      const int t = c.group_div.div(row);
-      return static_cast<const T *>(c.q) + static_cast<int64_t>(it.r.t0 + t) * c.q_stride +
-             (static_cast<int64_t>(head) * c.group + (row - t * static_cast<int>(c.group))) * D;
-    };
-    w.load_q(q_row, lane, row0, c.scale_log2);
-  };
-  long long u = u0;
-  bool more = it.find(c, u, u1);
-
-  next_item();
-  auto fetch = [&] {  // the next half tile: K of a tile and both its scales, then its V
-    if (f_any) {
-      const char *base = static_cast<const char *>(f_value ? c.v : c.k);
-      const unsigned to = ring + f_slot * S::kHalf;
-      if (!f_value) {
-        const int key = f.k0 + kTile * kg + f_i * kStep;
-        bool gone = false;
-        uint32_t of_scale = 0;  // the page of this lane's key
-        if (c.whole_tiles) {  // 16 keys lie in one page: rows past the end are another request's or stale, and cut out later
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            const int k = key + kt * kSub;
-            const int o = k - static_cast<int>(c.page_div.div(k) * c.page_size);
-            const bool none = static_cast<uint32_t>(page[kt]) >= c.n_pages;
-            gone |= none && k + kSub > f.r.first;
-            if (none) page[kt] = 0;
-            row_at[kt] = page[kt] * c.page_stride + f_head * c.head_stride + o * c.slot_stride;
-            if (lane / kSub == kt) of_scale = page[kt];
-          }
-        } else {
-          const int k = key + (lane & (kTile - 1));
-          const int o = k - static_cast<int>(c.page_div.div(k) * c.page_size);
-          const bool none = static_cast<uint32_t>(page[0]) >= c.n_pages;
-          gone = none && k >= f.r.first && k < f.k1;
-          row_at[0] = k < f.k1 && !none ? page[0] * c.page_stride + f_head * c.head_stride + o * c.slot_stride : -1;
-          of_scale = none ? 0 : page[0];
-        }
-        bad_slots = (bad_slots & ~(1u << f_slot)) | static_cast<unsigned>(gone) << f_slot;
-        if (rg == 0 && lane < kTile) {
-          const uint64_t at = static_cast<uint64_t>(of_scale) * c.n_kv + f_head;
-          const unsigned dst = to + S::kCodes + lane * 4;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(c.k_scale + at) : "memory");
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst + kTile * 4), "l"(c.v_scale + at) : "memory");
-        }
-      }
-      const unsigned mine = f_value ? my_v : my_k;
-      if (c.whole_tiles) {
-#pragma unroll
-        for (int x = 0; x < kAccesses; ++x) {
-          const int row = x * kPer;  // behind my_row
-          const long long at = KT == 1 ? row_at[0] : RW == 1 ? row_at[row / kSub] : my_row + row < kSub ? row_at[0] : row_at[KT - 1];
-          const unsigned dst = to + (mine ^ ((f_value ? v_order<D>(row) : k_order<D>(row)) << 4)) + row * D;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(base + at + my_src + (row & (kSub - 1)) * c.slot_stride)
-                       : "memory");
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < kAccesses; ++x) {
-          const int row = x * kPer;
-          const unsigned dst = to + (mine ^ ((f_value ? v_order<D>(row) : k_order<D>(row)) << 4)) + row * D;
-          const long long off = __shfl_sync(kFull, row_at[0], my_row + row);
-          cp_async_16_or_zero(dst, base + (off < 0 ? 0 : off) + my_chunk * 16, off >= 0);
-        }
-      }
-      f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
-      if (f_value) {
-        if (++f_i < f_n) look_up();
-        else next_item();
-      }
-      f_value = !f_value;
+  int slot = 0, stage = kg;
+  int ahead = kg;  // tiles until this group's next one, from the job's first
+  unsigned phase = 0, job_phase = 0, met_phase = 0;
+  bool dead = false;  // a wait ran out: the job at hand is the last
+  auto wait = [&](unsigned bar, unsigned of) {
+    if (!dead && !mbar_wait(bar, of)) {
+      dead = true;
+      report(GDN_DEVICE_WAIT_TIMEOUT);
     }
-    cp_async_commit();
   };
-#pragma unroll 1
-  for (int h = 0; h < kRing - 1; ++h) fetch();
-  if (more) begin_q();
-  // Before a half tile is used: its copies are there, for every warp of the group, and all of them are done with
-  // the one before, whose slot the next copies take.
-  auto arrived = [&] {
-    cp_async_wait<kRing - 2>();
-    if constexpr (RW == 1)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + kg), "n"(32 * RW) : "memory");
-    fetch();
+  auto meet = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.met);
+    wait(ring.met, met_phase);
+    met_phase ^= 1;
   };
-
-  unsigned slot = 0;
-  while (more) {
-    const Request &r = it.r;
-    const int rows = r.tokens * static_cast<int>(c.group);
-    // the last key each of this lane's columns sees
-    int last[NT][2], token[NT][2];
+  while (true) {
+    wait(ring.job_full + slot * 8, job_phase);
+    if (dead) break;
+    const Job &job = s_jobs[slot];
+    if (job.none) break;
+    // the last key each of this lane's columns sees, and keys that every row of this warp does: [all0, all1)
+    int last[NT][2];
+    const int first_row = job.block * kRows + row0, before = job.len - job.tokens, k1 = job.k1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = min(block * kRows + row0 + nt * 8 + (lane & 3) * 2 + j, rows - 1);
-        token[nt][j] = c.group_div.div(row);
-        last[nt][j] = r.len - r.tokens + token[nt][j];
-      }
-    const int t_first = c.group_div.div(min(block * kRows + row0, rows - 1));
-    const int t_last = c.group_div.div(min(block * kRows + row0 + NT * 8, rows) - 1);
-    // keys in [all0, all1) are seen by every row of this warp
-    const int all1 = min(r.len - r.tokens + t_first + 1, it.k1);
-    const int all0 = c.window ? less_window(r.len - r.tokens + t_last + 1, c.window) : 0;
+      for (int j = 0; j < 2; ++j) last[nt][j] = before + static_cast<int>(c.group_div.div(min(first_row + nt * 8 + (lane & 3) * 2 + j, job.rows - 1)));
+    const int last0 = before + static_cast<int>(c.group_div.div(min(first_row, job.rows - 1)));  // of the first and the last row
+    const int last1 = before + static_cast<int>(c.group_div.div(min(first_row + NT * 8, job.rows) - 1));
+    const int all1 = min(last0 + 1, k1), all0 = c.window ? less_window(last1 + 1, c.window) : 0;
 
     // Sums are kept relative to 2^m; m is 2^kTopBits below the running maximum, which it follows only when that has
     // grown by more than 2^kLagBits, so that the rescaling is rare.  Starting from the lowest finite value, a column
@@ -501,31 +729,43 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    const int n_tiles = it.tiles_of(kg);
-    int key0 = it.k0 + kTile * kg;
+    const int n_tiles = (k1 - job.k0 + kTile - 1) / kTile;
+    int key0 = job.k0 + ahead * kTile;
     bool bad_page = false;
+    if (ahead < n_tiles) w.template load_q<P::q_row>(ring.q + slot * P::q_bytes, lane, row0, c.scale_log2);
 #pragma unroll 1
-    for (int i = 0; i < n_tiles; ++i, key0 += kStep) {
+    for (; ahead < n_tiles; ahead += KW, key0 += kTile * KW) {
+      wait(ring.full + stage * 8, phase);
+      const unsigned k_tile = ring.stages + stage * S::kStage, v_tile = k_tile + S::kCodes, scales = ring.scales + stage * P::scales;
+      bad_page |= s_missing[stage] != 0u;
+      // the tile is done with: the next of this group
+      auto leave = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty + stage * 8);
+        stage += KW;
+        if (stage >= P::STAGES) {
+          stage -= P::STAGES;
+          phase ^= 1;
+        }
+      };
       // scores
-      arrived();
-      const unsigned k_tile = ring + slot * S::kHalf;
       float s[KT][NT][4];
       const bool edge = key0 + kTile > all1 || key0 < all0;
       // keys that a row of this warp sees, of the tile
-      const int seen0 = edge && c.window ? less_window(r.len - r.tokens + t_first + 1 - key0, c.window) : 0;
-      const int seen1 = edge ? min(r.len - r.tokens + t_last + 1, it.k1) - key0 : kTile;
+      const int seen0 = edge && c.window ? max(0, less_window(last0 + 1 - key0, c.window)) : 0;
+      const int seen1 = edge ? min(min(last1 + 1, k1) - key0, kTile) : kTile;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) w.scores(s[kt], k_tile + kt * kSub * D);
-      float vs[KT][2];  // the scales of this lane's keys' values
-      unsigned most = 0u, least = 0xffffffffu;
+      for (int kt = 0; kt < KT; ++kt) w.scores(s[kt], k_tile + kt * kSub * S::kRow);
+      float vs[KT][2];  // the scales of the values of this lane's keys; BOXED: of these groups of 8 keys
+      unsigned most = 0u, least = 0xffffffffu;  // of those that a row sees
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = kt * kSub + h * 8 + lane / 4;
-          const float ks = load_f32(k_tile + S::kCodes + key * 4);
-          vs[kt][h] = load_f32(k_tile + S::kCodes + (kTile + key) * 4);
-          if (key >= seen0 && key < seen1) {
+          const int from = kt * kSub + h * 8, key = from + (P::BOXED ? 0 : key_of<D>(lane / 4)), at = P::BOXED ? kt * 2 + h : key;
+          const float ks = load_f32(scales + at * 4);
+          vs[kt][h] = load_f32(scales + (P::groups + at) * 4);
+          if (!edge || (key + (P::BOXED ? 7 : 0) >= seen0 && key < seen1)) {
             most = max(most, __float_as_uint(vs[kt][h]));
             least = min(least, __float_as_uint(vs[kt][h]));
           }
@@ -541,13 +781,11 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int key = key0 + kt * kSub + lane / 4 + (j >> 1) * 8, hi = min(last[nt][j & 1], it.k1 - 1);
+              const int key = key0 + kt * kSub + key_of<D>(lane / 4) + (j >> 1) * 8, hi = min(last[nt][j & 1], k1 - 1);
               const long long lo = c.window ? static_cast<long long>(last[nt][j & 1]) - c.window : -1;
               if (key > hi || key <= lo) s[kt][nt][j] = -INFINITY;
             }
       }
-      bad_page |= bad_slots >> slot & 1;
-      slot = slot + 1 == kRing ? 0 : slot + 1;
       bool grown = false;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
@@ -592,8 +830,10 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
             l[nt][j] += s[kt][nt][j] + s[kt][nt][j + 2];
           }
       // The values' scales: one, or near one another and positive, or not (then `apart`).
-      most = __reduce_max_sync(kFull, most);
-      least = __reduce_min_sync(kFull, least);
+      if constexpr (!P::BOXED) {
+        most = __reduce_max_sync(kFull, most);
+        least = __reduce_min_sync(kFull, least);
+      }
       const float ref = __uint_as_float(most);
       bool apart = !(most < 0x7f800000u && __uint_as_float(least) * 256.0f >= ref) && most != 0u;
       if (most != least && !apart) {
@@ -613,28 +853,21 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) p[kt].take(s[kt]);
       // output
-      arrived();
-      const unsigned v_tile = ring + slot * S::kHalf;
-      slot = slot + 1 == kRing ? 0 : slot + 1;
-      // the tile's values, with CUT those of keys that no row sees as zeros
-      auto weigh = [&](auto cut) {
+      if (!edge && !apart) {
 #pragma unroll
-        for (int x = 0; x < S::kPieces; ++x) {
+        for (int x = 0; x < S::kParts; ++x) {
           typename W::V v[KT];
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            v[kt].load(w, v_tile + kt * kSub * D, x);
-            if constexpr (cut()) v[kt].keep(seen0 - kt * kSub, seen1 - kt * kSub, lane);
-          }
+          for (int kt = 0; kt < KT; ++kt) v[kt].load(w, v_tile + kt * kSub * S::kRow, x);
 #pragma unroll
           for (int md = 0; md < S::kBytes / 2; ++md) {
-            float y[NT][4] = {};
+            float y[NT][4];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
               unsigned a[4];
               v[kt].fragment(a, md);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) W::weigh(y[nt], a, p[kt], nt);
+              for (int nt = 0; nt < NT; ++nt) W::weigh(y[nt], a, p[kt], nt, kt == 0);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -642,57 +875,48 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
               for (int j = 0; j < 4; ++j) acc[x * (S::kBytes / 2) + md][nt][j] += ref * y[nt][j];
           }
         }
-      };
-      if (!edge && !apart) {
-        weigh(std::false_type{});
+        leave();
         continue;
       }
       // A key that a token does not see must not reach its row even as 0 * v (v may be stale or NaN).  Keys that no
-      // token of the warp sees are cut out of V; if tokens see different keys of the tile and one of those is NaN, each
-      // token's columns take products of their own.
+      // token of the warp sees are cut out of V; if tokens see different keys of the tile and one of those is NaN, or the
+      // scales are apart, each token's columns take products of their own, in the latter case 8 keys (or a page's) a time.
       const bool folded = !apart;
-      if (folded && t_first != t_last) {
+      if (folded && last0 != last1) {
         bool nan = false;
 #pragma unroll 1
-        for (int x = 0; x < S::kPieces * KT; ++x) {
+        for (int x = 0; x < S::kParts * KT; ++x) {
           typename W::V v;
-          v.load(w, v_tile + x % KT * kSub * D, x / KT);
+          v.load(w, v_tile + x % KT * kSub * S::kRow, x / KT);
           v.keep(seen0 - x % KT * kSub, seen1 - x % KT * kSub, lane);
           nan |= v.has_nan();
         }
         apart = __any_sync(kFull, nan);
       }
-      if (!apart) {
-        weigh(std::true_type{});
-        continue;
-      }
-      // Token by token and, where the scales are not in P, page by page.
 #pragma unroll 1
-      for (int t = t_first; t <= t_last; ++t) {
-        const int hi = min(r.len - r.tokens + t + 1, it.k1) - key0;
-        int from = c.window ? max(0, less_window(r.len - r.tokens + t + 1 - key0, c.window)) : 0;
-        while (from < min(hi, kTile)) {
-          int to = min(min(hi, kTile), (from / kSub + 1) * kSub);
+      for (int sees = apart ? last0 : last1; sees <= last1; ++sees) {  // the last key that the token sees
+        const int end = apart ? min(min(sees + 1, k1) - key0, kTile) : seen1;
+        int from = !apart ? seen0 : c.window ? max(0, less_window(sees + 1 - key0, c.window)) : 0;
+#pragma unroll 1
+        while (from < end) {
+          int to = min(end, (from / kSub + 1) * kSub);
           float by = ref;
           if (!folded) {
-            const int key = key0 + from;
-            to = min(to, from + static_cast<int>(c.page_size) - (key - static_cast<int>(c.page_div.div(key) * c.page_size)));
-            by = 0.0f;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float x = __shfl_sync(kFull, vs[kt][h], from % 8 * 4);
-                if (from / 8 == kt * 2 + h) by = x;
-              }
+            if constexpr (P::BOXED) {
+              to = min(to, (from / 8 + 1) * 8);
+            } else {
+              const int key = key0 + from;
+              to = min(to, from + static_cast<int>(c.page_size) - (key - static_cast<int>(c.page_div.div(key) * c.page_size)));
+            }
+            by = load_f32(scales + (P::groups + (P::BOXED ? from / 8 : from)) * 4);
           }
           const int kt0 = from / kSub;
           typename W::P pk = p[0];
           if (KT > 1 && kt0 > 0) pk = p[KT - 1];
 #pragma unroll
-          for (int x = 0; x < S::kPieces; ++x) {
+          for (int x = 0; x < S::kParts; ++x) {
             typename W::V v;
-            v.load(w, v_tile + kt0 * kSub * D, x);
+            v.load(w, v_tile + kt0 * kSub * S::kRow, x);
             v.keep(from - kt0 * kSub, to - kt0 * kSub, lane);
 #pragma unroll
             for (int md = 0; md < S::kBytes / 2; ++md) {
@@ -700,18 +924,20 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
               v.fragment(a, md);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                W::weigh(y, a, pk, nt);
+                float y[4];
+                W::weigh(y, a, pk, nt, true);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (token[nt][j & 1] == t) acc[x * (S::kBytes / 2) + md][nt][j] += by * y[j];
+                  if (!apart || last[nt][j & 1] == sees) acc[x * (S::kBytes / 2) + md][nt][j] += by * y[j];
               }
             }
           }
           from = to;
         }
       }
+      leave();
     }
+    ahead -= n_tiles;
 
     // Join the key groups.
     bad_page = __any_sync(kFull, bad_page);
@@ -720,7 +946,7 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = l[nt][j];
+        float x = dead ? NAN : l[nt][j];
         x += __shfl_xor_sync(kFull, x, 4);
         x += __shfl_xor_sync(kFull, x, 8);
         x += __shfl_xor_sync(kFull, x, 16);
@@ -729,66 +955,111 @@ __global__ void __launch_bounds__(32 * P::WARPS, P::CTAS) gdn_attn_fp8_kernel(co
           s_l[warp][nt * 8 + lane * 2 + j] = x;
         }
       }
-    const bool whole = it.tile0 == 0 && it.tile1 == r.tiles;
-    const int part_slot = 2 * cta + (u == u0 ? 0 : 1);  // an item that goes on from the CTA before is the share's first
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int d0 = 0; d0 < D; d0 += kJoinCols) {
+        // a lane has kBytes neighbouring elements of every 128 (64)
+        if (kJoinCols >= S::kRow || lane / 4 * S::kBytes / kJoinCols == d0 / kJoinCols) {
+          constexpr int kMine = S::kBytes / 2;
+          const int first = kJoinCols >= S::kRow ? d0 / 16 : 0;
 #pragma unroll
-        for (int md = 0; md < kJoinCols / 16; md += 2)
+          for (int md = 0; md < kMine; md += 2)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float (&a)[4] = acc[d0 / 16 + md][nt], (&b)[4] = acc[d0 / 16 + md + 1][nt];
-            *reinterpret_cast<float4 *>(join + (warp * 8 + (lane & 3) * 2 + j) * kJoinRow + lane / 4 * S::kBytes + md * 2) =
-                make_float4(a[j], a[2 + j], b[j], b[2 + j]);
-          }
-        __syncthreads();
-        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{&r, rows, head, block, whole, part_slot}, join, s_m, s_l, s_bad, nt, d0);
-        __syncthreads();
+            for (int j = 0; j < 2; ++j) {
+              const float (&a)[4] = acc[first + md][nt], (&b)[4] = acc[first + md + 1][nt];
+              *reinterpret_cast<float4 *>(join + (warp * 8 + (lane & 3) * 2 + j) * kJoinRow + lane / 4 * S::kBytes % kJoinCols + md * 2) =
+                  make_float4(a[j], a[2 + j], b[j], b[2 + j]);
+            }
+        }
+        meet();
+        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{job.t0, job.tokens, job.len, job.rows, job.head, job.block, job.slot < 0, job.slot}, join, s_m,
+                                                 s_l, s_bad, nt, d0);
+        meet();
       }
     }
-    if (!whole && it.tile0 == 0 && tid == 0) {
-      const long long end = u + it.units + (r.tiles - it.tile1) - 1;  // the item's last unit
-      c.splits[cta] = Split{part_slot, static_cast<int>(((end + 1) * ctas - 1) / total), block * kRows, rows, r.t0,
-                            head * static_cast<int>(c.group), r.len - r.tokens};
+    if (job.last >= 0 && tid == 0)
+      c.splits[sh.cta] = Split{job.slot, job.last, job.block * kRows, job.rows, job.t0, job.head * static_cast<int>(c.group), before};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.job_empty + slot * 8);
+    if (++slot == P::slots) {
+      slot = 0;
+      job_phase ^= 1;
     }
-    it.pass(u);
-    more = it.find(c, u, u1);
-    if (more) begin_q();
   }
-  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ host
 
+// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Whether the cache's pages go by tensor copies: they hold whole groups of 8 keys, and the strides are not too long for them.
+bool takes_boxes(const gdn_attn_params &p) {
+  const int64_t most = int64_t{1} << 40;
+  return p.page_size % 8 == 0 && p.cache_page_stride < most && p.cache_head_stride < most && p.cache_slot_stride < most &&
+         tensor_map_encoder() != nullptr;
+}
+
+// A cache as [head_dim, page_size, n_kv_heads, n_pages] with boxes of `rows` rows of 128 elements (or 64) within a page.
+cudaError_t cache_map(CUtensorMap *map, const void *cache, const gdn_attn_params &p, uint32_t rows) {
+  const cuuint64_t dims[4] = {p.head_dim, p.page_size, p.n_kv_heads, p.n_pages};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.cache_slot_stride), static_cast<cuuint64_t>(p.cache_head_stride),
+                                 static_cast<cuuint64_t>(p.cache_page_stride)};
+  const cuuint32_t box[4] = {p.head_dim < 128 ? p.head_dim : 128, rows, 1, 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r = tensor_map_encoder()(
+      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(cache), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      p.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Calls f with the variant of the call: the fewest rows per block that hold the rows of its requests.
 template <typename F>
-auto dispatch(const gdn_attn_params &p, F f) {
+auto dispatch(const gdn_attn_params &p, bool boxed, F f) {
   const uint64_t rows = rows_of(p);
   auto by_dim = [&](auto t) {
     using T = decltype(t);
     if (p.head_dim == 64)
-      return rows <= 8 ? f(Pick8<T, 64, 1, 1, 4, 2, 3, 24>{}) : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 3, 24>{}) : f(Pick8<T, 64, 2, 2, 4, 2, 3, 24>{});
+      return !boxed       ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, false>{})
+             : rows <= 8  ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, true>{})
+             : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 2, 2, true>{})
+                          : f(Pick8<T, 64, 2, 2, 6, 2, 2, 1, true>{});
     if (p.head_dim == 128)
-      return rows <= 8    ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 20>{})
-             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 4, 2, 2, 20>{})
-                          : f(Pick8<T, 128, 2, 2, 4, 2, 2, 20>{});
-    return rows <= 8    ? f(Pick8<T, 256, 1, 1, 4, 1, 2, 20>{})
-           : rows <= 16 ? f(Pick8<T, 256, 1, 2, 8, 1, 1, 24>{})
-                        : f(Pick8<T, 256, 1, 4, 8, 2, 1, 16>{});
+      return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false>{})
+             : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true>{})
+             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 3, 1, 2, 2, true>{})
+                          : f(Pick8<T, 128, 2, 2, 6, 2, 2, 1, true>{});
+    return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false>{})
+           : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true>{})
+           : rows <= 16 ? f(Pick8<T, 256, 1, 2, 6, 2, 1, 1, true>{})
+                        : f(Pick8<T, 256, 1, 4, 8, 2, 1, 1, true>{});
   };
   return p.dtype == GDN_DTYPE_BF16 ? by_dim(__nv_bfloat16{}) : by_dim(float{});
 }
 
 }  // namespace
 
+// For either way of feeding: a call's pages and strides do not matter.
 size_t attn_fp8_workspace_bytes(const gdn_attn_params &p) {
-  return dispatch(p, [&](auto pick) {
+  auto bytes = [](auto pick) {
     using P = decltype(pick);
     return part_floats(P::ctas, P::rows, P::D) * 4 + static_cast<size_t>(2) * P::ctas * P::rows * sizeof(float2) +
            P::ctas * sizeof(Split);
-  });
+  };
+  const size_t boxed = dispatch(p, true, bytes), rows = dispatch(p, false, bytes);
+  return boxed > rows ? boxed : rows;
 }
 
 cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream) {
@@ -796,10 +1067,18 @@ cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream) {
   Call c = call_of(p, a.q, a.k_cache, a.v_cache, a.block_table, a.kv_lens, a.token_start, a.output);
   c.k_scale = a.k_scale;
   c.v_scale = a.v_scale;
-  return dispatch(p, [&](auto pick) {
+  c.q_wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && p.q_stride % (p.dtype == GDN_DTYPE_BF16 ? 8 : 4) == 0;
+  return dispatch(p, takes_boxes(p), [&](auto pick) {
     using P = decltype(pick);
     using T = typename P::T;
-    c.whole_tiles = p.page_size % kSub == 0;
+    // boxes of 32, 16 or 8 rows, as divide a page
+    CUtensorMap k_map = {}, v_map = {};
+    if constexpr (P::BOXED) {
+      c.box = p.page_size % 16 ? 8 : p.page_size % 32 || P::S::kTile == 16 ? 16 : 32;
+      cudaError_t e = cache_map(&k_map, a.k_cache, p, c.box);
+      if (e == cudaSuccess) e = cache_map(&v_map, a.v_cache, p, c.box);
+      if (e != cudaSuccess) return e;
+    }
     const uint64_t seen = static_cast<uint64_t>(p.window) + p.n_tokens;  // keys a window of tokens sees at most
     const uint64_t keys = static_cast<uint64_t>(p.max_pages) * p.page_size;
     c.whole_items = (p.window && seen < keys ? seen : keys) <= 256;
@@ -809,7 +1088,7 @@ cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream) {
     const auto main = gdn_attn_fp8_kernel<P>;
     cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem);
     if (e != cudaSuccess) return e;
-    e = launch_in_order(main, dim3(P::ctas), 32 * P::WARPS, P::smem, stream, c);
+    e = launch_in_order(main, dim3(P::ctas), P::threads, P::smem, stream, c, k_map, v_map);
     if (e != cudaSuccess || c.whole_items) return e;
     return launch_join<T, P::D, P::rows>(c, P::ctas, static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas, stream);
   });

@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
           for (int j = 0; j < 4; ++j)
             join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
         __syncthreads();
-        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{&r, rows, head, block, whole, part_slot}, join, s_m, s_l, s_bad, nt, d0);
+        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{r.t0, r.tokens, r.len, rows, head, block, whole, part_slot}, join, s_m, s_l, s_bad, nt, d0);
         __syncthreads();
       }
     }

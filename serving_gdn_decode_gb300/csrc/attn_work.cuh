@@ -71,6 +71,9 @@ struct Call {
   bool whole_tiles;  // pages hold whole tiles
   bool whole_items;  // no item is split
   bool out_wide;     // output rows are aligned to four elements
+  // of an 8-bit cache's call:
+  bool q_wide;       // rows of q are aligned to 16 bytes
+  uint32_t box;      // rows of a box of tensor copies
 };
 
 // A request's share of the work.
@@ -277,7 +280,7 @@ __device__ __forceinline__ Share take_share(const Call &c, long long (&scan)[WAR
 
 // What the end of an item needs to know of it.
 struct End {
-  const Request *r;
+  int t0, tokens, len;  // its request's rows of q, and keys
   int rows, head, block;
   bool whole;  // it lies in this CTA: to the output; else to part slot `slot` of the workspace
   int slot;
@@ -290,7 +293,6 @@ __device__ __forceinline__ void put_rows(const Call &c, const End &end, const fl
                                          const float (&s_l)[WARPS][NT * 8], const int (&s_bad)[WARPS], int nt, int d0) {
   constexpr int KW = WARPS / RW, kThreads = 32 * WARPS, kRows = RW * NT * 8, kJoinRow = COLS + 4;
   const int tid = threadIdx.x;
-  const Request &r = *end.r;
   bool poison = false;  // rows over a page that does not exist are NaN
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) poison |= s_bad[i] != 0;
@@ -320,8 +322,8 @@ __device__ __forceinline__ void put_rows(const Call &c, const End &end, const fl
       const float inv = 1.0f / den;
       const int t = c.group_div.div(item_row);
       // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
-      const bool empty = r.len - r.tokens + t < 0 && !poison;
-      T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
+      const bool empty = end.len - end.tokens + t < 0 && !poison;
+      T *o = static_cast<T *>(c.out) + static_cast<int64_t>(end.t0 + t) * c.out_stride +
              (static_cast<int64_t>(end.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d0 + d;
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = empty ? 0.0f : sum[e] * inv;
