@@ -37,6 +37,12 @@
 #include <numeric>
 #include <type_traits>
 
+namespace gdn {
+namespace {
+constexpr int kItemUnits = 4;  // what an item's begin and end cost beside its keys, in units
+}
+}  // namespace gdn
+
 #include "attn_work.cuh"
 #include "fp8_common.cuh"
 
@@ -92,6 +98,12 @@ __device__ __forceinline__ void mbar_arrive(unsigned bar) {
 // Arrives once this thread's copies so far are done.
 __device__ __forceinline__ void mbar_arrive_after_copies(unsigned bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// True for one lane of the warp.
+__device__ __forceinline__ bool elected() {
+  unsigned one;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 // Whether the phase ended within about a second of clock.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase) {
@@ -478,7 +490,7 @@ template <typename P>
 __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_map, const CUtensorMap *v_map, const Share &sh, uint32_t seq,
                                            long long in_seq, const Ring &ring) {
   using S = typename P::S;
-  constexpr int kTile = S::kTile;
+  constexpr int kTile = S::kTile, kMost = kTile / 8;  // boxes of a tile
   Feed<P> d(c, ring);
   const int lane = d.lane, box = c.box, per_tile = kTile / box, batch = 32 * box;
   typename Feed<P>::Part f;
@@ -500,12 +512,14 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
     return;
   }
   int page = page_of(f, f.k0 + lane * box), page1 = page_of(f, f.k0 + batch + lane * box);
-  float ks = scale_of(c.k_scale, page, f.item / f.r.blocks), vs = scale_of(c.v_scale, page, f.item / f.r.blocks);
+  float ks = 0.0f, vs = 0.0f;
   while (more) {
     typename Feed<P>::Part g = f;
     int g_page = -1, g_page1 = -1;
     const int head = f.item / f.r.blocks;
     if (!d.put_job(sh, f, head, u)) return;
+    ks = scale_of(c.k_scale, page, head);
+    vs = scale_of(c.v_scale, page, head);
     bool looked = false;
     auto look_ahead = [&] {
       looked = true;
@@ -528,9 +542,29 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
       for (int x = d.skip * per_tile; x < 32 && b0 + x * box < f.k1; x += P::FEED * per_tile) {
         const unsigned of_tile = ((2u << (per_tile - 1)) - 1) << x;
         const unsigned full = ring.full + d.stage * 8, to = ring.stages + d.stage * S::kStage;
+        int pg[kMost], row[kMost];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          pg[i] = __shfl_sync(kFull, page, x + i);
+          row[i] = __shfl_sync(kFull, at, x + i);
+        }
         if (!mbar_wait(ring.empty + d.stage * 8, d.phase)) {
           d.give_up();
           return;
+        }
+        if (lane == 0) mbar_expect(full, __popc(valid & of_tile) * box * 2 * P::D);
+        // boxes past the item's end, or of no page, are left as they are and cut out later
+        if (elected()) {
+#pragma unroll
+          for (int i = 0; i < kMost; ++i)
+            if (valid & of_tile & 1u << (x + i & 31)) {
+              const unsigned dst = to + i * box * S::kRow;
+#pragma unroll
+              for (int e = 0; e < S::kParts; ++e) {
+                copy_box(dst + e * S::kPart, k_map, e * 128, row[i], head, pg[i], full);
+                copy_box(dst + S::kCodes + e * S::kPart, v_map, e * 128, row[i], head, pg[i], full);
+              }
+            }
         }
         {  // lane i has the scales of the tile's group i of 8 keys
           const int i = x + (lane & (P::groups - 1)) * 8 / box;
@@ -540,22 +574,9 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
             asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst), "f"(of_k) : "memory");
             asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst + P::groups * 4), "f"(of_v) : "memory");
           }
-        }
-        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(ring.missing + d.stage * 4), "r"(gone & of_tile) : "memory");
-        __syncwarp();
-        if (lane == 0) mbar_expect(full, __popc(valid & of_tile) * box * 2 * P::D);
-        // boxes past the item's end, or of no page, are left as they are and cut out later
-#pragma unroll 1
-        for (unsigned left = valid & of_tile; left; left &= left - 1) {
-          const int i = __ffs(left) - 1, pg = __shfl_sync(kFull, page, i), row = __shfl_sync(kFull, at, i);
-          const unsigned dst = to + (i - x) * box * S::kRow;
-          if (lane == 0) {
-#pragma unroll
-            for (int e = 0; e < S::kParts; ++e) {
-              copy_box(dst + e * S::kPart, k_map, e * 128, row, head, pg, full);
-              copy_box(dst + S::kCodes + e * S::kPart, v_map, e * 128, row, head, pg, full);
-            }
-          }
+          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(ring.missing + d.stage * 4), "r"(gone & of_tile) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
         }
         d.next_stage();
         if (!looked) look_ahead();
@@ -570,10 +591,6 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
     f = g;
     page = g_page;
     page1 = g_page1;
-    if (more) {
-      ks = scale_of(c.k_scale, page, f.item / f.r.blocks);
-      vs = scale_of(c.v_scale, page, f.item / f.r.blocks);
-    }
   }
   d.put_end();
 }
@@ -665,7 +682,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + join_bytes<D, WARPS>(),
                   smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(&s_met), s_jobs};
   if (tid < P::STAGES) {
-    mbar_init(ring.full + tid * 8, P::BOXED ? 1 : 33);  // what the feeding warp stores, and its lanes' copies
+    mbar_init(ring.full + tid * 8, P::BOXED ? 2 : 33);  // what the feeding warp stores, and its copies
     mbar_init(ring.empty + tid * 8, RW);
   }
   if (tid < P::slots) {

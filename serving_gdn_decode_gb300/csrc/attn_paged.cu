@@ -56,6 +56,12 @@
 #include <cmath>
 #include <type_traits>
 
+namespace gdn {
+namespace {
+constexpr int kItemUnits = 2;  // what an item's begin and end cost beside its keys, in units
+}
+}  // namespace gdn
+
 #include "attn_work.cuh"
 
 namespace gdn {

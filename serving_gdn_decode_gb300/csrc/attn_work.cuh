@@ -2,8 +2,8 @@
 // the call as the kernels see it, how its work is split over the CTAs, and the
 // join of an item's parts.
 //
-// The work of a call is a list of units: 64 keys, and two units for an item's
-// begin and end (an item is a request's key head and block of rows).  The lengths
+// The work of a call is a list of units: 64 keys, and kItemUnits, which the file
+// that includes this one defines, for an item's begin and end (an item is a request's key head and block of rows).  The lengths
 // are on the device, so every CTA takes the prefix sum of the requests' units and
 // then the same share of the whole list.  A share may begin and end inside an item:
 // such ends leave unnormalised sums with their running maximum in the workspace
@@ -23,7 +23,6 @@ namespace {
 constexpr int kSub = 16;   // keys of a matrix tile
 constexpr int kUnit = 64;  // keys per unit of work
 constexpr int kMostTile = 32;  // largest tile of a key group
-constexpr int kItemUnits = 2;  // what an item's begin and end cost beside its keys, in units
 constexpr int kSms = 152;
 constexpr int kJoinWarps = 8;
 
