@@ -325,16 +325,6 @@ struct Warp8 {
   }
 };
 
-// The join of a CTA's warps goes through shared memory in pieces of 8 rows x join_cols.
-template <int D>
-constexpr int join_cols() {
-  return D < 256 ? 64 : 128;
-}
-template <int D, int WARPS>
-constexpr int join_bytes() {
-  return WARPS * 8 * (join_cols<D>() + 4) * 4;
-}
-
 // A variant: NT 8-row tiles of a warp, RW warps that share their tiles, each with rows of its own, WARPS of a CTA beside
 // the FEED that feed them, KT matrix tiles of 16 keys in a step, CTAS on an SM.  BOXED: pages hold whole groups of 8 keys.
 template <typename T_, int D_, int NT_, int RW_, int WARPS_, int FEED_, int KT_, int CTAS_, bool BOXED_>
@@ -348,7 +338,8 @@ struct Pick8 {
   static constexpr int q_row = D * static_cast<int>(sizeof(T)) + 16, q_bytes = rows * q_row, slots = q_bytes <= 2400 ? 4 : q_bytes <= 4800 ? 3 : 2;
   // beside a stage: the scales of its groups of 8 keys (of its keys), and of their values
   static constexpr int groups = BOXED ? KT * 2 : S::kTile, scales = 2 * groups * 4;
-  static constexpr int fixed = join_bytes<D, WARPS>() + slots * q_bytes;
+  static constexpr int join_row = D + 4, join_bytes = WARPS * NT * 8 * join_row * 4;  // the sums of every warp at a job's end
+  static constexpr int fixed = join_bytes + slots * q_bytes;
   // the ring has what the SM's shared memory holds beside that and the static part
   static constexpr int fit = (228 * 1024 / CTAS - 1024 - 1024 - 512 - 64 * WARPS * NT - 24 * 32 - fixed) / (S::kStage + scales);
   // A stage is always filled by the same warp and emptied by the same group: waits tell two phases of a barrier apart, and
@@ -371,7 +362,7 @@ struct Job {
 // What the feeding warps and the others share beside the ring: shared-memory addresses.
 struct Ring {
   unsigned stages, scales, q, missing;
-  unsigned full, empty, job_full, job_empty, met;  // of barriers: of a stage, of a job's slot, of the CTA's key groups
+  unsigned full, empty, job_full, job_empty, joined;  // of barriers: of a stage, of a job's slot, of a row group's join
   Job *jobs;
 };
 
@@ -664,23 +655,22 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   using S = Shape8<D, KT>;
   using W = Warp8<T, D, NT, KT>;
   constexpr int kTile = S::kTile;
-  constexpr int kJoinCols = join_cols<D>(), kJoinRow = kJoinCols + 4;
   constexpr int kRows = P::rows;       // rows of a block
   constexpr int KW = WARPS / RW;       // key groups: group g takes every KW-th tile of the share
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[WARPS + P::FEED], s_offset;
   __shared__ uint32_t s_seq;
   __shared__ float s_m[WARPS][NT * 8], s_l[WARPS][NT * 8];
-  __shared__ int s_bad[WARPS];
+  __shared__ int s_bad[WARPS], s_done[RW];  // s_done: key groups that have left their sums
   __shared__ unsigned s_missing[P::STAGES];
-  __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_met;
+  __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_joined[RW];
   __shared__ Job s_jobs[P::slots];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned start = (1024u - (smem_u32(smem) & 1023u)) & 1023u;
   float *join = reinterpret_cast<float *>(smem + start + P::STAGES * (S::kStage + P::scales));
-  const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + join_bytes<D, WARPS>(),
-                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(&s_met), s_jobs};
+  const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + P::join_bytes,
+                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_joined), s_jobs};
   if (tid < P::STAGES) {
     mbar_init(ring.full + tid * 8, P::BOXED ? 2 : 33);  // what the feeding warp stores, and its copies
     mbar_init(ring.empty + tid * 8, RW);
@@ -689,7 +679,10 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     mbar_init(ring.job_full + tid * 8, 33);
     mbar_init(ring.job_empty + tid * 8, WARPS);
   }
-  if (tid == 0) mbar_init(ring.met, WARPS);
+  if (tid < RW) {
+    mbar_init(ring.joined + tid * 8, 1);
+    s_done[tid] = 0;
+  }
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   begin_in_order();
@@ -704,19 +697,13 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   W w(lane);
   int slot = 0, stage = kg;
   int ahead = kg;  // tiles until this group's next one, from the job's first
-  unsigned phase = 0, job_phase = 0, met_phase = 0;
+  unsigned phase = 0, job_phase = 0, joined_phase = 1;
   bool dead = false;  // a wait ran out: the job at hand is the last
   auto wait = [&](unsigned bar, unsigned of) {
     if (!dead && !mbar_wait(bar, of)) {
       dead = true;
       report(GDN_DEVICE_WAIT_TIMEOUT);
     }
-  };
-  auto meet = [&] {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(ring.met);
-    wait(ring.met, met_phase);
-    met_phase ^= 1;
   };
   while (true) {
     wait(ring.job_full + slot * 8, job_phase);
@@ -956,11 +943,14 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     }
     ahead -= n_tiles;
 
-    // Join the key groups.
+    // Every key group leaves its sums; the last one of a row group joins them, while the others go on with the next job.
+    wait(ring.joined + rg * 8, joined_phase);  // those of the job before have been read
+    joined_phase ^= 1;
     bad_page = __any_sync(kFull, bad_page);
     if (lane == 0) s_bad[warp] = bad_page;
+    float *const mine = join + warp * NT * 8 * P::join_row;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float x = dead ? NAN : l[nt][j];
@@ -971,32 +961,67 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
           s_m[warp][nt * 8 + lane * 2 + j] = m[nt][j];
           s_l[warp][nt * 8 + lane * 2 + j] = x;
         }
-      }
+        // this lane has kBytes neighbouring elements of every 128 (64)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int d0 = 0; d0 < D; d0 += kJoinCols) {
-        // a lane has kBytes neighbouring elements of every 128 (64)
-        if (kJoinCols >= S::kRow || lane / 4 * S::kBytes / kJoinCols == d0 / kJoinCols) {
-          constexpr int kMine = S::kBytes / 2;
-          const int first = kJoinCols >= S::kRow ? d0 / 16 : 0;
-#pragma unroll
-          for (int md = 0; md < kMine; md += 2)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float (&a)[4] = acc[first + md][nt], (&b)[4] = acc[first + md + 1][nt];
-              *reinterpret_cast<float4 *>(join + (warp * 8 + (lane & 3) * 2 + j) * kJoinRow + lane / 4 * S::kBytes % kJoinCols + md * 2) =
-                  make_float4(a[j], a[2 + j], b[j], b[2 + j]);
-            }
+        for (int md = 0; md < D / 16; md += 2) {
+          const float (&a)[4] = acc[md][nt], (&b)[4] = acc[md + 1][nt];
+          *reinterpret_cast<float4 *>(mine + (nt * 8 + (lane & 3) * 2 + j) * P::join_row + md / (S::kBytes / 2) * 128 + lane / 4 * S::kBytes +
+                                      md % (S::kBytes / 2) * 2) = make_float4(a[j], a[2 + j], b[j], b[2 + j]);
         }
-        meet();
-        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{job.t0, job.tokens, job.len, job.rows, job.head, job.block, job.slot < 0, job.slot}, join, s_m,
-                                                 s_l, s_bad, nt, d0);
-        meet();
       }
     }
-    if (job.last >= 0 && tid == 0)
-      c.splits[sh.cta] = Split{job.slot, job.last, job.block * kRows, job.rows, job.t0, job.head * static_cast<int>(c.group), before};
+    __threadfence_block();
+    __syncwarp();
+    int done = 0;
+    if (lane == 0) done = atomicAdd(&s_done[rg], 1);
+    if (__shfl_sync(kFull, done, 0) == KW - 1) {
+      __threadfence_block();
+      bool poison = false;  // rows over a page that does not exist are NaN
+#pragma unroll
+      for (int i = 0; i < KW; ++i) poison |= s_bad[i * RW + rg] != 0;
+      if (poison && lane == 0) report(GDN_DEVICE_BAD_PAGE);
+#pragma unroll 1
+      for (int x = lane; x < NT * 8 * D / 4; x += 32) {
+        const int n = x / (D / 4), d = x % (D / 4) * 4, item_row = first_row + n;
+        if (item_row >= job.rows) break;
+        float top = s_m[rg][n];
+#pragma unroll
+        for (int i = 1; i < KW; ++i) top = fmaxf(top, s_m[i * RW + rg][n]);
+        float sum[4] = {}, den = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const float g = exp2_fast(s_m[i * RW + rg][n] - top);
+          const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + rg) * NT * 8 + n) * P::join_row + d);
+          sum[0] += g * y.x;
+          sum[1] += g * y.y;
+          sum[2] += g * y.z;
+          sum[3] += g * y.w;
+          den += g * s_l[i * RW + rg][n];
+        }
+        if (poison) den = NAN;
+        if (job.slot < 0) {
+          const float inv = 1.0f / den;
+          const int t = c.group_div.div(item_row);
+          const bool none = before + t < 0 && !poison;  // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
+          T *o = static_cast<T *>(c.out) + static_cast<int64_t>(job.t0 + t) * c.out_stride +
+                 (static_cast<int64_t>(job.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = none ? 0.0f : sum[e] * inv;
+          put4(o, sum, c.out_wide);
+        } else {
+          const size_t at = static_cast<size_t>(job.slot) * kRows + row0 + n;
+          *reinterpret_cast<float4 *>(c.part + at * D + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+          if (d == 0) c.part_ml[at] = make_float2(top, den);
+        }
+      }
+      if (job.last >= 0 && rg == 0 && lane == 0)
+        c.splits[sh.cta] = Split{job.slot, job.last, job.block * kRows, job.rows, job.t0, job.head * static_cast<int>(c.group), before};
+      __syncwarp();
+      if (lane == 0) {
+        s_done[rg] = 0;
+        mbar_arrive(ring.joined + rg * 8);
+      }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(ring.job_empty + slot * 8);
     if (++slot == P::slots) {

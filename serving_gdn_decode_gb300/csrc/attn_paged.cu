@@ -818,7 +818,47 @@ __global__ void __launch_bounds__(32 * WARPS, (ctas_per_sm<T, D, NT, RW, WARPS, 
           for (int j = 0; j < 4; ++j)
             join[(warp * 8 + (lane & 3) * 2 + (j & 1)) * kJoinRow + md * 16 + lane / 4 + (j >> 1) * 8] = acc[d0 / 16 + md][nt][j];
         __syncthreads();
-        put_rows<T, D, NT, RW, WARPS, kJoinCols>(c, End{r.t0, r.tokens, r.len, rows, head, block, whole, part_slot}, join, s_m, s_l, s_bad, nt, d0);
+        bool poison = false;  // rows over a page that does not exist are NaN
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) poison |= s_bad[i] != 0;
+        if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
+#pragma unroll 1
+        for (int x = tid; x < RW * 8 * kJoinCols / 4; x += kThreads) {
+          const int row = x / (kJoinCols / 4), d = x % (kJoinCols / 4) * 4;
+          const int of = row / 8, in = row % 8, m_row = nt * 8 + in;  // rows of warps of, of + RW, ...
+          const int n = of * NT * 8 + m_row, item_row = block * kRows + n;
+          if (item_row >= rows) break;
+          float top = s_m[of][m_row];
+#pragma unroll
+          for (int i = 1; i < KW; ++i) top = fmaxf(top, s_m[i * RW + of][m_row]);
+          float sum[4] = {}, den = 0.0f;
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {
+            const float g = exp2_fast(s_m[i * RW + of][m_row] - top);
+            const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + of) * 8 + in) * kJoinRow + d);
+            sum[0] += g * y.x;
+            sum[1] += g * y.y;
+            sum[2] += g * y.z;
+            sum[3] += g * y.w;
+            den += g * s_l[i * RW + of][m_row];
+          }
+          if (poison) den = NAN;
+          if (whole) {
+            const float inv = 1.0f / den;
+            const int t = c.group_div.div(item_row);
+            // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
+            const bool empty = r.len - r.tokens + t < 0 && !poison;
+            T *o = static_cast<T *>(c.out) + static_cast<int64_t>(r.t0 + t) * c.out_stride +
+                   (static_cast<int64_t>(head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d0 + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = empty ? 0.0f : sum[e] * inv;
+            put4(o, sum, c.out_wide);
+          } else {
+            const size_t at = static_cast<size_t>(part_slot) * kRows + n;
+            *reinterpret_cast<float4 *>(c.part + at * D + d0 + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            if (d0 + d == 0) c.part_ml[at] = make_float2(top, den);
+          }
+        }
         __syncthreads();
       }
     }

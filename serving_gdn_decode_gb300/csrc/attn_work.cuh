@@ -277,64 +277,6 @@ __device__ __forceinline__ Share take_share(const Call &c, long long (&scan)[WAR
   return sh;
 }
 
-// What the end of an item needs to know of it.
-struct End {
-  int t0, tokens, len;  // its request's rows of q, and keys
-  int rows, head, block;
-  bool whole;  // it lies in this CTA: to the output; else to part slot `slot` of the workspace
-  int slot;
-};
-
-// The CTA's key groups joined, for rows nt * 8 .. + 8 of each of the RW row groups and COLS elements from d0: join has
-// 8 rows of COLS + 4 sums per warp, m and l their maximum and sum.  Every thread of the CTA takes part.
-template <typename T, int D, int NT, int RW, int WARPS, int COLS>
-__device__ __forceinline__ void put_rows(const Call &c, const End &end, const float *join, const float (&s_m)[WARPS][NT * 8],
-                                         const float (&s_l)[WARPS][NT * 8], const int (&s_bad)[WARPS], int nt, int d0) {
-  constexpr int KW = WARPS / RW, kThreads = 32 * WARPS, kRows = RW * NT * 8, kJoinRow = COLS + 4;
-  const int tid = threadIdx.x;
-  bool poison = false;  // rows over a page that does not exist are NaN
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) poison |= s_bad[i] != 0;
-  if (poison && tid == 0) report(GDN_DEVICE_BAD_PAGE);
-#pragma unroll 1
-  for (int x = tid; x < RW * 8 * COLS / 4; x += kThreads) {
-    const int row = x / (COLS / 4), d = x % (COLS / 4) * 4;
-    const int of = row / 8, in = row % 8, m_row = nt * 8 + in;  // rows of warps of, of + RW, ...
-    const int n = of * NT * 8 + m_row, item_row = end.block * kRows + n;
-    if (item_row >= end.rows) break;
-    float top = s_m[of][m_row];
-#pragma unroll
-    for (int i = 1; i < KW; ++i) top = fmaxf(top, s_m[i * RW + of][m_row]);
-    float sum[4] = {}, den = 0.0f;
-#pragma unroll
-    for (int i = 0; i < KW; ++i) {
-      const float g = exp2_fast(s_m[i * RW + of][m_row] - top);
-      const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + of) * 8 + in) * kJoinRow + d);
-      sum[0] += g * y.x;
-      sum[1] += g * y.y;
-      sum[2] += g * y.z;
-      sum[3] += g * y.w;
-      den += g * s_l[i * RW + of][m_row];
-    }
-    if (poison) den = NAN;
-    if (end.whole) {
-      const float inv = 1.0f / den;
-      const int t = c.group_div.div(item_row);
-      // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
-      const bool empty = end.len - end.tokens + t < 0 && !poison;
-      T *o = static_cast<T *>(c.out) + static_cast<int64_t>(end.t0 + t) * c.out_stride +
-             (static_cast<int64_t>(end.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d0 + d;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = empty ? 0.0f : sum[e] * inv;
-      put4(o, sum, c.out_wide);
-    } else {
-      const size_t at = static_cast<size_t>(end.slot) * kRows + n;
-      *reinterpret_cast<float4 *>(c.part + at * D + d0 + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      if (d0 + d == 0) c.part_ml[at] = make_float2(top, den);
-    }
-  }
-}
-
 // ------------------------------------------------------------ the join
 
 // The item that begins in main CTA blockIdx.x and goes on in later ones: CTA (x, y)
