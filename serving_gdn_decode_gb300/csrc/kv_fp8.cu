@@ -17,6 +17,8 @@
 // takes a unit and keeps its rows in registers between the maximum and the codes.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fp8_common.cuh"
 #include "paged_common.cuh"
 #include "paged_internal.h"
@@ -35,6 +37,18 @@ template <>
 struct Row16<float> {
   static constexpr int kElems = 4;
   float4 x;
+  static constexpr unsigned kInf = 0x7f800000u;
+  // the largest magnitude, as bits, so far; of the finite ones only, with FINITE
+  template <bool FINITE>
+  __device__ __forceinline__ void raise(unsigned &m) const {
+    const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned b = __float_as_uint(f[i]) & 0x7fffffffu;
+      m = max(m, FINITE && b >= kInf ? 0u : b);
+    }
+  }
+  static __device__ __forceinline__ unsigned top(unsigned m) { return m; }  // as an f32's bits
   __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w; }
   __device__ __forceinline__ void put(const float (&f)[4]) { x = make_float4(f[0], f[1], f[2], f[3]); }
 };
@@ -42,6 +56,17 @@ template <>
 struct Row16<__nv_bfloat16> {
   static constexpr int kElems = 8;
   uint4 x;
+  template <bool FINITE>
+  __device__ __forceinline__ void raise(unsigned &m) const {
+    const unsigned w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unsigned b = w[i] & 0x7fff7fffu;
+      if (FINITE) b &= ~__vcmpgeu2(b, 0x7f807f80u);
+      m = __vmaxu2(m, b);
+    }
+  }
+  static __device__ __forceinline__ unsigned top(unsigned m) { return max(m << 16, m & 0xffff0000u); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const unsigned w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -95,25 +120,31 @@ __device__ __forceinline__ float least_scale(float amax) {
 
 struct StoreCall {
   KvFp8Args a;
-  FastDiv page_div, row_div;  // by the page size; by the vectors of a row
-  uint32_t row_vecs;
+  FastDiv page_div, rows_div;  // by the page size; by a token's rows of k and v
+  uint32_t row_vecs;           // vectors of a row
   uint32_t window;   // tokens whose runs' beginnings a team looks for
   uint32_t windows;
   bool wide;         // rows of k and v are aligned to 16 bytes
 };
 
 template <typename T, int W>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) gdn_kv_store_kernel(const __grid_constant__ StoreCall c) {
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 4 : W > 2 ? 8 : 6) gdn_kv_store_kernel(const __grid_constant__ StoreCall c) {
   constexpr int E = Row16<T>::kElems, kTeams = W > 4 ? 1 : 4 / W;  // of a CTA
-  __shared__ float s_top[kTeams][W];
+  __shared__ unsigned s_top[kTeams][W];
   const gdn_kv_fp8_params &p = c.a.p;
   const int lane = threadIdx.x & 31, team = threadIdx.x / (32 * W), me = threadIdx.x % (32 * W);
   auto meet = [&] {
     if constexpr (W == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + team), "n"(32 * W) : "memory");
   };
+  // A thread keeps its place in a row, and goes through the rows of a run `at_once` apart.
+  const int at_once = 32 * W / static_cast<int>(c.row_vecs), my_row = me / static_cast<int>(c.row_vecs),
+            my_col = (me - my_row * static_cast<int>(c.row_vecs)) * E;
+  const bool active = my_row < at_once;
   begin_in_order();
-  const uint32_t unit = blockIdx.x * kTeams + team, which = blockIdx.y & 1, head = blockIdx.y >> 1;
+  // neighbouring CTAs have the heads of the same tokens, whose rows lie side by side
+  const uint32_t group = c.rows_div.div(blockIdx.x), of = blockIdx.x - group * c.rows_div.d;
+  const uint32_t unit = group * kTeams + team, which = of & 1, head = of >> 1;
   if (unit >= c.windows) return;  // the whole team
   const int n = static_cast<int>(p.n_tokens), t0 = unit * c.window, t1 = min(n, t0 + static_cast<int>(c.window));
   const T *src = static_cast<const T *>(which ? c.a.v : c.a.k) + head * p.head_dim;
@@ -123,11 +154,12 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) gdn_kv_store_kernel(cons
   const int32_t *slots = c.a.slot_map;
 
   for (int base = t0; base < t1; base += 32) {
-    // the tokens at which runs begin
+    // the tokens at which runs begin; slots of this and the next 32 tokens at once: a run's length is in them, or its end is not
     const int i = base + lane;
+    const int slot_i = i < n ? slots[i] : -1, slot_on = i + 32 < n ? slots[i + 32] : -1;
     bool begins = false;
     if (i < t1) {
-      const int slot = slots[i], before = i ? slots[i - 1] : -1;
+      const int slot = slot_i, before = i ? slots[i - 1] : -1;
       if (slot >= 0) {
         const uint32_t page = c.page_div.div(slot);
         const bool same = before >= 0 && c.page_div.div(before) == page;
@@ -142,54 +174,53 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) gdn_kv_store_kernel(cons
       }
     }
     for (unsigned left = __ballot_sync(kFull, begins); left; left &= left - 1) {
-      const int first = base + __ffs(left) - 1;
-      const int slot = slots[first];
+      const int from = __ffs(left) - 1, first = base + from;
+      const int slot = __shfl_sync(kFull, slot_i, from);
       const uint32_t page = c.page_div.div(slot);
       const int place = slot - static_cast<int>(page * p.page_size), most = static_cast<int>(p.page_size) - place;
-      int len = 1;  // tokens of the run
-      for (bool go = true; go && len < most;) {
+      // tokens of the run: up to the first that does not follow
+      const unsigned ends = __ballot_sync(kFull, lane >= from && (slot_i != slot + lane - from || lane - from >= most));
+      const unsigned ends_on = __ballot_sync(kFull, slot_on != slot + lane + 32 - from || lane + 32 - from >= most);
+      int len = ends ? __ffs(ends) - 1 - from : ends_on ? __ffs(ends_on) + 31 - from : 64 - from;
+      for (bool go = !ends && !ends_on; go;) {
         const int j = len + lane;
-        const unsigned ends = __ballot_sync(kFull, j >= most || first + j >= n || slots[first + j] != slot + j);
-        len += ends ? __ffs(ends) - 1 : 32;
-        go = ends == 0;
+        const unsigned e = __ballot_sync(kFull, j >= most || first + j >= n || slots[first + j] != slot + j);
+        len += e ? __ffs(e) - 1 : 32;
+        go = e == 0;
       }
       float *scale_at = scales + static_cast<uint64_t>(page) * p.n_kv_heads;
       const float old = place ? *scale_at : 0.0f;
       uint8_t *rows = cache + page * p.cache_page_stride;
-      const int vecs = len * static_cast<int>(c.row_vecs);
-      // the largest magnitude
+      const int mine = active ? len - my_row : 0;  // rows from this thread's first on
+      const T *from_row = src + static_cast<int64_t>(first + my_row) * src_stride + my_col;
+      const int64_t step = at_once * src_stride;
+      // the largest magnitude: of all values, and where one of them is not finite, of the others
       Row16<T> keep[kKeep];
-      float top = 0.0f;
-      auto at = [&](int x) {
-        const int r = c.row_div.div(x);
-        return src + (first + r) * src_stride + (x - r * static_cast<int>(c.row_vecs)) * E;
-      };
-      auto raise = [&](const Row16<T> &v) {
-        float f[E];
-        v.get(f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float m = fabsf(f[e]);
-          top = m <= 3.402823466e38f ? fmaxf(top, m) : top;
-        }
-      };
-#pragma unroll
-      for (int u = 0; u < kKeep; ++u) {
-        const int x = u * 32 * W + me;
-        if (x < vecs) keep[u] = load_row(at(x), c.wide);
-      }
 #pragma unroll
       for (int u = 0; u < kKeep; ++u)
-        if (u * 32 * W + me < vecs) raise(keep[u]);
-      for (int x = kKeep * 32 * W + me; x < vecs; x += 32 * W) raise(load_row(at(x), c.wide));
+        if (u * at_once < mine) keep[u] = load_row(from_row + u * step, c.wide);
+      unsigned top_bits = 0;
+      auto raise = [&](auto finite) {
+        unsigned m = 0;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-      if constexpr (W > 1) {
-        if (lane == 0) s_top[team][me / 32] = top;
-        meet();
+        for (int u = 0; u < kKeep; ++u)
+          if (u * at_once < mine) keep[u].template raise<finite()>(m);
+        for (int r = kKeep * at_once; r < mine; r += at_once) load_row(from_row + r / at_once * step, c.wide).template raise<finite()>(m);
+        m = Row16<T>::top(m);
+        m = __reduce_max_sync(kFull, m);
+        if constexpr (W > 1) {
+          if (lane == 0) s_top[team][me / 32] = m;
+          meet();
 #pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, s_top[team][w]);
-      }
+          for (int w = 0; w < W; ++w) m = max(m, s_top[team][w]);
+          meet();
+        }
+        top_bits = m;
+      };
+      raise(std::false_type{});
+      const bool finite = top_bits < 0x7f800000u;
+      if (!finite) raise(std::true_type{});
+      const float top = __uint_as_float(top_bits);
       const float need = least_scale(top);
       const float scale = old > need && old <= 3.402823466e38f ? old : need, inv = 1.0f / scale;
       // the page's earlier tokens, on the new scale; those of a scale that is none (negative, infinite, NaN) are NaN
@@ -208,25 +239,27 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) gdn_kv_store_kernel(cons
           *q = y;
         }
       }
-      auto put = [&](const Row16<T> &v, int x) {
+      uint8_t *to_row = rows + static_cast<int64_t>(place + my_row) * p.cache_slot_stride + my_col;
+      const int64_t to_step = at_once * p.cache_slot_stride;
+      auto put = [&](const Row16<T> &v, uint8_t *to) {
         float f[E];
         v.get(f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = fabsf(f[e]) <= 3.402823466e38f ? f[e] * inv : __int_as_float(0x7fffffff);
-        const int r = c.row_div.div(x);
-        uint8_t *to = rows + (place + r) * p.cache_slot_stride + (x - r * static_cast<int>(c.row_vecs)) * E;
+        for (int e = 0; e < E; ++e) f[e] *= inv;
+        if (!finite) {  // (a value that is not finite is not so after the product either)
+#pragma unroll
+          for (int e = 0; e < E; ++e) f[e] = fabsf(f[e]) <= 3.402823466e38f ? f[e] : __int_as_float(0x7fffffff);
+        }
         if constexpr (E == 8)
           *reinterpret_cast<uint2 *>(to) = make_uint2(codes_of(f[0], f[1], f[2], f[3]), codes_of(f[4], f[5], f[6], f[7]));
         else
           *reinterpret_cast<unsigned *>(to) = codes_of(f[0], f[1], f[2], f[3]);
       };
 #pragma unroll
-      for (int u = 0; u < kKeep; ++u) {
-        const int x = u * 32 * W + me;
-        if (x < vecs) put(keep[u], x);
-      }
-      for (int x = kKeep * 32 * W + me; x < vecs; x += 32 * W) put(load_row(at(x), c.wide), x);
-      meet();  // s_top and the old scale have been read
+      for (int u = 0; u < kKeep; ++u)
+        if (u * at_once < mine) put(keep[u], to_row + u * to_step);
+      for (int r = kKeep * at_once; r < mine; r += at_once) put(load_row(from_row + r / at_once * step, c.wide), to_row + r / at_once * to_step);
+      meet();  // the old scale has been read
       if (me == 0) *scale_at = scale;
     }
   }
@@ -303,12 +336,14 @@ cudaError_t launch_store(StoreCall c, cudaStream_t stream) {
   const gdn_kv_fp8_params &p = c.a.p;
   constexpr uint32_t kTeams = W > 4 ? 1 : 4 / W;
   // With few tokens a team each; with many a page of them, so that hardly a team finds no run's beginning.
-  const uint64_t units = static_cast<uint64_t>(p.n_tokens) * p.n_kv_heads * 2, enough = 152 * 32 / W;
+  const uint64_t units = static_cast<uint64_t>(p.n_tokens) * p.n_kv_heads * 2, enough = 152ull * 64 / W;
   c.window = static_cast<uint32_t>(units / enough);
   if (c.window < 1) c.window = 1;
   if (c.window > p.page_size) c.window = p.page_size;
+  while (c.window < p.n_tokens && units / c.window > 1u << 30) c.window *= 2;  // CTAs are counted in 31 bits
   c.windows = (p.n_tokens + c.window - 1) / c.window;
-  return launch_in_order(gdn_kv_store_kernel<T, W>, dim3((c.windows + kTeams - 1) / kTeams, 2 * p.n_kv_heads), W > 4 ? 32 * W : 128, 0, stream, c);
+  c.rows_div = FastDiv(2 * p.n_kv_heads);
+  return launch_in_order(gdn_kv_store_kernel<T, W>, dim3((c.windows + kTeams - 1) / kTeams * 2 * p.n_kv_heads), W > 4 ? 32 * W : 128, 0, stream, c);
 }
 
 template <typename T>
@@ -318,14 +353,14 @@ cudaError_t launch_store(const KvFp8Args &a, cudaStream_t stream) {
   c.a = a;
   c.page_div = FastDiv(a.p.page_size);
   c.row_vecs = a.p.head_dim / E;
-  c.row_div = FastDiv(c.row_vecs);
   c.wide = rows_wide(a, E);
-  // warps enough for the longest run's rows to stay in registers
-  const uint64_t rows = a.p.page_size < a.p.n_tokens ? a.p.page_size : a.p.n_tokens, vecs = rows * c.row_vecs;
-  return vecs <= 32 * kKeep       ? launch_store<T, 1>(c, stream)
-         : vecs <= 2 * 32 * kKeep ? launch_store<T, 2>(c, stream)
-         : vecs <= 4 * 32 * kKeep ? launch_store<T, 4>(c, stream)
-                                  : launch_store<T, 8>(c, stream);
+  // warps enough for the longest run's rows to stay in registers (and for a row)
+  const uint64_t rows = a.p.page_size < a.p.n_tokens ? a.p.page_size : a.p.n_tokens;
+  auto holds = [&](uint64_t w) { return 32 * w / c.row_vecs * kKeep >= rows; };
+  return holds(1)   ? launch_store<T, 1>(c, stream)
+         : holds(2) ? launch_store<T, 2>(c, stream)
+         : holds(4) ? launch_store<T, 4>(c, stream)
+                    : launch_store<T, 8>(c, stream);
 }
 
 template <typename T>
