@@ -121,7 +121,8 @@ __device__ __forceinline__ float least_scale(float amax) {
 struct StoreCall {
   KvFp8Args a;
   FastDiv page_div, rows_div;  // by the page size; by a token's rows of k and v
-  uint32_t row_vecs;           // vectors of a row
+  FastDiv row_div;   // by the vectors of a row
+  uint32_t at_once;  // rows that a team's threads take at once
   uint32_t window;   // tokens whose runs' beginnings a team looks for
   uint32_t windows;
   bool wide;         // rows of k and v are aligned to 16 bytes
@@ -138,8 +139,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 4 : W > 2 ? 8 : 
     else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + team), "n"(32 * W) : "memory");
   };
   // A thread keeps its place in a row, and goes through the rows of a run `at_once` apart.
-  const int at_once = 32 * W / static_cast<int>(c.row_vecs), my_row = me / static_cast<int>(c.row_vecs),
-            my_col = (me - my_row * static_cast<int>(c.row_vecs)) * E;
+  const int at_once = c.at_once, my_row = c.row_div.div(me), my_col = (me - my_row * static_cast<int>(c.row_div.d)) * E;
   const bool active = my_row < at_once;
   begin_in_order();
   // neighbouring CTAs have the heads of the same tokens, whose rows lie side by side
@@ -343,6 +343,7 @@ cudaError_t launch_store(StoreCall c, cudaStream_t stream) {
   while (c.window < p.n_tokens && units / c.window > 1u << 30) c.window *= 2;  // CTAs are counted in 31 bits
   c.windows = (p.n_tokens + c.window - 1) / c.window;
   c.rows_div = FastDiv(2 * p.n_kv_heads);
+  c.at_once = 32 * W / c.row_div.d;
   return launch_in_order(gdn_kv_store_kernel<T, W>, dim3((c.windows + kTeams - 1) / kTeams * 2 * p.n_kv_heads), W > 4 ? 32 * W : 128, 0, stream, c);
 }
 
@@ -352,11 +353,11 @@ cudaError_t launch_store(const KvFp8Args &a, cudaStream_t stream) {
   StoreCall c;
   c.a = a;
   c.page_div = FastDiv(a.p.page_size);
-  c.row_vecs = a.p.head_dim / E;
+  c.row_div = FastDiv(a.p.head_dim / E);
   c.wide = rows_wide(a, E);
   // warps enough for the longest run's rows to stay in registers (and for a row)
   const uint64_t rows = a.p.page_size < a.p.n_tokens ? a.p.page_size : a.p.n_tokens;
-  auto holds = [&](uint64_t w) { return 32 * w / c.row_vecs * kKeep >= rows; };
+  auto holds = [&](uint64_t w) { return 32 * w / c.row_div.d * kKeep >= rows; };
   return holds(1)   ? launch_store<T, 1>(c, stream)
          : holds(2) ? launch_store<T, 2>(c, stream)
          : holds(4) ? launch_store<T, 4>(c, stream)
