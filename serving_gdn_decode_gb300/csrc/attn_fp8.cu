@@ -338,7 +338,8 @@ struct Pick8 {
   static constexpr int q_row = D * static_cast<int>(sizeof(T)) + 16, q_bytes = rows * q_row, slots = q_bytes <= 2400 ? 4 : q_bytes <= 4800 ? 3 : 2;
   // beside a stage: the scales of its groups of 8 keys (of its keys), and of their values
   static constexpr int groups = BOXED ? KT * 2 : S::kTile, scales = 2 * groups * 4;
-  static constexpr int join_row = D + 4, join_bytes = WARPS * NT * 8 * join_row * 4;  // the sums of every warp at a job's end
+  // a row group's sums at a job's end, as its warps have them in registers: those of values, of probabilities, and the maximum
+  static constexpr int join_bytes = RW * (D / 16 * 4 + 4) * NT * 128;
   static constexpr int fixed = join_bytes + slots * q_bytes;
   // the ring has what the SM's shared memory holds beside that and the static part
   static constexpr int fit = (228 * 1024 / CTAS - 1024 - 1024 - 512 - 64 * WARPS * NT - 24 * 32 - fixed) / (S::kStage + scales);
@@ -362,7 +363,7 @@ struct Job {
 // What the feeding warps and the others share beside the ring: shared-memory addresses.
 struct Ring {
   unsigned stages, scales, q, missing;
-  unsigned full, empty, job_full, job_empty, joined;  // of barriers: of a stage, of a job's slot, of a row group's join
+  unsigned full, empty, job_full, job_empty, turn;  // of barriers: of a stage, of a job's slot, of a key group's turn to join
   Job *jobs;
 };
 
@@ -660,17 +661,16 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[WARPS + P::FEED], s_offset;
   __shared__ uint32_t s_seq;
-  __shared__ float s_m[WARPS][NT * 8], s_l[WARPS][NT * 8];
-  __shared__ int s_bad[WARPS], s_done[RW];  // s_done: key groups that have left their sums
+  __shared__ unsigned s_bad[RW];
   __shared__ unsigned s_missing[P::STAGES];
-  __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_joined[RW];
+  __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_turn[WARPS];
   __shared__ Job s_jobs[P::slots];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned start = (1024u - (smem_u32(smem) & 1023u)) & 1023u;
-  float *join = reinterpret_cast<float *>(smem + start + P::STAGES * (S::kStage + P::scales));
+  float4 *join = reinterpret_cast<float4 *>(smem + start + P::STAGES * (S::kStage + P::scales));
   const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + P::join_bytes,
-                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_joined), s_jobs};
+                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_turn), s_jobs};
   if (tid < P::STAGES) {
     mbar_init(ring.full + tid * 8, P::BOXED ? 2 : 33);  // what the feeding warp stores, and its copies
     mbar_init(ring.empty + tid * 8, RW);
@@ -679,10 +679,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     mbar_init(ring.job_full + tid * 8, 33);
     mbar_init(ring.job_empty + tid * 8, WARPS);
   }
-  if (tid < RW) {
-    mbar_init(ring.joined + tid * 8, 1);
-    s_done[tid] = 0;
-  }
+  if (tid < WARPS) mbar_init(ring.turn + tid * 8, 1);
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   begin_in_order();
@@ -697,7 +694,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   W w(lane);
   int slot = 0, stage = kg;
   int ahead = kg;  // tiles until this group's next one, from the job's first
-  unsigned phase = 0, job_phase = 0, joined_phase = 1;
+  unsigned phase = 0, job_phase = 0, turn_phase = 0;
   bool dead = false;  // a wait ran out: the job at hand is the last
   auto wait = [&](unsigned bar, unsigned of) {
     if (!dead && !mbar_wait(bar, of)) {
@@ -943,84 +940,78 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     }
     ahead -= n_tiles;
 
-    // Every key group leaves its sums; the last one of a row group joins them, while the others go on with the next job.
-    wait(ring.joined + rg * 8, joined_phase);  // those of the job before have been read
-    joined_phase ^= 1;
-    bad_page = __any_sync(kFull, bad_page);
-    if (lane == 0) s_bad[warp] = bad_page;
-    float *const mine = join + warp * NT * 8 * P::join_row;
+    // Join the key groups, one after the other, each adding its sums to those before, first the one whose last tile came
+    // first (so the order goes by the sizes alone); the last one puts the results.
+    const int turn = ahead;
+    const unsigned turns = ring.turn + rg * KW * 8;
+    wait(turns + (KW - 1) * 8, turn_phase ^ 1);  // the join of the job before is over (else a turn of that one would pass for this one's)
+    if (turn) wait(turns + (turn - 1) * 8, turn_phase);
+    turn_phase ^= 1;
+    bad_page = __any_sync(kFull, bad_page) || (turn && s_bad[rg]);
+    float4 *const sums = join + rg * (P::join_bytes / RW / 16) + lane;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float4 *const of = sums + nt * (D / 16 + 1) * 32;
+      if (turn) {
+        const float4 b = of[D / 16 * 32];
+        const float t0 = fmaxf(m[nt][0], b.x), t1 = fmaxf(m[nt][1], b.y);
+        const float g0 = exp2_fast(m[nt][0] - t0), g1 = exp2_fast(m[nt][1] - t1), h0 = exp2_fast(b.x - t0), h1 = exp2_fast(b.y - t1);
+        m[nt][0] = t0;
+        m[nt][1] = t1;
+        l[nt][0] = l[nt][0] * g0 + b.z * h0;
+        l[nt][1] = l[nt][1] * g1 + b.w * h1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x = dead ? NAN : l[nt][j];
-        x += __shfl_xor_sync(kFull, x, 4);
-        x += __shfl_xor_sync(kFull, x, 8);
-        x += __shfl_xor_sync(kFull, x, 16);
-        if (lane < 4) {
-          s_m[warp][nt * 8 + lane * 2 + j] = m[nt][j];
-          s_l[warp][nt * 8 + lane * 2 + j] = x;
+        for (int md = 0; md < D / 16; ++md) {
+          const float4 y = of[md * 32];
+          acc[md][nt][0] = acc[md][nt][0] * g0 + y.x * h0;
+          acc[md][nt][1] = acc[md][nt][1] * g1 + y.y * h1;
+          acc[md][nt][2] = acc[md][nt][2] * g0 + y.z * h0;
+          acc[md][nt][3] = acc[md][nt][3] * g1 + y.w * h1;
         }
-        // this lane has kBytes neighbouring elements of every 128 (64)
+      }
+      if (turn < KW - 1) {
+        of[D / 16 * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int md = 0; md < D / 16; md += 2) {
-          const float (&a)[4] = acc[md][nt], (&b)[4] = acc[md + 1][nt];
-          *reinterpret_cast<float4 *>(mine + (nt * 8 + (lane & 3) * 2 + j) * P::join_row + md / (S::kBytes / 2) * 128 + lane / 4 * S::kBytes +
-                                      md % (S::kBytes / 2) * 2) = make_float4(a[j], a[2 + j], b[j], b[2 + j]);
-        }
+        for (int md = 0; md < D / 16; ++md) of[md * 32] = make_float4(acc[md][nt][0], acc[md][nt][1], acc[md][nt][2], acc[md][nt][3]);
       }
     }
-    __threadfence_block();
+    if (lane == 0 && turn < KW - 1) s_bad[rg] = bad_page;
     __syncwarp();
-    int done = 0;
-    if (lane == 0) done = atomicAdd(&s_done[rg], 1);
-    if (__shfl_sync(kFull, done, 0) == KW - 1) {
-      __threadfence_block();
-      bool poison = false;  // rows over a page that does not exist are NaN
+    if (lane == 0) mbar_arrive(turns + turn * 8);
+    if (turn == KW - 1) {
+      if (bad_page && lane == 0) report(GDN_DEVICE_BAD_PAGE);
+      // column 2 (lane % 4) + j of the tile is a row; this lane has kBytes neighbouring elements of every 128 (64) of it
 #pragma unroll
-      for (int i = 0; i < KW; ++i) poison |= s_bad[i * RW + rg] != 0;
-      if (poison && lane == 0) report(GDN_DEVICE_BAD_PAGE);
-#pragma unroll 1
-      for (int x = lane; x < NT * 8 * D / 4; x += 32) {
-        const int n = x / (D / 4), d = x % (D / 4) * 4, item_row = first_row + n;
-        if (item_row >= job.rows) break;
-        float top = s_m[rg][n];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 1; i < KW; ++i) top = fmaxf(top, s_m[i * RW + rg][n]);
-        float sum[4] = {}, den = 0.0f;
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const float g = exp2_fast(s_m[i * RW + rg][n] - top);
-          const float4 y = *reinterpret_cast<const float4 *>(join + ((i * RW + rg) * NT * 8 + n) * P::join_row + d);
-          sum[0] += g * y.x;
-          sum[1] += g * y.y;
-          sum[2] += g * y.z;
-          sum[3] += g * y.w;
-          den += g * s_l[i * RW + rg][n];
-        }
-        if (poison) den = NAN;
-        if (job.slot < 0) {
-          const float inv = 1.0f / den;
+        for (int j = 0; j < 2; ++j) {
+          float den = l[nt][j];
+          den += __shfl_xor_sync(kFull, den, 4);
+          den += __shfl_xor_sync(kFull, den, 8);
+          den += __shfl_xor_sync(kFull, den, 16);
+          if (dead || bad_page) den = NAN;  // rows over a page that does not exist are NaN
+          const int n = nt * 8 + (lane & 3) * 2 + j, item_row = first_row + n;
+          if (item_row >= job.rows) continue;
           const int t = c.group_div.div(item_row);
-          const bool none = before + t < 0 && !poison;  // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
-          T *o = static_cast<T *>(c.out) + static_cast<int64_t>(job.t0 + t) * c.out_stride +
-                 (static_cast<int64_t>(job.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D + d;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = none ? 0.0f : sum[e] * inv;
-          put4(o, sum, c.out_wide);
-        } else {
+          // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
+          const bool none = before + t < 0 && !bad_page && !dead;
+          const float by = job.slot >= 0 ? 1.0f : 1.0f / den;
+          T *const o = static_cast<T *>(c.out) + static_cast<int64_t>(job.t0 + t) * c.out_stride +
+                       (static_cast<int64_t>(job.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D;
           const size_t at = static_cast<size_t>(job.slot) * kRows + row0 + n;
-          *reinterpret_cast<float4 *>(c.part + at * D + d) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-          if (d == 0) c.part_ml[at] = make_float2(top, den);
+#pragma unroll
+          for (int md = 0; md < D / 16; md += 2) {
+            const int d = md / (S::kBytes / 2) * 128 + lane / 4 * S::kBytes + md % (S::kBytes / 2) * 2;
+            float x[4] = {acc[md][nt][j], acc[md][nt][2 + j], acc[md + 1][nt][j], acc[md + 1][nt][2 + j]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = none ? 0.0f : x[e] * by;
+            if (job.slot < 0) put4(o + d, x, c.out_wide);
+            else *reinterpret_cast<float4 *>(c.part + at * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+          }
+          if (job.slot >= 0 && lane < 4) c.part_ml[at] = make_float2(m[nt][j], den);
         }
-      }
       if (job.last >= 0 && rg == 0 && lane == 0)
         c.splits[sh.cta] = Split{job.slot, job.last, job.block * kRows, job.rows, job.t0, job.head * static_cast<int>(c.group), before};
-      __syncwarp();
-      if (lane == 0) {
-        s_done[rg] = 0;
-        mbar_arrive(ring.joined + rg * 8);
-      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(ring.job_empty + slot * 8);
