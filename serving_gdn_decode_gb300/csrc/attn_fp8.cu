@@ -163,12 +163,34 @@ __device__ __forceinline__ constexpr int row_of(int key) {  // the reverse
   return D >= 128 ? key ^ (key & 1) << 2 : (key >> 1 & 1) | ((key ^ key >> 1) & 1) << 1 | (key & 4);
 }
 
-// What a warp has of q and does with a tile.  HALVES: f16 halves of q and of the probabilities (bf16 1, f32 2).
-template <typename T, int D, int NT, int KT>
+// What a warp has of q and does with a tile.  Q_SMEM: its fragments of q are in shared memory, not in registers.
+template <typename T, int D, int NT, int KT, bool Q_SMEM>
 struct Warp8 {
   using S = Shape8<D, KT>;
-  static constexpr int kHalves = sizeof(T) == 4 ? 2 : 1;
-  unsigned q[S::kSteps][NT][kHalves][2];
+  static constexpr int kHalves = sizeof(T) == 4 ? 2 : 1;  // f16 halves of q and of the probabilities
+  static constexpr int kFragments = S::kSteps * NT * kHalves;  // of q
+  static constexpr int kQBytes = Q_SMEM ? kFragments * 256 : 0;
+  unsigned q[Q_SMEM ? 1 : kFragments][2];
+  unsigned q_at;  // Q_SMEM: where this lane's are
+  static constexpr int fragment_of(int ks, int nt, int h) { return (ks * NT + nt) * kHalves + h; }
+  __device__ __forceinline__ void put_q(int i, unsigned b0, unsigned b1) {
+    if constexpr (Q_SMEM) {
+      asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(q_at + i * 256), "r"(b0), "r"(b1) : "memory");
+    } else {
+      q[i][0] = b0;
+      q[i][1] = b1;
+    }
+  }
+  __device__ __forceinline__ Words<2> get_q(int i) const {
+    Words<2> b;
+    if constexpr (Q_SMEM) {
+      load_words(b, q_at + i * 256);
+    } else {
+      b.w[0] = q[i][0];
+      b.w[1] = q[i][1];
+    }
+    return b;
+  }
   float by[NT][2];  // what takes the column's sums of codes to scores in the log2 domain
   unsigned k_at, v_at[2];  // this lane's offsets: of row g = lane / 4 of K; of rows g = 2 (lane % 4), and one more, of V
 
@@ -211,53 +233,65 @@ struct Warp8 {
 #pragma unroll
       for (int j = 0; j < 2; ++j) by[nt][j] = __shfl_sync(kFull, back, ((lane & 3) * 2 + j) * 4);
 #pragma unroll
-      for (int ks = 0; ks < S::kSteps; ++ks)
+      for (int ks = 0; ks < S::kSteps; ++ks) {
+        unsigned hi[2], lo[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float u = x[ks][2 * b] * f, v = x[ks][2 * b + 1] * f;
-          q[ks][nt][0][b] = f16x2(u, v);
-          if constexpr (kHalves == 2) {
-            const float2 h = f32x2(q[ks][nt][0][b]);
-            q[ks][nt][1][b] = f16x2(u - h.x, v - h.y);
-          }
+          hi[b] = f16x2(u, v);
+          const float2 h = f32x2(hi[b]);
+          lo[b] = f16x2(u - h.x, v - h.y);
         }
+        put_q(fragment_of(ks, nt, 0), hi[0], hi[1]);
+        if constexpr (kHalves == 2) put_q(fragment_of(ks, nt, 1), lo[0], lo[1]);
+      }
     }
+    __syncwarp();
   }
 
-  // s = K Q^T of 16 keys, as sums of codes
-  __device__ __forceinline__ void scores(float (&s)[NT][4], unsigned k_tile) const {
+  // s = K Q^T of the tile, as sums of codes
+  __device__ __forceinline__ void scores(float (&s)[KT][NT][4], unsigned k_tile) const {
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
-      Words<4> lo, hi;
-      const unsigned at = k_tile + (k_at ^ ((g & 1) << 6)) + (g >> 1) * S::kPart;
-      load_words(lo, at);
-      load_words(hi, at + 8 * S::kRow);
-      float t[NT][4];  // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements
-      unsigned a[4][4];
+      unsigned a[KT][4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i][0] = codes_f16x2(lo.w[i], 0);
-        a[i][1] = codes_f16x2(hi.w[i], 0);
-        a[i][2] = codes_f16x2(lo.w[i], 2);
-        a[i][3] = codes_f16x2(hi.w[i], 2);
+      for (int kt = 0; kt < KT; ++kt) {
+        Words<4> lo, hi;
+        const unsigned at = k_tile + kt * kSub * S::kRow + (k_at ^ ((g & 1) << 6)) + (g >> 1) * S::kPart;
+        load_words(lo, at);
+        load_words(hi, at + 8 * S::kRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[kt][i][0] = codes_f16x2(lo.w[i], 0);
+          a[kt][i][1] = codes_f16x2(hi.w[i], 0);
+          a[kt][i][2] = codes_f16x2(lo.w[i], 2);
+          a[kt][i][3] = codes_f16x2(hi.w[i], 2);
+        }
       }
+      float t[KT][NT][4];  // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements
 #pragma unroll
       for (int h = kHalves - 1; h >= 0; --h)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float (&to)[4] = kHalves == 2 && g > 0 ? t[nt] : s[nt];
-            const bool first = i == 0 && h == kHalves - 1 && (kHalves == 2 || g == 0);
-            if (first) mma_f16_first(to, a[i], q[g * 4 + i][nt][h][0], q[g * 4 + i][nt][h][1]);
-            else mma_f16(to, a[i], q[g * 4 + i][nt][h][0], q[g * 4 + i][nt][h][1]);
+            const Words<2> b = get_q(fragment_of(g * 4 + i, nt, h));
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              float (&to)[4] = kHalves == 2 && g > 0 ? t[kt][nt] : s[kt][nt];
+              const bool first = i == 0 && h == kHalves - 1 && (kHalves == 2 || g == 0);
+              if (first) mma_f16_first(to, a[kt][i], b.w[0], b.w[1]);
+              else mma_f16(to, a[kt][i], b.w[0], b.w[1]);
+            }
           }
       if constexpr (kHalves == 2) {
         if (g > 0)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[nt][j] += t[nt][j];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[kt][nt][j] += t[kt][nt][j];
       }
     }
   }
@@ -327,12 +361,13 @@ struct Warp8 {
 
 // A variant: NT 8-row tiles of a warp, RW warps that share their tiles, each with rows of its own, WARPS of a CTA beside
 // the FEED that feed them, KT matrix tiles of 16 keys in a step, CTAS on an SM.  BOXED: pages hold whole groups of 8 keys.
-template <typename T_, int D_, int NT_, int RW_, int WARPS_, int FEED_, int KT_, int CTAS_, bool BOXED_>
+template <typename T_, int D_, int NT_, int RW_, int WARPS_, int FEED_, int KT_, int CTAS_, bool BOXED_, bool Q_SMEM_ = false>
 struct Pick8 {
   using T = T_;
   using S = Shape8<D_, KT_>;
   static constexpr int D = D_, NT = NT_, RW = RW_, WARPS = WARPS_, FEED = FEED_, KT = KT_, CTAS = CTAS_;
   static constexpr bool BOXED = BOXED_;
+  using W = Warp8<T_, D_, NT_, KT_, Q_SMEM_>;
   static constexpr int rows = NT * RW * 8, ctas = kSms * CTAS, threads = 32 * (WARPS + FEED);
   // items that are known ahead, with their q
   static constexpr int q_row = D * static_cast<int>(sizeof(T)) + 16, q_bytes = rows * q_row, slots = q_bytes <= 2400 ? 4 : q_bytes <= 4800 ? 3 : 2;
@@ -340,7 +375,8 @@ struct Pick8 {
   static constexpr int groups = BOXED ? KT * 2 : S::kTile, scales = 2 * groups * 4;
   // a row group's sums at a job's end, as its warps have them in registers: those of values, of probabilities, and the maximum
   static constexpr int join_bytes = RW * (D / 16 * 4 + 4) * NT * 128;
-  static constexpr int fixed = join_bytes + slots * q_bytes;
+  static constexpr int fragment_bytes = slots * RW * W::kQBytes;
+  static constexpr int fixed = join_bytes + slots * q_bytes + fragment_bytes;
   // the ring has what the SM's shared memory holds beside that and the static part
   static constexpr int fit = (228 * 1024 / CTAS - 1024 - 1024 - 512 - 64 * WARPS * NT - 24 * 32 - fixed) / (S::kStage + scales);
   // A stage is always filled by the same warp and emptied by the same group: waits tell two phases of a barrier apart, and
@@ -362,7 +398,7 @@ struct Job {
 
 // What the feeding warps and the others share beside the ring: shared-memory addresses.
 struct Ring {
-  unsigned stages, scales, q, missing;
+  unsigned stages, scales, q, fragments, missing;
   unsigned full, empty, job_full, job_empty, turn;  // of barriers: of a stage, of a job's slot, of a key group's turn to join
   Job *jobs;
 };
@@ -654,7 +690,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   using T = typename P::T;
   constexpr int D = P::D, NT = P::NT, RW = P::RW, WARPS = P::WARPS, KT = P::KT;
   using S = Shape8<D, KT>;
-  using W = Warp8<T, D, NT, KT>;
+  using W = typename P::W;
   constexpr int kTile = S::kTile;
   constexpr int kRows = P::rows;       // rows of a block
   constexpr int KW = WARPS / RW;       // key groups: group g takes every KW-th tile of the share
@@ -669,7 +705,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned start = (1024u - (smem_u32(smem) & 1023u)) & 1023u;
   float4 *join = reinterpret_cast<float4 *>(smem + start + P::STAGES * (S::kStage + P::scales));
-  const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + P::join_bytes,
+  const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + P::join_bytes, smem_u32(join) + P::join_bytes + P::slots * P::q_bytes,
                   smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_turn), s_jobs};
   if (tid < P::STAGES) {
     mbar_init(ring.full + tid * 8, P::BOXED ? 2 : 33);  // what the feeding warp stores, and its copies
@@ -733,6 +769,8 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     const int n_tiles = (k1 - job.k0 + kTile - 1) / kTile;
     int key0 = job.k0 + ahead * kTile;
     bool bad_page = false;
+    // (every key group puts the same fragments)
+    w.q_at = ring.fragments + (slot * RW + rg) * W::kQBytes + lane * 8;
     if (ahead < n_tiles) w.template load_q<P::q_row>(ring.q + slot * P::q_bytes, lane, row0, c.scale_log2);
 #pragma unroll 1
     for (; ahead < n_tiles; ahead += KW, key0 += kTile * KW) {
@@ -755,8 +793,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
       // keys that a row of this warp sees, of the tile
       const int seen0 = edge && c.window ? max(0, less_window(last0 + 1 - key0, c.window)) : 0;
       const int seen1 = edge ? min(min(last1 + 1, k1) - key0, kTile) : kTile;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) w.scores(s[kt], k_tile + kt * kSub * S::kRow);
+      w.scores(s, k_tile);
       float vs[KT][2];  // the scales of the values of this lane's keys; BOXED: of these groups of 8 keys
       unsigned most = 0u, least = 0xffffffffu;  // of those that a row sees
 #pragma unroll
@@ -1068,16 +1105,16 @@ auto dispatch(const gdn_attn_params &p, bool boxed, F f) {
       return !boxed       ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, false>{})
              : rows <= 8  ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, true>{})
              : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 2, 2, true>{})
-                          : f(Pick8<T, 64, 2, 2, 6, 2, 2, 1, true>{});
+                          : f(Pick8<T, 64, 4, 1, 4, 2, 2, 1, true, true>{});
     if (p.head_dim == 128)
-      return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false>{})
-             : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true>{})
-             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 3, 1, 2, 2, true>{})
-                          : f(Pick8<T, 128, 2, 2, 6, 2, 2, 1, true>{});
-    return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false>{})
-           : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true>{})
-           : rows <= 16 ? f(Pick8<T, 256, 1, 2, 6, 2, 1, 1, true>{})
-                        : f(Pick8<T, 256, 1, 4, 8, 2, 1, 1, true>{});
+      return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false, sizeof(T) == 4>{})
+             : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true, sizeof(T) == 4>{})
+             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 6, 2, 2, 1, true, true>{})
+                          : f(Pick8<T, 128, 2, 2, 6, 2, 2, 1, true, true>{});
+    return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false, sizeof(T) == 4>{})
+           : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true, sizeof(T) == 4>{})
+           : rows <= 16 ? f(Pick8<T, 256, 2, 1, 6, 2, 1, 1, true, true>{})
+                        : f(Pick8<T, 256, 2, 2, 6, 2, 1, 1, true, true>{});
   };
   return p.dtype == GDN_DTYPE_BF16 ? by_dim(__nv_bfloat16{}) : by_dim(float{});
 }
