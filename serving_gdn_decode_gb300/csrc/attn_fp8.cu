@@ -251,6 +251,9 @@ struct Warp8 {
 
   // s = K Q^T of the tile, as sums of codes
   __device__ __forceinline__ void scores(float (&s)[KT][NT][4], unsigned k_tile) const {
+    // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements; bf16's in two chains, for the
+    // products' latency
+    float t[KT][NT][4];
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
       unsigned a[KT][4][4];
@@ -268,7 +271,6 @@ struct Warp8 {
           a[kt][i][3] = codes_f16x2(hi.w[i], 2);
         }
       }
-      float t[KT][NT][4];  // the tensor cores cut the low bits of a running sum: f32's are taken over 64 elements
 #pragma unroll
       for (int h = kHalves - 1; h >= 0; --h)
 #pragma unroll
@@ -278,14 +280,13 @@ struct Warp8 {
             const Words<2> b = get_q(fragment_of(g * 4 + i, nt, h));
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-              float (&to)[4] = kHalves == 2 && g > 0 ? t[kt][nt] : s[kt][nt];
-              const bool first = i == 0 && h == kHalves - 1 && (kHalves == 2 || g == 0);
+              float (&to)[4] = kHalves == 2 ? (g > 0 ? t[kt][nt] : s[kt][nt]) : g & 1 ? t[kt][nt] : s[kt][nt];
+              const bool first = i == 0 && h == kHalves - 1 && (kHalves == 2 || g < 2);
               if (first) mma_f16_first(to, a[kt][i], b.w[0], b.w[1]);
               else mma_f16(to, a[kt][i], b.w[0], b.w[1]);
             }
           }
-      if constexpr (kHalves == 2) {
-        if (g > 0)
+      if (kHalves == 2 ? g > 0 : D > 64 && g == D / 64 - 1) {
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -384,6 +385,7 @@ struct Pick8 {
   static constexpr int turn = std::lcm(WARPS / RW, FEED), STAGES = (fit < 32 ? fit : 32) / turn * turn;
   static constexpr int smem = 1024 + STAGES * (S::kStage + scales) + fixed;  // stages begin at multiples of 1024
   static_assert(STAGES > WARPS / RW && STAGES % (WARPS / RW) == 0 && STAGES % FEED == 0, "two stages per key group at least");
+  static_assert(FEED <= 8 && (FEED & (FEED - 1)) == 0, "a batch of the feeding warps' boxes holds a multiple of FEED tiles");
 };
 
 // An item, or the part of it that lies in a CTA's share, as the feeding warps tell the others.
@@ -1105,11 +1107,11 @@ auto dispatch(const gdn_attn_params &p, bool boxed, F f) {
       return !boxed       ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, false>{})
              : rows <= 8  ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, true>{})
              : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 2, 2, true>{})
-                          : f(Pick8<T, 64, 4, 1, 4, 2, 2, 1, true, true>{});
+                          : f(Pick8<T, 64, 2, 2, 4, 2, 2, 2, true, sizeof(T) == 4>{});
     if (p.head_dim == 128)
       return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false, sizeof(T) == 4>{})
              : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true, sizeof(T) == 4>{})
-             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 6, 2, 2, 1, true, true>{})
+             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 4, 2, 1, 2, true, true>{})
                           : f(Pick8<T, 128, 2, 2, 6, 2, 2, 1, true, true>{});
     return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false, sizeof(T) == 4>{})
            : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true, sizeof(T) == 4>{})
