@@ -132,7 +132,6 @@ __device__ __forceinline__ void copy_box(unsigned dst, const CUtensorMap *map, i
 template <int D, int KT>
 struct Shape8 {
   static constexpr int kTile = kSub * KT;
-  static constexpr int kChunks = D / 16;  // 16-byte chunks per row
   static constexpr int kRow = D < 128 ? D : 128;  // of a part
   static constexpr int kParts = D / kRow;
   static constexpr int kPart = kTile * kRow;
@@ -405,8 +404,8 @@ struct Ring {
   Job *jobs;
 };
 
-// A feeding warp: puts every FEED-th tile of the share's items into the ring, and the first one an item's rows of q before.
-// (One alone takes 600 to 1000 clocks for a tile, all latency: waits, exchanges of lanes, 140 to issue a tensor copy.)
+// A feeding warp: puts every FEED-th tile of the share's items into the ring, and the last one the items themselves.
+// (One alone takes 600 to 1000 clocks for a tile, all latency: waits, exchanges of lanes, 60 to 80 to issue a tensor copy.)
 template <typename P>
 struct Feed {
   using T = typename P::T;
@@ -434,7 +433,7 @@ struct Feed {
   // The item at unit u as a job, and its rows of q: row n is token n / group, query head n % group of the key head; zeros
   // for those that are not.
   __device__ __forceinline__ bool put_job(const Share &sh, const Part &f, int head, long long u) {
-    if (id != 0) return true;
+    if (id != P::FEED - 1) return true;  // (the other one has the first tile meanwhile)
     if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) return give_up();
     const int block = f.item - head * f.r.blocks, rows = f.r.tokens * static_cast<int>(c.group);
     if (lane == 0) {
@@ -482,7 +481,7 @@ struct Feed {
   }
   // After the last item.
   __device__ __forceinline__ void put_end() {
-    if (id == 0) {
+    if (id == P::FEED - 1) {
       if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) {
         give_up();
         return;
@@ -518,7 +517,7 @@ struct Feed {
 // the pages looked up two such batches ahead and the scales one.
 template <typename P>
 __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_map, const CUtensorMap *v_map, const Share &sh, uint32_t seq,
-                                           long long in_seq, const Ring &ring) {
+                                           long long in_seq, const Request &first, const Ring &ring) {
   using S = typename P::S;
   constexpr int kTile = S::kTile, kMost = kTile / 8;  // boxes of a tile
   Feed<P> d(c, ring);
@@ -526,7 +525,7 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
   typename Feed<P>::Part f;
   f.seq = seq;
   f.in_seq = in_seq;
-  f.r = request<P::rows>(c, seq);
+  f.r = first;
   long long u = sh.u0;
   // of a batch: this lane's box's page, or -1 where there is none, and its scales; what an item begins with is found while the
   // one before is fed
@@ -627,19 +626,20 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
 
 // Row by row, for pages of any size: a lane has a key of the tile.
 template <typename P>
-__device__ __forceinline__ void feed_rows(const Call &c, const Share &sh, uint32_t seq, long long in_seq, const Ring &ring) {
+__device__ __forceinline__ void feed_rows(const Call &c, const Share &sh, uint32_t seq, long long in_seq, const Request &first, const Ring &ring) {
   using S = typename P::S;
   constexpr int D = P::D, kTile = S::kTile;
-  constexpr int kPer = 32 / S::kChunks;               // rows one access of the warp covers
-  constexpr int kAccesses = kTile * S::kChunks / 32;  // of K or V
+  constexpr int kChunks = D / 16;                  // 16-byte chunks per row
+  constexpr int kPer = 32 / kChunks;               // rows one access of the warp covers
+  constexpr int kAccesses = kTile * kChunks / 32;  // of K or V
   Feed<P> d(c, ring);
-  const int lane = d.lane, my_row = lane / S::kChunks, my_chunk = lane % S::kChunks;
+  const int lane = d.lane, my_row = lane / kChunks, my_chunk = lane % kChunks;
   const unsigned mine = place<D, P::KT>(my_row, my_chunk);
   const char *const k = static_cast<const char *>(c.k) + my_chunk * 16, *const v = static_cast<const char *>(c.v) + my_chunk * 16;
   typename Feed<P>::Part f;
   f.seq = seq;
   f.in_seq = in_seq;
-  f.r = request<P::rows>(c, seq);
+  f.r = first;
   for (long long u = sh.u0; f.find(c, u, sh.u1); f.pass(u)) {
     const int head = f.item / f.r.blocks;
     const int32_t *const table = c.table + static_cast<uint64_t>(f.seq) * c.max_pages;
@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[WARPS + P::FEED], s_offset;
   __shared__ uint32_t s_seq;
+  __shared__ Request s_first;
   __shared__ unsigned s_bad[RW];
   __shared__ unsigned s_missing[P::STAGES];
   __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_turn[WARPS];
@@ -721,11 +722,11 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   begin_in_order();
-  const Share sh = take_share<kRows, WARPS + P::FEED>(c, s_scan, s_seq, s_offset);  // (its barriers show the initialised ones)
+  const Share sh = take_share<kRows, WARPS + P::FEED>(c, s_scan, s_seq, s_offset, &s_first);  // (its barriers show the initialised ones)
   if (sh.cta >= sh.ctas) return;
   if (warp >= WARPS) {
-    if constexpr (P::BOXED) feed_boxes<P>(c, &k_map, &v_map, sh, s_seq, s_offset, ring);
-    else feed_rows<P>(c, sh, s_seq, s_offset, ring);
+    if constexpr (P::BOXED) feed_boxes<P>(c, &k_map, &v_map, sh, s_seq, s_offset, s_first, ring);
+    else feed_rows<P>(c, sh, s_seq, s_offset, s_first, ring);
     return;
   }
   const int kg = warp / RW, rg = warp % RW, row0 = rg * NT * 8;  // key group; rows of the block

@@ -222,9 +222,11 @@ struct Share {
 };
 
 // The share of this CTA, by the prefix sum of the requests' units, a contiguous run of requests per thread.  `seq` and
-// `offset` become the request of its first unit and the unit's place in the request.  Every thread of the CTA takes part.
+// `offset` become the request of its first unit and the unit's place in the request, `first` that request.  Every thread
+// of the CTA takes part.
 template <int ROWS, int WARPS>
-__device__ __forceinline__ Share take_share(const Call &c, long long (&scan)[WARPS], uint32_t &seq, long long &offset) {
+__device__ __forceinline__ Share take_share(const Call &c, long long (&scan)[WARPS], uint32_t &seq, long long &offset,
+                                            Request *first = nullptr) {
   constexpr int kThreads = 32 * WARPS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t per = (c.n_seqs + kThreads - 1) / kThreads;
@@ -264,8 +266,10 @@ __device__ __forceinline__ Share take_share(const Call &c, long long (&scan)[WAR
   if (sh.u0 >= before && sh.u0 < before + mine) {
     long long at = before;
     for (uint32_t s = s_first; s < s_last; ++s) {
-      const long long n = request<ROWS>(c, s).units(c);
+      const Request r = request<ROWS>(c, s);
+      const long long n = r.units(c);
       if (sh.u0 < at + n) {
+        if (first) *first = r;
         seq = s;
         offset = sh.u0 - at;
         break;
