@@ -637,7 +637,13 @@ gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const v
  * byte and multiples of 16), the same rows, windows, table rules, checks,
  * workspace rules (gdn_attn_fp8_workspace_size) and reports.  Codes are exact
  * in the products; a page's scale multiplies the scores (k) and the sums (v) in
- * f32.  A scale that is NaN reaches the rows that see a key of its page.
+ * f32.  q is exact in bf16 (down to 2^-31 of its row's largest element; f32: good
+ * to 2^-22), a probability good to 2^-11 in bf16, where the result's rounding takes
+ * 2^-8, and to 2^-22 in f32.  Values above 2^95 may give infinities.  A scale that is
+ * NaN reaches the rows that see a key of its page.  Pages of whole groups of 8 (for
+ * heads of 64: 16) tokens go by tensor copies and are the fastest; any page_size is
+ * taken.  A wait inside the kernel that runs out, which no call is known to cause,
+ * sets GDN_DEVICE_WAIT_TIMEOUT; the rows concerned are NaN or not written.
  */
 gdn_status gdn_attn_fp8_workspace_size(const gdn_attn_params *params, size_t *bytes);
 
@@ -653,7 +659,7 @@ gdn_status gdn_attn_paged_fp8(const void *q, const void *k_cache, const void *v_
 const char *gdn_last_error(void);
 
 /* Bits of the device status word. */
-#define GDN_DEVICE_WAIT_TIMEOUT 0x1u /* a chunked kernel's bounded wait ran out */
+#define GDN_DEVICE_WAIT_TIMEOUT 0x1u /* a bounded wait ran out: a chunked kernel's, gdn_attn_paged_fp8's */
 #define GDN_DEVICE_OUT_OF_PAGES 0x2u /* gdn_kv_plan: the free stack could not serve a request */
 #define GDN_DEVICE_BAD_REQUEST 0x4u  /* gdn_kv_plan, gdn_attn_paged*: impossible lengths or offsets; gdn_kv_store_fp8: a page's
                                         tokens out of order */

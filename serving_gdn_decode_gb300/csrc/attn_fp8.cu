@@ -3,30 +3,47 @@
 // of k_j and v_j is an e4m3 code times the scale of its page and key head.
 //
 // What bounds it.  Every code is read once and used for group x window rows: 4 to
-// 200 flops a byte, so HBM bounds it up to some 16 rows per key head, as it bounds
-// the kernel over a bf16 cache, at half the bytes.  The same structure serves (its
-// file gives the reasons): a token's rows on the N side of the warp-level matrix
-// instruction (S^T = K Q^T, O^T = V^T P^T), and shares of a list of units.  What
-// differs is how codes become operands, and how they come: one warp of a CTA feeds
-// a ring of tiles with 16-byte asynchronous copies, across items, and the others
-// take its tiles in turn, so that these have neither the copies' instructions nor
-// their registers, and more of them fit an SM.
+// 200 flops a byte.  HBM bounds 1 to 8 rows per key head; past that the warp-level
+// instructions do.  As in the kernel over a cache of f32 or bf16 (attn_paged.cu), a
+// token's rows are on the N side of the matrix instruction (S^T = K Q^T, O^T = V^T
+// P^T), and the CTAs take shares of a list of units.  What differs is how codes
+// become operands, and how they come.
 //
-// Operands.  e4m3 is a part of f16, so a code is exact there, and the products are
-// those of f16 matrix instructions with f32 sums.  q goes in with each row scaled
-// by a power of two to below 2^14 (exact for bf16; f32 as two halves), the
-// probabilities relative to a maximum such that they lie below 2^15 and lose
-// nothing above 2^-35 of the largest.  The contraction of a product may go
-// in any order, so the order is that of the memory: a lane takes 16 neighbouring
-// bytes of a key for four steps of Q K^T, and 16 neighbouring elements of four
-// values for eight steps of P V, whose result then has 16 neighbouring elements in
-// each lane.  So shared memory is read 16 bytes at a time, and nothing is
-// transposed but bytes of two keys in registers.
+// Operands.  e4m3 is a part of f16, so a code is exact there (one instruction for
+// two), and the products are those of f16 matrix instructions with f32 sums.  q goes
+// in with each row scaled by a power of two to below 2^14 (exact for bf16 down to
+// 2^-31 of the row's largest; f32 as two halves), the probabilities relative to a
+// maximum such that they lie below 2^15 and lose nothing above 2^-35 of the largest.
+// f16 rounds a probability by 2^-11 of itself at most, to either side, an eighth of
+// what the result's rounding to bf16 takes; for f32 it is two halves.  The contraction
+// of a product may go in any order, so the order is that of the memory: a lane takes
+// 16 neighbouring bytes of a key for four steps of Q K^T, and 16 neighbouring elements
+// of four values for eight steps of P V, whose result then has 16 neighbouring elements
+// in each lane.  So shared memory is read 16 bytes at a time without bank conflicts,
+// and nothing is transposed but bytes of two keys in registers.
 //
 // Scales.  A key's scale multiplies its scores.  A tile's values are summed as
 // codes, times their page's scale over the largest of the tile, and the sums are
 // added to the running ones, in f32, times that largest.  Where scales of a tile
 // are further apart than 2^8 its pages take products of their own.
+//
+// Feeding.  Some warps of a CTA do nothing but fill a ring of tiles, by tensor copies
+// of boxes of a page's rows, across items; the others take its tiles in turn.  So these
+// have neither the copies' instructions nor their registers, hold no request (an item
+// comes to them as a job in shared memory), and more of them fit an SM: 12 warps of
+// 168 registers.  With the copies in every warp, a ring for each (8 warps of 240
+// registers): 64 requests of up to 4096 keys, 32/8 heads of 128, bf16: 68 us, now 53;
+// 256 requests, 48/8 heads: 214, now 170.  A feeding warp needs 600 to 900 clocks for a
+// tile, all latency, an SM's share of HBM one in 360: hence two in each of two CTAs.
+//
+// Measured on a GB300, back to back over three sets of buffers, as shares of the
+// measured copy bandwidth (6767 GB/s): 256 requests as above 170 us, 0.92; 64: 53 us,
+// 0.75; one request of 400 009 keys, 32/4 heads of 128: 76 us, 0.79 (in between 0.97:
+// 5 us until the first tile -- lengths, pages, tile and q are dependent reads -- and 7 for
+// the join); 32 requests, windows of 1 to 4, 16/2 heads of 256: 60 us, 0.32; f32, 24
+// requests with a window of 1000 keys, 16/16 heads of 64: 19.6 us; pages of 24, 24/8
+// heads of 64: 19.6 us.  32 requests up to 4096 keys, 8 key heads of 128, by rows per key
+// head: 8: 37 us, 16: 48, 32: 71 (over a bf16 cache 56, 60, 83).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1078,10 +1095,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// Whether the cache's pages go by tensor copies: they hold whole groups of 8 keys, and the strides are not too long for them.
+// Whether the cache's pages go by tensor copies: they hold whole groups of 8 keys, and the strides are not too long for
+// them.  Boxes of 8 rows of 64 elements are 512 bytes: the copies' instructions would take longer than asynchronous copies
+// row by row (pages of 24, 40 requests up to 3001 keys, 24/8 heads: 22.5 us by boxes, 19.6 by rows).
 bool takes_boxes(const gdn_attn_params &p) {
   const int64_t most = int64_t{1} << 40;
-  return p.page_size % 8 == 0 && p.cache_page_stride < most && p.cache_head_stride < most && p.cache_slot_stride < most &&
+  return p.page_size % (p.head_dim == 64 ? 16 : 8) == 0 && p.cache_page_stride < most && p.cache_head_stride < most && p.cache_slot_stride < most &&
          tensor_map_encoder() != nullptr;
 }
 
@@ -1098,7 +1117,12 @@ cudaError_t cache_map(CUtensorMap *map, const void *cache, const gdn_attn_params
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Calls f with the variant of the call: the fewest rows per block that hold the rows of its requests.
+// Calls f with the variant of the call: the fewest rows per block that hold the rows of its requests.  A warp with two row
+// tiles converts a code once for 16 rows, where two warps with one would do it twice (32 requests, windows of 1 to 4, 8 heads of
+// 256 per key head: 71 us with four warps of a row tile each, 60 with two of two); q's fragments are in shared memory where they
+// would not fit the registers.  32 requests up to 4096 keys, 8 key heads of 128, 12 rows: 54.6 us with six warps of 255
+// registers, 47.9 with eight of 168; 32 rows: 69.8 and 75.6; of 64, 32 rows: 74.7 with one CTA, whose two feeding warps are too
+// few, 46.2 with two.
 template <typename F>
 auto dispatch(const gdn_attn_params &p, bool boxed, F f) {
   const uint64_t rows = rows_of(p);

@@ -14,7 +14,20 @@
 // follow one another in a page) of one head of k or of v: its largest magnitude
 // decides the scale, with the scale of the page's earlier tokens if it does not
 // begin the page.  Units share nothing, so nothing is atomic.  A team of warps
-// takes a unit and keeps its rows in registers between the maximum and the codes.
+// takes a unit and keeps its rows in registers between the maximum and the codes;
+// the heads of the same tokens go to neighbouring CTAs, so that rows which lie side
+// by side are read at one time (23.1 -> 21.5 us for four prompts of 12 400 tokens
+// together, 8 heads of 128, bf16).  The maximum is taken of the bits, two bf16 at a
+// time, and values that are not finite are looked for only where it shows one.
+//
+// Measured on a GB300: those four prompts, pages of 64: 18.1 us, 4.2 TB/s, 0.62 of
+// the copy bandwidth: instructions bound it (19 for an element at first: 24.9 us),
+// and a team's life is a chain of slots, rows and codes with nothing of the next run
+// on its way; 64 tokens: 2.9 us, launch latency; 37 requests, decodes and two prompts
+// of up to 333 tokens, f32, 2 heads of 256: 8.5 us.
+//
+// Load.  A warp takes a token: 28 us for 33 000 tokens of 8 heads of 128 to bf16, 0.9
+// of the copy bandwidth.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -163,7 +176,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 4 : W > 2 ? 8 : 
       if (slot >= 0) {
         const uint32_t page = c.page_div.div(slot);
         const bool same = before >= 0 && c.page_div.div(before) == page;
-        begins = !(same && before + 1 == slot);
+        begins = !(same && before == slot - 1);
         if (page >= p.n_pages) {
           if (begins) report(GDN_DEVICE_BAD_PAGE);
           begins = false;
