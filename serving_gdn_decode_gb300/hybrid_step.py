@@ -11,7 +11,8 @@ graph and replayed::
     python -m serving_gdn_decode_gb300.hybrid_step --requests 16 --prompt 100 --steps 64
 
 With ``--check`` the logits of the last step are compared with those of a model
-that sees all tokens at once.
+that sees all tokens at once.  With ``--cache fp8`` keys and values are held in 8
+bits (``gdn_kv_store_fp8`` after ``gdn_rope``, and ``gdn_attn_paged_fp8``).
 """
 from __future__ import annotations
 
@@ -21,8 +22,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (gdn_attn_paged, gdn_attn_workspace_size, gdn_forward, gdn_kv_plan, gdn_rope_store,
-               pack_params)
+from . import (gdn_attn_fp8_workspace_size, gdn_attn_paged, gdn_attn_paged_fp8, gdn_attn_workspace_size, gdn_forward,
+               gdn_kv_plan, gdn_kv_store_fp8, gdn_rope, gdn_rope_store, pack_params)
 
 
 @dataclass(frozen=True)
@@ -40,6 +41,7 @@ class Config:
     vocab: int = 1024
     page: int = 16
     max_tokens: int = 4096
+    cache: str = "f32"  # or fp8: e4m3 codes with a scale for each page and key head
 
 
 def rope_table(cfg: Config, device) -> torch.Tensor:
@@ -68,6 +70,8 @@ class Server:
 
     def __init__(self, model: Model, requests: int, prompt: int, tokens: int):
         cfg, dev, s = model.cfg, model.device, requests
+        if cfg.cache not in ("f32", "fp8"):
+            raise ValueError(f"no cache of {cfg.cache!r}")
         if tokens > cfg.max_tokens:  # past the table of cosines the rotated q and k would be NaN
             raise ValueError(f"{tokens} tokens per request, but the model has {cfg.max_tokens} positions")
         self.model, self.requests = model, s
@@ -76,7 +80,10 @@ class Server:
         i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device=dev)  # noqa: E731
         self.states = [torch.zeros(s * cfg.gdn_v_heads * cfg.gdn_dim ** 2, device=dev) for _ in model.gdn]
         shape = (self.n_pages, cfg.kv_heads, cfg.page, cfg.head_dim)
-        self.caches = [(torch.zeros(shape, device=dev), torch.zeros(shape, device=dev)) for _ in model.attn]
+        self.fp8 = cfg.cache == "fp8"
+        dtype = torch.float8_e4m3fn if self.fp8 else torch.float32
+        self.caches = [tuple(torch.zeros(shape, device=dev).to(dtype) for _ in range(2)) for _ in model.attn]
+        self.scales = [tuple(torch.zeros(shape[:2], device=dev) for _ in range(2)) for _ in model.attn]  # of an fp8 cache
         self.table = torch.full((s, self.max_pages), -1, dtype=torch.int32, device=dev)
         self.free = torch.arange(self.n_pages, dtype=torch.int32, device=dev)
         self.ctx, self.owned, self.n_free = i32(s), i32(s), torch.full((1,), self.n_pages, dtype=torch.int32, device=dev)
@@ -84,10 +91,11 @@ class Server:
         self.by_width = {}  # per step width: buffers of the step, made once
         for width in (prompt, 1):
             q = torch.empty(s * width, cfg.q_heads, cfg.head_dim, device=dev)
+            size = gdn_attn_fp8_workspace_size if self.fp8 else gdn_attn_workspace_size
             self.by_width[width] = dict(
                 new=torch.full((s,), width, dtype=torch.int32, device=dev), slots=i32(s * width), positions=i32(s * width),
-                q=q, o=torch.empty_like(q),
-                workspace=torch.empty(gdn_attn_workspace_size(q, self.caches[0][0], s), dtype=torch.uint8, device=dev))
+                q=q, k=torch.empty(s * width, cfg.kv_heads, cfg.head_dim, device=dev), o=torch.empty_like(q),
+                workspace=torch.empty(size(q, self.caches[0][0], s), dtype=torch.uint8, device=dev))
 
     def step(self, ids: torch.Tensor, width: int) -> torch.Tensor:
         """`width` new tokens per request (ids: [requests * width]); the logits of the last one of each."""
@@ -98,7 +106,7 @@ class Server:
         for i in range(cfg.blocks):
             for j in range(i * cfg.gdn_per_block, (i + 1) * cfg.gdn_per_block):
                 x = x + self._gdn(m.gdn[j], self.states[j], _norm(x), width)
-            x = x + self._attn(m.attn[i], self.caches[i], _norm(x), b)
+            x = x + self._attn(m.attn[i], self.caches[i], self.scales[i], _norm(x), b)
         # the next step starts where this one ended
         self.ctx.copy_(self.kv_lens)
         self.owned.copy_(self.owned_out)
@@ -118,13 +126,18 @@ class Server:
         gdn_forward(q, k, v.contiguous(), g, beta, state, y, state, p)
         return y.view(x.shape[0], -1) @ w["out"]
 
-    def _attn(self, w, cache, x, b):
+    def _attn(self, w, cache, scales, x, b):
         cfg = self.model.cfg
         d, nq, nkv = cfg.head_dim, cfg.q_heads, cfg.kv_heads
         qkv = x @ w["qkv"]
         q, k, v = (t.unflatten(1, (-1, d)) for t in qkv.split([nq * d, nkv * d, nkv * d], 1))
-        gdn_rope_store(q, k, v, b["positions"], self.model.table, b["slots"], *cache, b["q"])
-        gdn_attn_paged(b["q"], *cache, self.table, self.kv_lens, self.start, b["o"], b["workspace"])
+        if self.fp8:
+            gdn_rope(q, k, b["positions"], self.model.table, b["q"], b["k"])
+            gdn_kv_store_fp8(b["k"], v, b["slots"], *cache, *scales)
+            gdn_attn_paged_fp8(b["q"], *cache, *scales, self.table, self.kv_lens, self.start, b["o"], b["workspace"])
+        else:
+            gdn_rope_store(q, k, v, b["positions"], self.model.table, b["slots"], *cache, b["q"])
+            gdn_attn_paged(b["q"], *cache, self.table, self.kv_lens, self.start, b["o"], b["workspace"])
         return b["o"].view(x.shape[0], -1) @ w["out"]
 
 
@@ -164,9 +177,10 @@ def main(argv=None):
     ap.add_argument("--requests", type=int, default=16)
     ap.add_argument("--prompt", type=int, default=100)
     ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--cache", choices=("f32", "fp8"), default="f32")
     ap.add_argument("--check", action="store_true", help="compare the last logits with those of one pass over all tokens")
     a = ap.parse_args(argv)
-    model = Model(Config())
+    model = Model(Config(cache=a.cache))
     prompts = torch.randint(0, model.cfg.vocab, (a.requests, a.prompt), generator=torch.Generator().manual_seed(1)).cuda()
     generate(model, prompts, min(a.steps, 3))  # warm-up
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
