@@ -18,18 +18,25 @@
 // the heads of the same tokens go to neighbouring CTAs, so that rows which lie side
 // by side are read at one time (23.1 -> 21.5 us for four prompts of 12 400 tokens
 // together, 8 heads of 128, bf16).  The maximum is taken of the bits, two bf16 at a
-// time, and values that are not finite are looked for only where it shows one.
+// time, and values that are not finite are looked for only where it shows one.  With many tokens a team has
+// up to a page of them, far apart and with no divisor in common with the page size: so each finds about one
+// of a prompt's runs, and decodes, which are neighbours in the call, go to different teams.  (A team with
+// neighbouring tokens took 100 decodes one after the other: with them and 100 prompts of up to 1000 tokens,
+// 8 heads of 128, pages of 64, bf16, 55.9 -> 18.1 us; a run's length, which is then not among the slots
+// already read, costs prompts alone 18.1 -> 19.4 us.  Reading a likely whole page's rows before its length
+// is known: 22.1 us.)
 //
-// Measured on a GB300: those four prompts, pages of 64: 18.1 us, 4.2 TB/s, 0.62 of
+// Measured on a GB300: those four prompts, pages of 64: 19.4 us, 3.9 TB/s, 0.58 of
 // the copy bandwidth: instructions bound it (19 for an element at first: 24.9 us),
 // and a team's life is a chain of slots, rows and codes with nothing of the next run
 // on its way; 64 tokens: 2.9 us, launch latency; 37 requests, decodes and two prompts
-// of up to 333 tokens, f32, 2 heads of 256: 8.5 us.
+// of up to 333 tokens, f32, 2 heads of 256: 6.3 us.
 //
 // Load.  A warp takes a token: 28 us for 33 000 tokens of 8 heads of 128 to bf16, 0.9
 // of the copy bandwidth.
 #include <cuda_runtime.h>
 
+#include <numeric>
 #include <type_traits>
 
 #include "fp8_common.cuh"
@@ -159,47 +166,49 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 4 : W > 2 ? 8 : 
   const uint32_t group = c.rows_div.div(blockIdx.x), of = blockIdx.x - group * c.rows_div.d;
   const uint32_t unit = group * kTeams + team, which = of & 1, head = of >> 1;
   if (unit >= c.windows) return;  // the whole team
-  const int n = static_cast<int>(p.n_tokens), t0 = unit * c.window, t1 = min(n, t0 + static_cast<int>(c.window));
+  const int n = static_cast<int>(p.n_tokens);
   const T *src = static_cast<const T *>(which ? c.a.v : c.a.k) + head * p.head_dim;
   const int64_t src_stride = which ? p.v_stride : p.k_stride;
   uint8_t *cache = static_cast<uint8_t *>(which ? c.a.v_cache : c.a.k_cache) + head * p.cache_head_stride;
   float *scales = (which ? c.a.v_scale : c.a.k_scale) + head;
   const int32_t *slots = c.a.slot_map;
 
-  for (int base = t0; base < t1; base += 32) {
-    // the tokens at which runs begin; slots of this and the next 32 tokens at once: a run's length is in them, or its end is not
-    const int i = base + lane;
-    const int slot_i = i < n ? slots[i] : -1, slot_on = i + 32 < n ? slots[i + 32] : -1;
-    bool begins = false;
-    if (i < t1) {
-      const int slot = slot_i, before = i ? slots[i - 1] : -1;
-      if (slot >= 0) {
-        const uint32_t page = c.page_div.div(slot);
-        const bool same = before >= 0 && c.page_div.div(before) == page;
-        begins = !(same && before == slot - 1);
-        if (page >= p.n_pages) {
-          if (begins) report(GDN_DEVICE_BAD_PAGE);
-          begins = false;
-        } else if (begins && same) {  // a page's tokens out of order
-          report(GDN_DEVICE_BAD_REQUEST);
-          begins = false;
-        }
+  for (uint32_t base = 0; base < c.window; base += 32) {
+    // The team's tokens lie `windows` apart, so that neighbouring decodes, a run each, go to different teams; the runs that begin
+    // at them are the team's.
+    const int64_t mine_at = unit + static_cast<int64_t>(base + lane) * c.windows;
+    const bool have = base + lane < c.window && mine_at < n;
+    const int i = have ? static_cast<int>(mine_at) : 0;
+    const int slot_i = have ? slots[i] : -1, before = have && i ? slots[i - 1] : -1, next = have && i + 1 < n ? slots[i + 1] : -1;
+    bool begins = false, more = false;
+    if (slot_i >= 0) {
+      const uint32_t page = c.page_div.div(slot_i);
+      const bool same = before >= 0 && c.page_div.div(before) == page;
+      begins = !(same && before == slot_i - 1);
+      more = next - 1 == slot_i && c.page_div.div(next) == page;
+      if (page >= p.n_pages) {
+        if (begins) report(GDN_DEVICE_BAD_PAGE);
+        begins = false;
+      } else if (begins && same) {  // a page's tokens out of order
+        report(GDN_DEVICE_BAD_REQUEST);
+        begins = false;
       }
     }
+    const unsigned longer = __ballot_sync(kFull, more);
     for (unsigned left = __ballot_sync(kFull, begins); left; left &= left - 1) {
-      const int from = __ffs(left) - 1, first = base + from;
+      const int from = __ffs(left) - 1, first = __shfl_sync(kFull, i, from);
       const int slot = __shfl_sync(kFull, slot_i, from);
       const uint32_t page = c.page_div.div(slot);
       const int place = slot - static_cast<int>(page * p.page_size), most = static_cast<int>(p.page_size) - place;
       // tokens of the run: up to the first that does not follow
-      const unsigned ends = __ballot_sync(kFull, lane >= from && (slot_i != slot + lane - from || lane - from >= most));
-      const unsigned ends_on = __ballot_sync(kFull, slot_on != slot + lane + 32 - from || lane + 32 - from >= most);
-      int len = ends ? __ffs(ends) - 1 - from : ends_on ? __ffs(ends_on) + 31 - from : 64 - from;
-      for (bool go = !ends && !ends_on; go;) {
-        const int j = len + lane;
-        const unsigned e = __ballot_sync(kFull, j >= most || first + j >= n || slots[first + j] != slot + j);
-        len += e ? __ffs(e) - 1 : 32;
-        go = e == 0;
+      int len = 1;
+      for (bool go = longer >> from & 1; go;) {
+        const int a = len + lane, b = a + 32;
+        const bool on_a = a < most && a < n - first && slots[first + a] == slot + a;
+        const bool on_b = b < most && b < n - first && slots[first + b] == slot + b;
+        const unsigned e_a = __ballot_sync(kFull, !on_a), e_b = __ballot_sync(kFull, !on_b);
+        len += e_a ? __ffs(e_a) - 1 : e_b ? __ffs(e_b) + 31 : 64;
+        go = !e_a && !e_b;
       }
       float *scale_at = scales + static_cast<uint64_t>(page) * p.n_kv_heads;
       const float old = place ? *scale_at : 0.0f;
@@ -355,6 +364,9 @@ cudaError_t launch_store(StoreCall c, cudaStream_t stream) {
   if (c.window > p.page_size) c.window = p.page_size;
   while (c.window < p.n_tokens && units / c.window > 1u << 30) c.window *= 2;  // CTAs are counted in 31 bits
   c.windows = (p.n_tokens + c.window - 1) / c.window;
+  // a prompt's runs begin a page apart: with no divisor in common the teams get one each
+  if (c.window > 1)
+    while (std::gcd(c.windows, p.page_size) != 1) ++c.windows;
   c.rows_div = FastDiv(2 * p.n_kv_heads);
   c.at_once = 32 * W / c.row_div.d;
   return launch_in_order(gdn_kv_store_kernel<T, W>, dim3((c.windows + kTeams - 1) / kTeams * 2 * p.n_kv_heads), W > 4 ? 32 * W : 128, 0, stream, c);

@@ -243,6 +243,19 @@ def test_store_of_many_requests(torch, dtype, page):  # noqa: F811
         same(torch, now[~stored], torch.where(earlier[:, :, None], grown, first[0][i][:, 0])[~stored])
 
 
+@pytest.mark.parametrize("dtype,dim,n_kv,page", [("bf16", 128, 8, 64), ("bf16", 64, 8, 100), ("f32", 256, 8, 64)])
+def test_store_of_prompts_between_decodes(torch, dtype, dim, n_kv, page):  # noqa: F811
+    """Thousands of tokens, so that a team looks at more than 32 of them: prompts that begin and end inside pages, hundreds of
+    decodes in a row, idle tokens among them."""
+    r = np.random.RandomState(dim + page)
+    order, used, slots = r.permutation(500), 0, []
+    for n in [1] * 150 + [2500, 1, 1700, 2 * page] + [1] * 120 + [1111] + [1, 5] * 20:
+        a = int(r.randint(0, page))
+        slots += [int(order[used + (a + j) // page]) * page + (a + j) % page for j in range(n)] + [-1] * int(r.randint(0, 2))
+        used += (a + n - 1) // page + 1
+    Store(torch, dtype, slots, n_pages=500, page=page, dim=dim, n_kv=n_kv).check()
+
+
 def test_hybrid_example_over_an_fp8_cache(torch, capsys):  # noqa: F811
     """The example's decode steps (captured and replayed) end where one pass over all tokens does.  Both hold the same
     values in 8 bits but for those that f32's roundings, which differ between the two, bring over a border of the codes,
