@@ -638,8 +638,10 @@ gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const v
  * workspace rules (gdn_attn_fp8_workspace_size) and reports.  Codes are exact
  * in the products; a page's scale multiplies the scores (k) and the sums (v) in
  * f32.  q is exact in bf16 (down to 2^-31 of its row's largest element; f32: good
- * to 2^-22), a probability good to 2^-11 in bf16, where the result's rounding takes
- * 2^-8, and to 2^-22 in f32.  Values above 2^95 may give infinities.  A scale that is
+ * to 2^-22).  A probability times its value's scale is good to 2^-11 of itself in
+ * bf16, where the result's rounding takes 2^-8, and to 2^-22 in f32, or to 2^-31
+ * (f32: 2^-35) of the row's largest such product, whichever is more; probabilities
+ * below 2^-137 of the largest are zero.  Values above 2^95 may give infinities.  A scale that is
  * NaN reaches the rows that see a key of its page.  Pages of whole groups of 8 (for
  * heads of 64: 16) tokens go by tensor copies and are the fastest; any page_size is
  * taken.  A wait inside the kernel that runs out, which no call is known to cause,

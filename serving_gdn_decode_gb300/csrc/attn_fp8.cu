@@ -13,9 +13,11 @@
 // two), and the products are those of f16 matrix instructions with f32 sums.  q goes
 // in with each row scaled by a power of two to below 2^14 (exact for bf16 down to
 // 2^-31 of the row's largest; f32 as two halves), the probabilities relative to a
-// maximum such that they lie below 2^15 and lose nothing above 2^-35 of the largest.
-// f16 rounds a probability by 2^-11 of itself at most, to either side, an eighth of
-// what the result's rounding to bf16 takes; for f32 it is two halves.  The contraction
+// maximum such that they lie below 2^15.  f16 rounds one by 2^-11 of itself at most,
+// to either side, an eighth of what the result's rounding to bf16 takes; for f32 it is
+// two halves, 2^-22.  (Two halves for bf16 too, good to 2^-22, would take 59.6 us in place
+// of 52.2 for 64 requests, 182 in place of 168 for 256 and 113 in place of 67 for windows.)
+// Either way it loses up to 2^-25 where it is small, 2^-36 of the largest; see Scales.  The contraction
 // of a product may go in any order, so the order is that of the memory: a lane takes
 // 16 neighbouring bytes of a key for four steps of Q K^T, and 16 neighbouring elements
 // of four values for eight steps of P V, whose result then has 16 neighbouring elements
@@ -25,7 +27,14 @@
 // Scales.  A key's scale multiplies its scores.  A tile's values are summed as
 // codes, times their page's scale over the largest of the tile, and the sums are
 // added to the running ones, in f32, times that largest.  Where scales of a tile
-// are further apart than 2^8 its pages take products of their own.
+// are further apart than 2^8 its pages take products of their own.  What f16 cuts off
+// a small probability would show where its value's scale is far above that of the key
+// with the maximum: once a tile's largest scale is more than 2^5 (f32: 2) times the
+// smallest before it, each column of its probabilities is first lifted to the top of
+// f16's range by a power of two.  So a probability times its scale is good to 2^-11 (2^-22)
+// of itself or 2^-31 (2^-35) of the row's largest such product.  (64 requests whose value
+// scales differ by up to 2^6: 56.5 us in place of 51.4; windows: 72 in place of 62.7.  A test
+// of each column's probabilities in place of the scales: 66 for the windows whatever they hold.)
 //
 // Feeding.  Some warps of a CTA do nothing but fill a ring of tiles, by tensor copies
 // of boxes of a page's rows, across items; the others take its tiles in turn.  So these
@@ -184,6 +193,8 @@ template <typename T, int D, int NT, int KT, bool Q_SMEM>
 struct Warp8 {
   using S = Shape8<D, KT>;
   static constexpr int kHalves = sizeof(T) == 4 ? 2 : 1;  // f16 halves of q and of the probabilities
+  // How far a tile's largest value scale may be above the smallest so far before its probabilities are lifted.
+  static constexpr float kRaised = sizeof(T) == 4 ? 2.0f : 32.0f;
   static constexpr int kFragments = S::kSteps * NT * kHalves;  // of q
   static constexpr int kQBytes = Q_SMEM ? kFragments * 256 : 0;
   unsigned q[Q_SMEM ? 1 : kFragments][2];
@@ -331,6 +342,26 @@ struct Warp8 {
         }
     }
   };
+
+  // Brings a score tile's probabilities near the top of f16's range, by a power of two of the column.  `of` becomes what
+  // takes the sums of products back, times `by`.
+  static __device__ __forceinline__ void lift(float (&s)[NT][4], float by, float (&of)[NT][2]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float t = fmaxf(s[nt][j], s[nt][j + 2]);
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+        // to [2^14, 2^15)
+        const int up = t > 0.0f ? min(max(14 + 127 - (__float_as_int(t) >> 23), 0), 120) : 0;
+        const float f = __int_as_float((127 + up) << 23);
+        of[nt][j] = by * __int_as_float((127 - up) << 23);
+        s[nt][j] *= f;
+        s[nt][j + 2] *= f;
+      }
+  }
 
   // This lane's part of 16 values: kBytes neighbouring elements of four keys.
   struct V {
@@ -789,6 +820,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     const int n_tiles = (k1 - job.k0 + kTile - 1) / kTile;
     int key0 = job.k0 + ahead * kTile;
     bool bad_page = false;
+    unsigned least_scale = 0x7f800000u;  // of the job's values so far (of this key group): an f32's bits
     // (every key group puts the same fragments)
     w.q_at = ring.fragments + (slot * RW + rg) * W::kQBytes + lane * 8;
     if (ahead < n_tiles) w.template load_q<P::q_row>(ring.q + slot * P::q_bytes, lane, row0, c.scale_log2);
@@ -907,11 +939,14 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
               for (int j = 0; j < 2; ++j) s[kt][nt][2 * h + j] = use ? s[kt][nt][2 * h + j] * by : 0.0f;
           }
       }
-      typename W::P p[KT];
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) p[kt].take(s[kt]);
+      // Whether what f16 cuts off small probabilities may show in this tile's values.
+      least_scale = most > 0x7f800000u ? 0u : min(least_scale, least);  // (0: none that could be compared with)
+      const bool raised = ref > __uint_as_float(least_scale) * W::kRaised;
       // output
-      if (!edge && !apart) {
+      if (!edge && !apart && !raised) {
+        typename W::P p[KT];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) p[kt].take(s[kt]);
 #pragma unroll
         for (int x = 0; x < S::kParts; ++x) {
           typename W::V v[KT];
@@ -939,6 +974,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
       // A key that a token does not see must not reach its row even as 0 * v (v may be stale or NaN).  Keys that no
       // token of the warp sees are cut out of V; if tokens see different keys of the tile and one of those is NaN, or the
       // scales are apart, each token's columns take products of their own, in the latter case 8 keys (or a page's) a time.
+      // Where the scales are apart or raised, the probabilities of such a product are lifted.
       const bool folded = !apart;
       if (folded && last0 != last1) {
         bool nan = false;
@@ -958,7 +994,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
 #pragma unroll 1
         while (from < end) {
           int to = min(end, (from / kSub + 1) * kSub);
-          float by = ref;
+          const int kt0 = from / kSub;
           if (!folded) {
             if constexpr (P::BOXED) {
               to = min(to, (from / 8 + 1) * 8);
@@ -966,11 +1002,26 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
               const int key = key0 + from;
               to = min(to, from + static_cast<int>(c.page_size) - (key - static_cast<int>(c.page_div.div(key) * c.page_size)));
             }
-            by = load_f32(scales + (P::groups + (P::BOXED ? from / 8 : from)) * 4);
           }
-          const int kt0 = from / kSub;
-          typename W::P pk = p[0];
-          if (KT > 1 && kt0 > 0) pk = p[KT - 1];
+          float ps[NT][4], of[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            of[nt][0] = of[nt][1] = ref;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ps[nt][j] = KT > 1 && kt0 > 0 ? s[KT - 1][nt][j] : s[0][nt][j];
+          }
+          if (!folded || raised) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int key = kt0 * kSub + key_of<D>(lane / 4) + (j >> 1) * 8;
+                if (key < from || key >= to) ps[nt][j] = 0.0f;
+              }
+            W::lift(ps, folded ? ref : load_f32(scales + (P::groups + (P::BOXED ? from / 8 : from)) * 4), of);
+          }
+          typename W::P pk;
+          pk.take(ps);
 #pragma unroll
           for (int x = 0; x < S::kParts; ++x) {
             typename W::V v;
@@ -986,7 +1037,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
                 W::weigh(y, a, pk, nt, true);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (!apart || last[nt][j & 1] == sees) acc[x * (S::kBytes / 2) + md][nt][j] += by * y[j];
+                  if (!apart || last[nt][j & 1] == sees) acc[x * (S::kBytes / 2) + md][nt][j] += of[nt][j & 1] * y[j];
               }
             }
           }
