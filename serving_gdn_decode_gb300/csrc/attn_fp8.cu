@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float by = most ? vs[kt][h] / ref : 0.0f;  // a key that no row sees has the probability 0
-            const bool use = most && by <= 1.0f;
+            const bool use = most && by >= 0.0f && by <= 1.0f;  // (what no row sees may have any scale)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
