@@ -646,7 +646,13 @@ gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const v
  * heads of 64: 16) tokens go by tensor copies and are the fastest; any page_size is
  * taken.  A wait inside the kernel that runs out, which no call is known to cause,
  * sets GDN_DEVICE_WAIT_TIMEOUT; the rows concerned are NaN or not written.
+ *
+ * gdn_attn_fp8_wait_clocks -- the clocks of an SM after which such a wait runs out,
+ * in calls made from now on by any thread: at most 2^31; 0: the default, 2 * 10^9,
+ * about a second.
  */
+gdn_status gdn_attn_fp8_wait_clocks(uint32_t clocks);
+
 gdn_status gdn_attn_fp8_workspace_size(const gdn_attn_params *params, size_t *bytes);
 
 gdn_status gdn_attn_paged_fp8(const void *q, const void *k_cache, const void *v_cache,

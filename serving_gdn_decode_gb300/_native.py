@@ -132,6 +132,8 @@ def lib() -> ctypes.CDLL:
             L.gdn_attn_fp8_workspace_size.restype = ctypes.c_int
             L.gdn_attn_paged_fp8.argtypes = [vp] * 9 + [ctypes.POINTER(AttnParams), vp, sz, vp]
             L.gdn_attn_paged_fp8.restype = ctypes.c_int
+            L.gdn_attn_fp8_wait_clocks.argtypes = [ctypes.c_uint32]
+            L.gdn_attn_fp8_wait_clocks.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -171,14 +173,22 @@ GDN_DEVICE_BAD_POSITION = 0x10
 
 def gdn_device_status(reset: bool = False, stream=0) -> int:
     """The library's device status word on the current device (0 = no
-    failure; GDN_DEVICE_WAIT_TIMEOUT when a chunked kernel's bounded wait ran
-    out), after all work enqueued on ``stream`` so far (the call synchronises
+    failure; GDN_DEVICE_WAIT_TIMEOUT when a bounded wait of a chunked kernel or of
+    ``gdn_attn_paged_fp8`` ran out), after all work enqueued on ``stream`` so far (the call synchronises
     that stream); cleared afterwards when ``reset``."""
     out = ctypes.c_uint32()
     st = lib().gdn_device_status(ctypes.byref(out), 1 if reset else 0, _stream_ptr(stream))
     if st != GDN_OK:
         raise GdnError(st, gdn_last_error())
     return int(out.value)
+
+
+def gdn_attn_fp8_wait_clocks(clocks: int = 0) -> None:
+    """The SM clocks after which a wait inside ``gdn_attn_paged_fp8`` runs out, in calls
+    made from now on; 0: the default, about a second."""
+    st = lib().gdn_attn_fp8_wait_clocks(clocks)
+    if st != GDN_OK:
+        raise GdnError(st, gdn_last_error())
 
 
 def _stream_ptr(stream) -> int:

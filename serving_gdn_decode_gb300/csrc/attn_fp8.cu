@@ -58,6 +58,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <numeric>
@@ -131,17 +132,42 @@ __device__ __forceinline__ bool elected() {
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
 }
-// Whether the phase ended within about a second of clock.
-__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase) {
-  long long t0 = 0;
-  for (int i = 0;; ++i) {
-    unsigned done;
+constexpr unsigned kWaitClocks = 2000000000;  // about a second
+constexpr unsigned kSleepClocks = 1 << 22;    // shorter limits are waited for awake: a warp may sleep for a good part of this
+
+// Whether the phase has ended, for the whole warp alike; SLEEP: or does within a time that the hardware sets.
+template <bool SLEEP>
+__device__ __forceinline__ bool mbar_ended(unsigned bar, unsigned phase) {
+  unsigned done;
+  if constexpr (SLEEP)
     asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(done) : "r"(bar), "r"(phase) : "memory");
-    if (done) return true;
-    if (i == 0) t0 = clock64();
-    else if (clock64() - t0 > 2000000000LL) return false;
-  }
+  else
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+  return __all_sync(kFull, done != 0u);
+}
+// Whether it ends within `clocks` from now, and before *failed, for the whole warp alike; looked at once more after that.
+__device__ __forceinline__ bool mbar_wait_on(unsigned bar, unsigned phase, unsigned clocks, const volatile int *failed) {
+  const unsigned t0 = static_cast<unsigned>(clock());
+  bool done, late;
+  do {
+    late = __any_sync(kFull, static_cast<unsigned>(clock()) - t0 > clocks || (failed && *failed));
+    done = clocks > kSleepClocks ? mbar_ended<true>(bar, phase) : mbar_ended<false>(bar, phase);
+  } while (!done && !late);
+  return done;
+}
+__device__ __noinline__ bool mbar_wait_on_call(unsigned bar, unsigned phase, unsigned clocks, const volatile int *failed) {
+  return mbar_wait_on(bar, phase, clocks, failed);
+}
+// CALL: the wait proper is a function of its own.  Shapes of two row tiles, whose loops are long, gain by it (32 requests up to
+// 4096 keys, bf16, 16 rows per key head of 64 / 128 / 256: 35.6 / 48.8 / 58.7 us, else 37.0 / 51.4 / 63.1), those of one lose
+// (8 rows: 28.8 / 35.3 / 40.1, else 27.7 / 35.3 / 39.2).
+template <bool CALL>
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase, unsigned clocks, const volatile int *failed) {
+  if (mbar_ended<false>(bar, phase)) return true;
+  if constexpr (CALL) return mbar_wait_on_call(bar, phase, clocks, failed);
+  else return mbar_wait_on(bar, phase, clocks, failed);
 }
 
 // Arrives, and expects `bytes` of copies that report to the barrier themselves.
@@ -450,7 +476,17 @@ struct Ring {
   unsigned stages, scales, q, fragments, missing;
   unsigned full, empty, job_full, job_empty, turn;  // of barriers: of a stage, of a job's slot, of a key group's turn to join
   Job *jobs;
+  volatile int *failed;  // a wait of a warp ran out
 };
+
+// A warp whose wait ran out tells the others, which then stop at the next wait that they would have to wait at.
+__device__ __forceinline__ void give_up(const Ring &ring) {
+  if ((threadIdx.x & 31) == 0) {
+    *ring.failed = 1;
+    report(GDN_DEVICE_WAIT_TIMEOUT);
+  }
+  __syncwarp();
+}
 
 // A feeding warp: puts every FEED-th tile of the share's items into the ring, and the last one the items themselves.
 // (One alone takes 600 to 1000 clocks for a tile, all latency: waits, exchanges of lanes, 60 to 80 to issue a tensor copy.)
@@ -466,23 +502,32 @@ struct Feed {
   int stage, slot = 0;
   int skip;  // tiles before this warp's next one, from the item's first
   unsigned phase = 1, job_phase = 1;
-  bool filled = false;  // every stage has been
+  bool filled = false, slots_filled = false;  // every stage, every slot has been
 
   __device__ __forceinline__ Feed(const Call &c_, const Ring &r) : c(c_), ring(r), lane(threadIdx.x & 31), id((threadIdx.x >> 5) - P::WARPS), stage(id), skip(id) {}
 
-  // Copies have to land before the CTA ends: where every wait ended well, the other warps have seen to it.
-  __device__ __forceinline__ bool give_up() {
-    report(GDN_DEVICE_WAIT_TIMEOUT);
-    for (int x = id; x < P::STAGES; x += P::FEED)
-      if (x < stage || filled) mbar_wait(ring.full + x * 8, x < stage ? phase ^ 1 : phase);
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  __device__ __forceinline__ bool wait(unsigned bar, unsigned of) {
+    if (mbar_wait<(P::NT > 1)>(bar, of, c.wait_clocks, ring.failed)) return true;
+    give_up(ring);
+    drain();
     return false;
+  }
+  // This warp's copies have to land before the CTA ends, whatever has become of the warps that take them.
+  __device__ __forceinline__ void drain() {
+#pragma unroll 1
+    for (int x = id; x < P::STAGES; x += P::FEED)
+      if (x < stage || filled) mbar_wait<(P::NT > 1)>(ring.full + x * 8, x < stage ? phase ^ 1 : phase, kWaitClocks, nullptr);
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    if (id == P::FEED - 1)
+#pragma unroll 1
+      for (int x = 0; x < P::slots; ++x)
+        if (x < slot || slots_filled) mbar_wait<(P::NT > 1)>(ring.job_full + x * 8, x < slot ? job_phase ^ 1 : job_phase, kWaitClocks, nullptr);
   }
   // The item at unit u as a job, and its rows of q: row n is token n / group, query head n % group of the key head; zeros
   // for those that are not.
   __device__ __forceinline__ bool put_job(const Share &sh, const Part &f, int head, long long u) {
     if (id != P::FEED - 1) return true;  // (the other one has the first tile meanwhile)
-    if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) return give_up();
+    if (!wait(ring.job_empty + slot * 8, job_phase)) return false;
     const int block = f.item - head * f.r.blocks, rows = f.r.tokens * static_cast<int>(c.group);
     if (lane == 0) {
       Job &j = ring.jobs[slot];
@@ -530,23 +575,21 @@ struct Feed {
   // After the last item.
   __device__ __forceinline__ void put_end() {
     if (id == P::FEED - 1) {
-      if (!mbar_wait(ring.job_empty + slot * 8, job_phase)) {
-        give_up();
-        return;
-      }
+      if (!wait(ring.job_empty + slot * 8, job_phase)) return;
       if (lane == 0) {
         ring.jobs[slot].none = 1;
         mbar_arrive(ring.job_full + slot * 8);
       }
       next_job();
     }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    drain();
   }
   __device__ __forceinline__ void next_job() {
     mbar_arrive_after_copies(ring.job_full + slot * 8);
     if (++slot == P::slots) {
       slot = 0;
       job_phase ^= 1;
+      slots_filled = true;
     }
   }
   __device__ __forceinline__ void next_stage() {
@@ -625,10 +668,7 @@ __device__ __forceinline__ void feed_boxes(const Call &c, const CUtensorMap *k_m
           pg[i] = __shfl_sync(kFull, page, x + i);
           row[i] = __shfl_sync(kFull, at, x + i);
         }
-        if (!mbar_wait(ring.empty + d.stage * 8, d.phase)) {
-          d.give_up();
-          return;
-        }
+        if (!d.wait(ring.empty + d.stage * 8, d.phase)) return;
         if (lane == 0) mbar_expect(full, __popc(valid & of_tile) * box * 2 * P::D);
         // boxes past the item's end, or of no page, are left as they are and cut out later
         if (elected()) {
@@ -702,10 +742,7 @@ __device__ __forceinline__ void feed_rows(const Call &c, const Share &sh, uint32
       const long long row_at = valid ? page * c.page_stride + head * c.head_stride + o * c.slot_stride : -1;  // -1: zeros
       const uint64_t scale_at = (valid ? static_cast<uint64_t>(page) * c.n_kv : 0) + head;
       const unsigned full = ring.full + d.stage * 8, to = ring.stages + d.stage * S::kStage;
-      if (!mbar_wait(ring.empty + d.stage * 8, d.phase)) {
-        d.give_up();
-        return;
-      }
+      if (!d.wait(ring.empty + d.stage * 8, d.phase)) return;
       if (lane < kTile) {
         const unsigned dst = ring.scales + d.stage * P::scales + lane * 4;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(c.k_scale + scale_at) : "memory");
@@ -752,12 +789,13 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   __shared__ unsigned s_missing[P::STAGES];
   __shared__ alignas(8) uint64_t s_full[P::STAGES], s_empty[P::STAGES], s_job_full[P::slots], s_job_empty[P::slots], s_turn[WARPS];
   __shared__ Job s_jobs[P::slots];
+  __shared__ int s_failed;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned start = (1024u - (smem_u32(smem) & 1023u)) & 1023u;
   float4 *join = reinterpret_cast<float4 *>(smem + start + P::STAGES * (S::kStage + P::scales));
   const Ring ring{smem_u32(smem) + start, smem_u32(smem) + start + P::STAGES * S::kStage, smem_u32(join) + P::join_bytes, smem_u32(join) + P::join_bytes + P::slots * P::q_bytes,
-                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_turn), s_jobs};
+                  smem_u32(s_missing), smem_u32(s_full), smem_u32(s_empty), smem_u32(s_job_full), smem_u32(s_job_empty), smem_u32(s_turn), s_jobs, &s_failed};
   if (tid < P::STAGES) {
     mbar_init(ring.full + tid * 8, P::BOXED ? 2 : 33);  // what the feeding warp stores, and its copies
     mbar_init(ring.empty + tid * 8, RW);
@@ -767,9 +805,13 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     mbar_init(ring.job_empty + tid * 8, WARPS);
   }
   if (tid < WARPS) mbar_init(ring.turn + tid * 8, 1);
+  if (tid == 0) s_failed = 0;
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   begin_in_order();
+  // what the join finds in the place of a part that is not put because a wait ran out: rows of NaN
+  if (!c.whole_items)
+    for (int i = tid; i < 2 * kRows; i += P::threads) c.part_ml[static_cast<size_t>(2) * blockIdx.x * kRows + i] = make_float2(0.0f, NAN);
   const Share sh = take_share<kRows, WARPS + P::FEED>(c, s_scan, s_seq, s_offset, &s_first);  // (its barriers show the initialised ones)
   if (sh.cta >= sh.ctas) return;
   if (warp >= WARPS) {
@@ -782,16 +824,14 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
   int slot = 0, stage = kg;
   int ahead = kg;  // tiles until this group's next one, from the job's first
   unsigned phase = 0, job_phase = 0, turn_phase = 0;
-  bool dead = false;  // a wait ran out: the job at hand is the last
+  // Where a wait runs out the warp ends, and with it, at the next turns that it does not give, all that its row group would put.
   auto wait = [&](unsigned bar, unsigned of) {
-    if (!dead && !mbar_wait(bar, of)) {
-      dead = true;
-      report(GDN_DEVICE_WAIT_TIMEOUT);
-    }
+    const bool ended = mbar_wait<(P::NT > 1)>(bar, of, c.wait_clocks, ring.failed);
+    if (!ended) give_up(ring);
+    return ended;
   };
   while (true) {
-    wait(ring.job_full + slot * 8, job_phase);
-    if (dead) break;
+    if (!wait(ring.job_full + slot * 8, job_phase)) return;
     const Job &job = s_jobs[slot];
     if (job.none) break;
     // the last key each of this lane's columns sees, and keys that every row of this warp does: [all0, all1)
@@ -826,7 +866,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     if (ahead < n_tiles) w.template load_q<P::q_row>(ring.q + slot * P::q_bytes, lane, row0, c.scale_log2);
 #pragma unroll 1
     for (; ahead < n_tiles; ahead += KW, key0 += kTile * KW) {
-      wait(ring.full + stage * 8, phase);
+      if (!wait(ring.full + stage * 8, phase)) return;
       const unsigned k_tile = ring.stages + stage * S::kStage, v_tile = k_tile + S::kCodes, scales = ring.scales + stage * P::scales;
       bad_page |= s_missing[stage] != 0u;
       // the tile is done with: the next of this group
@@ -1052,8 +1092,8 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
     // first (so the order goes by the sizes alone); the last one puts the results.
     const int turn = ahead;
     const unsigned turns = ring.turn + rg * KW * 8;
-    wait(turns + (KW - 1) * 8, turn_phase ^ 1);  // the join of the job before is over (else a turn of that one would pass for this one's)
-    if (turn) wait(turns + (turn - 1) * 8, turn_phase);
+    if (!wait(turns + (KW - 1) * 8, turn_phase ^ 1)) return;  // the join of the job before is over (else a turn of that one would pass for this one's)
+    if (turn && !wait(turns + (turn - 1) * 8, turn_phase)) return;
     turn_phase ^= 1;
     bad_page = __any_sync(kFull, bad_page) || (turn && s_bad[rg]);
     float4 *const sums = join + rg * (P::join_bytes / RW / 16) + lane;
@@ -1097,12 +1137,12 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
           den += __shfl_xor_sync(kFull, den, 4);
           den += __shfl_xor_sync(kFull, den, 8);
           den += __shfl_xor_sync(kFull, den, 16);
-          if (dead || bad_page) den = NAN;  // rows over a page that does not exist are NaN
+          if (bad_page) den = NAN;  // rows over a page that does not exist are NaN
           const int n = nt * 8 + (lane & 3) * 2 + j, item_row = first_row + n;
           if (item_row >= job.rows) continue;
           const int t = c.group_div.div(item_row);
           // a row that sees no key is zero; one whose visible scores are all -inf is 0 / 0
-          const bool none = before + t < 0 && !bad_page && !dead;
+          const bool none = before + t < 0 && !bad_page;
           const float by = job.slot >= 0 ? 1.0f : 1.0f / den;
           T *const o = static_cast<T *>(c.out) + static_cast<int64_t>(job.t0 + t) * c.out_stride +
                        (static_cast<int64_t>(job.head) * c.group + (item_row - t * static_cast<int>(c.group))) * D;
@@ -1145,6 +1185,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+std::atomic<unsigned> g_wait_clocks{kWaitClocks};
 
 // Whether the cache's pages go by tensor copies: they hold whole groups of 8 keys, and the strides are not too long for
 // them.  Boxes of 8 rows of 64 elements are 512 bytes: the copies' instructions would take longer than asynchronous copies
@@ -1215,6 +1257,7 @@ cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream) {
   Call c = call_of(p, a.q, a.k_cache, a.v_cache, a.block_table, a.kv_lens, a.token_start, a.output);
   c.k_scale = a.k_scale;
   c.v_scale = a.v_scale;
+  c.wait_clocks = g_wait_clocks.load(std::memory_order_relaxed);
   c.q_wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && p.q_stride % (p.dtype == GDN_DTYPE_BF16 ? 8 : 4) == 0;
   return dispatch(p, takes_boxes(p), [&](auto pick) {
     using P = decltype(pick);
@@ -1241,6 +1284,8 @@ cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream) {
     return launch_join<T, P::D, P::rows>(c, P::ctas, static_cast<uint64_t>(p.n_seqs) * p.n_kv_heads * 4 < P::ctas, stream);
   });
 }
+
+void attn_fp8_wait_clocks(uint32_t clocks) { g_wait_clocks.store(clocks ? clocks : kWaitClocks, std::memory_order_relaxed); }
 
 cudaError_t attn_fp8_status_word(unsigned int **word) { return paged_status_word(word); }
 

@@ -73,6 +73,7 @@ struct Call {
   // of an 8-bit cache's call:
   bool q_wide;       // rows of q are aligned to 16 bytes
   uint32_t box;      // rows of a box of tensor copies
+  uint32_t wait_clocks;  // after which a wait runs out
 };
 
 // A request's share of the work.

@@ -482,6 +482,13 @@ gdn_status gdn_attn_fp8_workspace_size(const gdn_attn_params *params, size_t *by
   return GDN_OK;
 }
 
+gdn_status gdn_attn_fp8_wait_clocks(uint32_t clocks) {
+  gdn::g_last_error[0] = '\0';
+  if (clocks > 1u << 31) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn: clocks must be at most 2^31");
+  gdn::attn_fp8_wait_clocks(clocks);
+  return GDN_OK;
+}
+
 gdn_status gdn_attn_paged_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                               const float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
                               const int32_t *token_start, void *output, const gdn_attn_params *params, void *workspace,

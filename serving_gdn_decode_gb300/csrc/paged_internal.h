@@ -76,6 +76,7 @@ struct AttnFp8Args {
 };
 size_t attn_fp8_workspace_bytes(const gdn_attn_params &p);
 cudaError_t launch_attn_paged_fp8(const AttnFp8Args &a, cudaStream_t stream);
+void attn_fp8_wait_clocks(uint32_t clocks);  // 0: the default
 
 // The status words of the files' kernels on the current device (read_device_status).
 cudaError_t kv_plan_status_word(unsigned int **word);
