@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 4 : W > 2 ? 8 : 
       // the page's earlier tokens, on the new scale; those of a scale that is none (negative, infinite, NaN) are NaN
       if (place && scale != old) {
         const float by = old >= 0.0f && old <= 3.402823466e38f ? old * inv : __int_as_float(0x7fffffff);
-        const int row16 = p.head_dim / 16, all = place * row16;
-        for (int x = me; x < all; x += 32 * W) {
-          uint4 *q = reinterpret_cast<uint4 *>(rows + x / row16 * p.cache_slot_stride + x % row16 * 16);
+        const int row16 = p.head_dim / 16, rows_at_once = 32 * W / row16, first_row = me / row16;
+        for (int r = first_row < rows_at_once ? first_row : place; r < place; r += rows_at_once) {
+          uint4 *q = reinterpret_cast<uint4 *>(rows + r * p.cache_slot_stride + me % row16 * 16);
           uint4 y = *q;
           unsigned *w = &y.x;
 #pragma unroll
