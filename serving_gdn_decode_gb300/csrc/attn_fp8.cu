@@ -245,6 +245,7 @@ struct Warp8 {
     return b;
   }
   float by[NT][2];  // what takes the column's sums of codes to scores in the log2 domain
+  bool wide;  // sums of codes times `by` may pass f32's range: a small key scale goes first
   unsigned k_at, v_at[2];  // this lane's offsets: of row g = lane / 4 of K; of rows g = 2 (lane % 4), and one more, of V
 
   __device__ __forceinline__ explicit Warp8(int lane) {
@@ -259,6 +260,7 @@ struct Warp8 {
   // rows: q's rows of the block in shared memory, ROW bytes apart; this warp's begin at row0
   template <int ROW>
   __device__ __forceinline__ void load_q(unsigned rows, int lane, int row0, float scale_log2) {
+    wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const unsigned p = rows + (row0 + nt * 8 + lane / 4) * ROW;
@@ -285,6 +287,7 @@ struct Warp8 {
       const float f = __int_as_float((up + 127) << 23), back = __int_as_float((127 - up) << 23) * scale_log2;
 #pragma unroll
       for (int j = 0; j < 2; ++j) by[nt][j] = __shfl_sync(kFull, back, ((lane & 3) * 2 + j) * 4);
+      wide |= __any_sync(kFull, fabsf(back) > 0x1p90f) != 0;  // the sums are below 2^31
 #pragma unroll
       for (int ks = 0; ks < S::kSteps; ++ks) {
         unsigned hi[2], lo[2];
@@ -893,7 +896,14 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int from = kt * kSub + h * 8, key = from + (P::BOXED ? 0 : key_of<D>(lane / 4)), at = P::BOXED ? kt * 2 + h : key;
-          const float ks = load_f32(scales + at * 4);
+          float ks = load_f32(scales + at * 4);
+          if (w.wide && fabsf(ks) < 1.0f) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) s[kt][nt][2 * h + j] *= ks;
+            ks = 1.0f;
+          }
           vs[kt][h] = load_f32(scales + (P::groups + at) * 4);
           if (!edge || (key + (P::BOXED ? 7 : 0) >= seen0 && key < seen1)) {
             most = max(most, __float_as_uint(vs[kt][h]));

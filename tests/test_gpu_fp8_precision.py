@@ -101,3 +101,21 @@ def test_attn_tails_of_equal_probabilities(torch, dtype, nats):  # noqa: F811
     c.cache[1][:, :, 0] = 0.0
     upload(c, torch)
     assert rel(c.run(torch), c.reference(torch)) <= TOL[dtype] + bits * SCORE + 2.0 ** (bits - 36)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group,page", [(64, 4, 16), (64, 12, 24), (128, 4, 16), (128, 12, 16), (128, 30, 32), (256, 2, 24), (256, 12, 16)])
+def test_attn_large_queries_of_small_keys(torch, dtype, dim, group, page):  # noqa: F811
+    """Queries near the largest values against key scales near the smallest: neither is out of range, nor are the scores.  One
+    head's queries stay small, so that its scores are about zero."""
+    c = Case(torch, dtype, [100, 64, 33], wins=[3, 1, 1], group=group, dim=dim, page=page, spread=1)
+    c.q = (c.q.double() * 2.0 ** 121).to(c.q.dtype)
+    c.q[:, 1] = (c.q[:, 1].double() * 2.0 ** -150).to(c.q.dtype)
+    c.scale[0] = (c.scale[0].double() * 2.0 ** -121).float()
+    assert bool(c.q.isfinite().all()) and bool((c.scale[0] != 0).all())
+    upload(c, torch)
+    c.check(torch, dtype)
+    c.q = (c.q.double() * 2.0 ** -200).to(c.q.dtype)  # and small ones against large keys
+    c.scale[0] = (c.scale[0].double() * 2.0 ** 200).float()
+    upload(c, torch)
+    c.check(torch, dtype)
