@@ -643,8 +643,8 @@ gdn_status gdn_kv_load_fp8(const int32_t *slot_map, const void *k_cache, const v
  * (f32: 2^-35) of the row's largest such product, whichever is more; probabilities
  * below 2^-137 of the largest are zero.  Values above 2^95 may give infinities.  A scale that is
  * NaN reaches the rows that see a key of its page.  Pages of whole groups of 8 (for
- * heads of 64: 16) tokens go by tensor copies and are the fastest; any page_size is
- * taken.  A wait inside the kernel that runs out, which no call is known to cause,
+ * heads of 64 with few rows per key head: 16) tokens go by tensor copies and are the
+ * fastest; any page_size is taken.  A wait inside the kernel that runs out, which no call is known to cause,
  * sets GDN_DEVICE_WAIT_TIMEOUT; the rows concerned are NaN or not written.
  *
  * gdn_attn_fp8_wait_clocks -- the clocks of an SM after which such a wait runs out,

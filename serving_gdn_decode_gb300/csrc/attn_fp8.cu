@@ -1199,11 +1199,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 std::atomic<unsigned> g_wait_clocks{kWaitClocks};
 
 // Whether the cache's pages go by tensor copies: they hold whole groups of 8 keys, and the strides are not too long for
-// them.  Boxes of 8 rows of 64 elements are 512 bytes: the copies' instructions would take longer than asynchronous copies
-// row by row (pages of 24, 40 requests up to 3001 keys, 24/8 heads: 22.5 us by boxes, 19.6 by rows).
+// them.  Boxes of 8 rows of 64 elements are 512 bytes: up to 8 rows per key head the copies' instructions take longer than
+// asynchronous copies row by row; past that the shapes of 16 and 32 rows, which only boxes have, convert a code fewer times.  32
+// requests up to 4096 keys, 8 key heads of 64, pages of 24, bf16, by boxes and by rows, at 3 / 8 / 9 / 16 / 17 / 32 rows per key
+// head: 30.6 / 30.9 / 37.0 / 37.5 / 48.3 / 49.2 us and 27.2 / 27.5 / 42.7 / 42.9 / 59.4 / 75.7; f32: 31.4 / 31.7 / 42.0 / 43.3 /
+// 62.1 / 64.0 and 27.7 / 28.0 / 44.5 / 45.1 / 62.3 / 80.2; pages of 8 and 40 alike.
 bool takes_boxes(const gdn_attn_params &p) {
   const int64_t most = int64_t{1} << 40;
-  return p.page_size % (p.head_dim == 64 ? 16 : 8) == 0 && p.cache_page_stride < most && p.cache_head_stride < most && p.cache_slot_stride < most &&
+  return p.page_size % (p.head_dim == 64 && rows_of(p) <= 8 ? 16 : 8) == 0 && p.cache_page_stride < most && p.cache_head_stride < most && p.cache_slot_stride < most &&
          tensor_map_encoder() != nullptr;
 }
 
