@@ -245,7 +245,13 @@ struct Warp8 {
     return b;
   }
   float by[NT][2];  // what takes the column's sums of codes to scores in the log2 domain
-  bool wide;  // sums of codes times `by` may pass f32's range: a small key scale goes first
+  // Whether sums of codes, below 2^31, times `by` may pass f32's range: a small key scale goes first then.
+  __device__ __forceinline__ bool wide() const {
+    float t = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) t = fmaxf(t, fmaxf(fabsf(by[nt][0]), fabsf(by[nt][1])));
+    return t > 0x1p90f;
+  }
   unsigned k_at, v_at[2];  // this lane's offsets: of row g = lane / 4 of K; of rows g = 2 (lane % 4), and one more, of V
 
   __device__ __forceinline__ explicit Warp8(int lane) {
@@ -260,7 +266,6 @@ struct Warp8 {
   // rows: q's rows of the block in shared memory, ROW bytes apart; this warp's begin at row0
   template <int ROW>
   __device__ __forceinline__ void load_q(unsigned rows, int lane, int row0, float scale_log2) {
-    wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const unsigned p = rows + (row0 + nt * 8 + lane / 4) * ROW;
@@ -287,7 +292,6 @@ struct Warp8 {
       const float f = __int_as_float((up + 127) << 23), back = __int_as_float((127 - up) << 23) * scale_log2;
 #pragma unroll
       for (int j = 0; j < 2; ++j) by[nt][j] = __shfl_sync(kFull, back, ((lane & 3) * 2 + j) * 4);
-      wide |= __any_sync(kFull, fabsf(back) > 0x1p90f) != 0;  // the sums are below 2^31
 #pragma unroll
       for (int ks = 0; ks < S::kSteps; ++ks) {
         unsigned hi[2], lo[2];
@@ -897,7 +901,7 @@ __global__ void __launch_bounds__(P::threads, P::CTAS) gdn_attn_fp8_kernel(const
         for (int h = 0; h < 2; ++h) {
           const int from = kt * kSub + h * 8, key = from + (P::BOXED ? 0 : key_of<D>(lane / 4)), at = P::BOXED ? kt * 2 + h : key;
           float ks = load_f32(scales + at * 4);
-          if (w.wide && fabsf(ks) < 1.0f) {
+          if (w.wide() && fabsf(ks) < 1.0f) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1228,24 +1232,26 @@ cudaError_t cache_map(CUtensorMap *map, const void *cache, const gdn_attn_params
 // 256 per key head: 71 us with four warps of a row tile each, 60 with two of two); q's fragments are in shared memory where they
 // would not fit the registers.  32 requests up to 4096 keys, 8 key heads of 128, 12 rows: 54.6 us with six warps of 255
 // registers, 47.9 with eight of 168; 32 rows: 69.8 and 75.6; of 64, 32 rows: 74.7 with one CTA, whose two feeding warps are too
-// few, 46.2 with two.
+// few, 46.2 with two.  f32, 12 rows, heads of 128: 65.4 us with six warps of 255 registers, 73.4 with eight of 168, which spill;
+// of 64: 40.2 us with q's fragments in shared memory, 43.9 in registers.
 template <typename F>
 auto dispatch(const gdn_attn_params &p, bool boxed, F f) {
   const uint64_t rows = rows_of(p);
   auto by_dim = [&](auto t) {
     using T = decltype(t);
+    constexpr bool f32 = sizeof(T) == 4;
     if (p.head_dim == 64)
       return !boxed       ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, false>{})
              : rows <= 8  ? f(Pick8<T, 64, 1, 1, 4, 2, 2, 2, true>{})
-             : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 2, 2, true>{})
-                          : f(Pick8<T, 64, 2, 2, 4, 2, 2, 2, true, sizeof(T) == 4>{});
+             : rows <= 16 ? f(Pick8<T, 64, 2, 1, 4, 2, 2, 2, true, f32>{})
+                          : f(Pick8<T, 64, 2, 2, 4, 2, 2, 2, true, f32>{});
     if (p.head_dim == 128)
-      return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false, sizeof(T) == 4>{})
-             : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true, sizeof(T) == 4>{})
-             : rows <= 16 ? f(Pick8<T, 128, 2, 1, 4, 2, 1, 2, true, true>{})
+      return !boxed       ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, false, f32>{})
+             : rows <= 8  ? f(Pick8<T, 128, 1, 1, 4, 2, 2, 2, true, f32>{})
+             : rows <= 16 ? f(Pick8<T, 128, 2, 1, f32 ? 6 : 4, 2, f32 ? 2 : 1, f32 ? 1 : 2, true, true>{})
                           : f(Pick8<T, 128, 2, 2, 6, 2, 2, 1, true, true>{});
-    return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false, sizeof(T) == 4>{})
-           : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true, sizeof(T) == 4>{})
+    return !boxed       ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, false, f32>{})
+           : rows <= 8  ? f(Pick8<T, 256, 1, 1, 3, 1, 1, 2, true, f32>{})
            : rows <= 16 ? f(Pick8<T, 256, 2, 1, 6, 2, 1, 1, true, true>{})
                         : f(Pick8<T, 256, 2, 2, 6, 2, 1, 1, true, true>{});
   };

@@ -17,14 +17,19 @@ SOURCE = os.path.join(os.path.dirname(__file__), "..", "serving_gdn_decode_gb300
 def shapes():
     """(WARPS, RW, FEED, STAGES, slots) of the kernel's variants, f32 and bf16: Pick8's arithmetic."""
     with open(SOURCE) as f:
-        picks = re.findall(r"f\(Pick8<T, (\d+), (\d+), (\d+), (\d+), (\d+), (\d+), (\d+), (true|false)(?:, ([^>]*))?>\{\}\)", f.read())
-    assert len(picks) == 12
+        picks = [x.split(", ") for x in re.findall(r"f\(Pick8<T, ([^>]*)>\{\}\)", f.read())]
+    assert len(picks) == 12 and all(len(x) in (8, 9) for x in picks)
     out = set()
     for size in (2, 4):
-        for *numbers, boxed, q_smem in picks:
-            d, nt, rw, warps, feed, kt, ctas = map(int, numbers)
-            in_smem = {"": False, "true": True, "sizeof(T) == 4": size == 4}[q_smem]
-            rows, tile, groups = nt * rw * 8, 16 * kt, 2 * kt if boxed == "true" else 16 * kt
+        def value(text):  # a number, a truth value, or either for f32 and for bf16
+            both = re.fullmatch(r"f32 \? (\w+) : (\w+)", text)
+            if both:
+                return value(both[1] if size == 4 else both[2])
+            return int(text) if text.isdigit() else {"true": True, "false": False, "f32": size == 4}[text]
+
+        for pick in picks:
+            d, nt, rw, warps, feed, kt, ctas, boxed, in_smem = [value(x) for x in pick] + [False] * (9 - len(pick))
+            rows, tile, groups = nt * rw * 8, 16 * kt, 2 * kt if boxed else 16 * kt
             q_bytes = rows * (d * size + 16)
             slots = 4 if q_bytes <= 2400 else 3 if q_bytes <= 4800 else 2
             fragments = slots * rw * (d // 16 * nt * (2 if size == 4 else 1) * 256 if in_smem else 0)
