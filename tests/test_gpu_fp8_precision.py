@@ -119,3 +119,23 @@ def test_attn_large_queries_of_small_keys(torch, dtype, dim, group, page):  # no
     c.scale[0] = (c.scale[0].double() * 2.0 ** 200).float()
     upload(c, torch)
     c.check(torch, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group,page", [(64, 4, 16), (64, 12, 8), (64, 30, 24), (128, 4, 12), (128, 12, 16), (128, 30, 8), (256, 2, 16), (256, 30, 24)])
+@pytest.mark.parametrize("far", [0, 3, 12, 40])
+def test_attn_scales_of_any_value(torch, dtype, dim, group, page, far):  # noqa: F811
+    """Scales that are no powers of two, negative and zero, up to 2^far apart."""
+    c = Case(torch, dtype, [700, 64, 33, 130], wins=[3, 1, 2, 1], group=group, dim=dim, page=page, spread=0, seed=far)
+    g = torch.Generator().manual_seed(far + page)
+    for i in range(2):
+        s = c.scale[i]
+        by = (0.5 + torch.rand(s.shape, generator=g)) * torch.sign(torch.rand(s.shape, generator=g) - 0.3)
+        if i:
+            by = by * torch.exp2(-(far * torch.rand(s.shape, generator=g)))
+            by[torch.rand(s.shape, generator=g) < 0.05] = 0.0
+        c.scale[i] = s * by
+    upload(c, torch)
+    check(c, torch, dtype, 35)
+    check(c, torch, dtype, 35, window=100)
+    assert status() == 0
