@@ -596,12 +596,13 @@ typedef struct gdn_kv_fp8_params {
  *     the page's codes at places 0 .. a - 1, where its scale grows, become
  *             code * (old scale / scale), rounded to the nearest e4m3
  *     the run's codes become x / scale, rounded to the nearest e4m3 (ties to
- *             even; at most 448); NaN and infinities become NaN
+ *             even; at most 448); NaN and infinities become NaN.  For a page's
+ *             scale that is no power of two it is x * (1 / scale), both in f32
  * So a page's first token starts a new scale, whatever the page held, and later
  * ones can only raise it; after a rollback into a page its scale stays.  Places
  * from b on keep their codes: they mean nothing until they are stored.  An old
- * scale of 0 makes the codes before zero, one that is negative, infinite or
- * NaN makes them NaN.
+ * scale of 0 makes the codes before zero (a NaN stays NaN), one that is
+ * negative, infinite or NaN makes them NaN.
  *
  * Tokens of one page must be neighbours, slot after slot: a page that two runs
  * of a call share has unspecified contents where they are not neighbours, and

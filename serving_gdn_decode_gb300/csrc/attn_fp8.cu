@@ -33,26 +33,32 @@
 // smallest before it, each column of its probabilities is first lifted to the top of
 // f16's range by a power of two.  So a probability times its scale is good to 2^-11 (2^-22)
 // of itself or 2^-31 (2^-35) of the row's largest such product.  (64 requests whose value
-// scales differ by up to 2^6: 56.5 us in place of 51.4; windows: 72 in place of 62.7.  A test
-// of each column's probabilities in place of the scales: 66 for the windows whatever they hold.)
+// scales differ by up to 2^6: 55.0 us in place of 51.5; windows: 72 in place of 61.7.  A test
+// of each column's probabilities in place of the scales took 66 for the windows whatever they held.)
 //
 // Feeding.  Some warps of a CTA do nothing but fill a ring of tiles, by tensor copies
 // of boxes of a page's rows, across items; the others take its tiles in turn.  So these
 // have neither the copies' instructions nor their registers, hold no request (an item
 // comes to them as a job in shared memory), and more of them fit an SM: 12 warps of
 // 168 registers.  With the copies in every warp, a ring for each (8 warps of 240
-// registers): 64 requests of up to 4096 keys, 32/8 heads of 128, bf16: 68 us, now 53;
-// 256 requests, 48/8 heads: 214, now 170.  A feeding warp needs 600 to 900 clocks for a
+// registers): 64 requests of up to 4096 keys, 32/8 heads of 128, bf16: 68 us, now 51.5;
+// 256 requests, 48/8 heads: 214, now 168.  A feeding warp needs 600 to 900 clocks for a
 // tile, all latency, an SM's share of HBM one in 360: hence two in each of two CTAs.
 //
+// Waits.  Every wait on a barrier is bounded.  Where one runs out the warp ends there and
+// tells the others, nothing is put from then on that would need it, parts that the join
+// looks for are NaN, and the feeding warps end only after their copies have landed.
+//
 // Measured on a GB300, back to back over three sets of buffers, as shares of the
-// measured copy bandwidth (6767 GB/s): 256 requests as above 170 us, 0.92; 64: 53 us,
-// 0.75; one request of 400 009 keys, 32/4 heads of 128: 76 us, 0.79 (in between 0.97:
+// measured copy bandwidth (6767 GB/s): 256 requests as above 168 us, 0.93; 64: 51.5 us,
+// 0.78; one request of 400 009 keys, 32/4 heads of 128: 75.2 us, 0.81 (in between 0.97:
 // 5 us until the first tile -- lengths, pages, tile and q are dependent reads -- and 7 for
-// the join); 32 requests, windows of 1 to 4, 16/2 heads of 256: 60 us, 0.32; f32, 24
-// requests with a window of 1000 keys, 16/16 heads of 64: 19.6 us; pages of 24, 24/8
-// heads of 64: 19.6 us.  32 requests up to 4096 keys, 8 key heads of 128, by rows per key
-// head: 8: 37 us, 16: 48, 32: 71 (over a bf16 cache 56, 60, 83).
+// the join); 32 requests, windows of 1 to 4, 16/2 heads of 256: 61.7 us, 0.31; f32, 24
+// requests with a window of 1000 keys, 16/16 heads of 64: 19.8 us; pages of 24, 24/8
+// heads of 64: 20.1 us.  32 requests up to 4096 keys, 8 key heads of 128, by rows per key
+// head: 8: 35.4 us, 16: 48.8, 32: 70.7 (over a bf16 cache 55.9, 60.5, 82.7).  One request
+// of 1021 keys, 16/2 heads of 256: 11.4 us, over a bf16 cache 8.8; 4096 new tokens of
+// one request, 32/8 heads of 128: 3.68 ms, over a bf16 cache 3.45.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

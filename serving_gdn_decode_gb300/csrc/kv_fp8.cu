@@ -26,14 +26,17 @@
 // already read, costs prompts alone 18.1 -> 19.4 us.  Reading a likely whole page's rows before its length
 // is known: 22.1 us.)
 //
-// Measured on a GB300: those four prompts, pages of 64: 19.4 us, 3.9 TB/s, 0.58 of
+// Measured on a GB300: those four prompts, pages of 64: 19.3 us, 4.0 TB/s, 0.59 of
 // the copy bandwidth: instructions bound it (19 for an element at first: 24.9 us),
 // and a team's life is a chain of slots, rows and codes with nothing of the next run
-// on its way; 64 tokens: 2.9 us, launch latency; 37 requests, decodes and two prompts
-// of up to 333 tokens, f32, 2 heads of 256: 6.3 us.
+// on its way; pages of 16 and 128: 23.9 and 26.8 us; f32, pages of 16, 64 and 128: 53.6, 29.7
+// and 54.0.  37 requests, decodes and two prompts of up to 333 tokens, f32, 2 heads of 256: 6.3 us.
+// 64 decodes in pages of 16: 2.9 us, launch latency; 512 and 2048 decodes in pages of 16: 6.3 and
+// 15.3 us, of 64: 13.7 and 46.5, of 128: 26.8 and 102 (0.4 and 1.8 for the bytes): a team has the
+// warps that a whole page's rows need, of which a single token's use one row.
 //
 // Load.  A warp takes a token: 28 us for 33 000 tokens of 8 heads of 128 to bf16, 0.9
-// of the copy bandwidth.
+// of the copy bandwidth; to f32 45.8 us, 0.92.
 #include <cuda_runtime.h>
 
 #include <numeric>
