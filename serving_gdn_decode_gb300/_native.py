@@ -186,7 +186,7 @@ def gdn_device_status(reset: bool = False, stream=0) -> int:
 def gdn_attn_fp8_wait_clocks(clocks: int = 0) -> None:
     """The SM clocks after which a wait inside ``gdn_attn_paged_fp8`` runs out, in calls
     made from now on; 0: the default, about a second."""
-    st = lib().gdn_attn_fp8_wait_clocks(clocks)
+    st = lib().gdn_attn_fp8_wait_clocks(clocks if 0 <= clocks < 1 << 32 else (1 << 32) - 1)  # (ctypes would take the low bits)
     if st != GDN_OK:
         raise GdnError(st, gdn_last_error())
 

@@ -10,5 +10,7 @@ def test_wait_clocks(L):  # noqa: F811
     assert "2^31" in nat.gdn_last_error()
     for clocks in (1, 1 << 31, 0):
         assert L.gdn_attn_fp8_wait_clocks(clocks) == nat.GDN_OK and nat.gdn_last_error() == ""
-    with pytest.raises(nat.GdnError, match="2\\^31"):
-        nat.gdn_attn_fp8_wait_clocks((1 << 32) - 1)
+    for clocks in ((1 << 31) + 1, (1 << 32) - 1, 1 << 32, (1 << 32) + 5, -1):
+        with pytest.raises(nat.GdnError, match="2\\^31"):
+            nat.gdn_attn_fp8_wait_clocks(clocks)
+    nat.gdn_attn_fp8_wait_clocks()
